@@ -226,7 +226,7 @@ typedef struct {
     int32_t *block_exp;     /* int32[ceil(M/32)][ceil(N/32)] row-major, written: the exponent E
                                of each 32 x 32 tile's scale (block_scale); 4-byte aligned */
     const float *a_block_scales; /* FP32[ceil(M/br)][ceil(K/bk)] row-major (block-scaled operands) */
-    const float *b_block_scales; /* FP32[ceil(N/br)][ceil(K/bk)] row-major */
+    const float *b_block_scales; /* FP32[ceil(N/br_b)][ceil(K/bk)] row-major, per group of a grouped plan */
 } tst_epilogue_args;
 
 /* Optional plan settings.  Zero-initialise and set what you need. */
@@ -560,6 +560,118 @@ enum {
 };
 tst_status gemm_plan_set_debug(tst_plan *plan, int32_t flags, void *trace_buf, int64_t cap,
                                int64_t timeout_ns);
+
+/* ---------------------------------------------------------------- mixture of experts
+ *
+ * The calls around a grouped GEMM whose groups are the experts of a mixture:
+ *
+ *   moe_route      chooses each token's experts from the router's logits, counts each
+ *                  expert's rows (the grouped GEMM's group_rows), numbers the rows in the
+ *                  experts' order and computes the balance loss; moe_route_backward is its
+ *                  gradient
+ *   moe_dispatch   writes each token into its rows, unchanged or as e4m3 with one scale
+ *                  per 1 x 128 tile (the grouped GEMM's A and a_block_scales)
+ *   (gemm_grouped_run computes the experts' products)
+ *   moe_combine    adds each token's rows, weighted; moe_combine_backward is its gradient
+ *
+ * The gradient of moe_dispatch with respect to x is moe_combine of the rows' gradient
+ * without weights.  Each call is asynchronous and ordered on its stream, allocates nothing,
+ * and gives the same bits each time for the same inputs.  A plan is not re-entrant (its
+ * workspace is per plan): do not run one plan on two streams at once.  Outputs may not
+ * overlap inputs. */
+typedef struct tst_moe_plan tst_moe_plan;
+
+typedef struct {
+    int32_t normalize;    /* 1: the weights of a token's experts are divided by their sum */
+    float balance_coef;   /* factor of the balance loss */
+    int32_t host_only;    /* 1: no GPU (the runs then fail with TST_ERR_NO_DEVICE) */
+} tst_moe_options;
+
+typedef struct {
+    int64_t max_tokens;
+    int32_t experts, top_k;
+    int32_t normalize;
+    float balance_coef;
+    int64_t workspace_bytes;   /* device bytes owned by the plan */
+} tst_moe_plan_info;
+
+/* Plan for calls of up to max_tokens tokens, each sent to top_k of `experts` experts.
+ * Allocates the routing workspace: 8 bytes per expert and chunk of tokens.  Errors:
+ * INVALID_ARG (null plan or opts, sizes < 1, top_k > experts, max_tokens * top_k beyond
+ * int32, a NaN balance_coef), UNSUPPORTED (more than 1024 experts or 32 per token, or a GPU
+ * other than sm_103), OOM, CUDA, NO_DEVICE. */
+tst_status moe_plan_create(tst_moe_plan **plan, int64_t max_tokens, int32_t experts, int32_t top_k,
+                           const tst_moe_options *opts);
+tst_status moe_plan_get_info(const tst_moe_plan *plan, tst_moe_plan_info *info);
+/* NULL is accepted. */
+tst_status moe_plan_destroy(tst_moe_plan *plan);
+
+/* Whether the runs since the last query met a row index outside its matrix (skipped by the
+ * kernels): TST_ERR_DEVICE_CHECK, else TST_OK.  Synchronises the last run's stream. */
+tst_status moe_status_query(tst_moe_plan *plan);
+
+/* Route `tokens` (0 .. max_tokens) rows of logits, tokens x experts of dtype TST_OUT_F32 or
+ * TST_OUT_BF16, rows `ld` elements apart.  mask (NULL, or one byte per token) closes the
+ * tokens whose byte is 0; their logits are not read.  A logit of -inf closes its expert to
+ * its token.  With p = softmax(logits) per row:
+ *
+ *   expert[t][j]  the token's top_k open experts by falling logit (ties: the lower expert
+ *                 first; a NaN ranks first); -1 where fewer are open
+ *   weight[t][j]  p of that expert, divided by the sum over j when the plan normalizes;
+ *                 0 where expert is -1
+ *   row[t][j]     its row in the experts' order: the rows of expert 0 by token, then those
+ *                 of expert 1, ...; -1 where expert is -1
+ *   counts[e]     rows of expert e (group_rows of the grouped GEMM)
+ *   totals        {R, n}: rows in all, tokens with an open expert
+ *   loss          balance_coef * experts * sum_e (counts[e] / R) * (sum_t p[t][e] / n), 0
+ *                 when R is 0
+ *
+ * all DEVICE arrays (int32, FP32), contiguous.  Sums are FP32.  tokens = 0 writes counts,
+ * totals and loss only.  Errors: INVALID_ARG, ALIGNMENT (a pointer not aligned to its
+ * elements), NO_DEVICE, CUDA. */
+tst_status moe_route(tst_moe_plan *plan, int64_t tokens, const void *logits, int32_t dtype, int64_t ld,
+                     const uint8_t *mask, int32_t *expert, float *weight, int32_t *row, int32_t *counts,
+                     int32_t *totals, float *loss, void *stream);
+
+/* The logits' gradient, given moe_route's inputs and its expert, counts and totals, the
+ * gradient d_weight of the weights (NULL: none) and that of the loss (d_loss, FP32[1], NULL:
+ * none).  The counts are constants of the loss.  Closed tokens and experts get 0.  d_logits
+ * has the logits' type, rows d_ld elements apart.  Errors as moe_route. */
+tst_status moe_route_backward(tst_moe_plan *plan, int64_t tokens, const void *logits, int32_t dtype, int64_t ld,
+                              const uint8_t *mask, const int32_t *expert, const int32_t *counts,
+                              const int32_t *totals, const float *d_weight, const float *d_loss, void *d_logits,
+                              int64_t d_ld, void *stream);
+
+/* rows[row[t][j]] = x[t] for every token and choice with row >= 0.  x: tokens x hidden of
+ * x_dtype (FP32 or BF16), rows x_ld elements apart; rows: n_rows x hidden, contiguous, of
+ * x_dtype (copied) or TST_OUT_E4M3: then each 1 x 128 tile (the last may be narrower) of a
+ * row has the FP32 scale s = max |x| / 448 (max |x| taken as at least 2^-96), written to
+ * scales[n_rows][ceil(hidden / 128)], and holds x * (448 / max |x|) rounded to nearest even,
+ * saturated to +-448: A and a_block_scales of a GEMM with ab_block (1, 128).  A NaN gives
+ * its tile a NaN scale, an infinity an infinite one.  row = NULL: row t is token t (up to max_tokens
+ * * top_k tokens), to quantize rows that are in order already.  Rows that no token names
+ * stay as they were.  Errors: INVALID_ARG, UNSUPPORTED (a copy into another type),
+ * ALIGNMENT (as moe_route; e4m3: hidden not a multiple of 16 or rows not 16-byte aligned),
+ * NO_DEVICE, CUDA. */
+tst_status moe_dispatch(tst_moe_plan *plan, int64_t tokens, int64_t hidden, const void *x, int32_t x_dtype,
+                        int64_t x_ld, const int32_t *row, void *rows, int32_t rows_dtype, int64_t n_rows,
+                        float *scales, void *stream);
+
+/* out[t] = sum_j weight[t][j] * rows[row[t][j]] over the choices with row >= 0 (weight NULL:
+ * 1), summed in FP32 in the order of j; a token without rows gets 0.  rows: n_rows x hidden,
+ * contiguous; out: tokens x hidden, rows out_ld elements apart; each FP32 or BF16.  Errors as
+ * moe_route. */
+tst_status moe_combine(tst_moe_plan *plan, int64_t tokens, int64_t hidden, const void *rows, int32_t rows_dtype,
+                       int64_t n_rows, const int32_t *row, const float *weight, void *out, int32_t out_dtype,
+                       int64_t out_ld, void *stream);
+
+/* d_rows[row[t][j]] = weight[t][j] * d_out[t] and d_weight[t][j] = <d_out[t], rows[row[t][j]]>
+ * (0 where row is -1).  d_out has the type out_dtype of moe_combine's out, d_rows that of
+ * rows.  Errors as moe_route. */
+tst_status moe_combine_backward(tst_moe_plan *plan, int64_t tokens, int64_t hidden, const void *rows,
+                                int32_t rows_dtype, int64_t n_rows, const int32_t *row, const float *weight,
+                                const void *d_out, int32_t out_dtype, int64_t d_out_ld, void *d_rows,
+                                float *d_weight, void *stream);
 
 /* Size of the fixed device scratch array used by gemm_streamk_noalloc: 16 MiB,
  * held by every GPU that loads this library until the process exits. */

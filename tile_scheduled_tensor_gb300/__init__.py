@@ -154,10 +154,12 @@ def gemm_grouped_plan_create(groups: int, M: int, N: int, K: int, dtype="bf16", 
                              aux_dtype="f32", bn: int = 0, num_ctas: int = 0, host_only: bool = False,
                              num_sms: int = 0, timeout_ns: int = 0, cta_group: int = 0, stages: int = 0,
                              bk: int = 0, pdl: bool = False, l2_hint="none", tma_boxes="auto",
-                             block_scale: bool = False) -> Plan:
+                             block_scale: bool = False, ab_block=None) -> Plan:
     """Plan `groups` GEMMs sharing N and K in one persistent launch: A holds the groups'
     rows one after another (at most M in all), B one N x K matrix per group; the row
-    counts are given to gemm_grouped_run as a device int32 array."""
+    counts are given to gemm_grouped_run as a device int32 array.  ab_block as in
+    gemm_plan_create: A's scales are ceil(M / br) x ceil(K / bk), B's groups x
+    ceil(N / br_b) x ceil(K / bk)."""
     kind, group = mapping if isinstance(mapping, (tuple, list)) else (mapping, 1)
     m = _capi.tst_mapping(_enum(_MAPS, kind, "mapping"), int(group))
     opts = _capi.tst_plan_options(int(bn), int(num_ctas), 0, int(bool(host_only)), int(num_sms), int(cta_group),
@@ -168,10 +170,12 @@ def gemm_grouped_plan_create(groups: int, M: int, N: int, K: int, dtype="bf16", 
         (TST_BIAS_COL if has_bias else TST_BIAS_NONE)
     act = _enum(_ACT, activation, "activation") if activation is not None else \
         (TST_ACT_RELU if relu else TST_ACT_NONE)
+    br, ab_k, br_b = (tuple(ab_block) + (0,))[:3] if ab_block is not None else (0, 0, 0)
     epi = _capi.tst_epilogue_ex(_enum(_OUT, out_dtype, "out_dtype"), float(alpha), float(beta), int(bool(has_c)),
                                 _enum(_OUT, c_dtype, "c_dtype"), bmode, act, int(bool(use_scales)),
                                 int(bool(row_scale)), int(bool(col_scale)), int(bool(d_scale)), int(bool(amax)),
-                                int(bool(aux)), _enum(_OUT, aux_dtype, "aux_dtype"), int(bool(block_scale)))
+                                int(bool(aux)), _enum(_OUT, aux_dtype, "aux_dtype"), int(bool(block_scale)), int(br),
+                                int(ab_k), int(br_b))
     h = ctypes.c_void_p()
     _check(lib.gemm_grouped_plan_create(ctypes.byref(h), int(groups), int(M), int(N), int(K),
                                         _enum(_DTYPES, dtype, "dtype"), TST_LAYOUT_A_ROW_B_NK, m, ctypes.byref(epi),
@@ -182,12 +186,14 @@ def gemm_grouped_plan_create(groups: int, M: int, N: int, K: int, dtype="bf16", 
 
 
 def gemm_grouped_run(plan: Plan, group_rows, A, B, D, bias=None, scales=None, c=None, row_scale=None,
-                     col_scale=None, d_scale=None, amax=None, aux=None, stream=None):
+                     col_scale=None, d_scale=None, amax=None, aux=None, stream=None, a_block_scales=None,
+                     b_block_scales=None):
     """Enqueue a grouped GEMM; group_rows is a CUDA int32 tensor of the groups' row counts."""
     if hasattr(group_rows, "dtype") and str(group_rows.dtype) != "torch.int32":
         raise ValueError("group_rows must be an int32 CUDA tensor")
     args = _capi.tst_epilogue_args(_ptr(c), _ptr(bias), _ptr(scales), _ptr(row_scale), _ptr(col_scale),
-                                   _ptr(d_scale), _ptr(amax), _ptr(aux))
+                                   _ptr(d_scale), _ptr(amax), _ptr(aux), None, _ptr(a_block_scales),
+                                   _ptr(b_block_scales))
     _check(lib.gemm_grouped_run(plan._h, _ptr(group_rows), _ptr(A), _ptr(B), _ptr(D), ctypes.byref(args),
                                 _stream(stream)), "gemm_grouped_run")
 
@@ -360,3 +366,196 @@ def gemm_streamk_noalloc(M: int, N: int, K: int, A, B, C, dtype="bf16", mapping=
                                     _enum(_SCHED, schedule, "schedule"), ctypes.byref(epi), int(bn), int(num_ctas),
                                     _ptr(A), _ptr(B), _ptr(C), _ptr(bias), _ptr(scales), _ptr(device_status),
                                     _stream(stream)), "gemm_streamk_noalloc")
+
+
+# ---------------------------------------------------------------- mixture of experts
+class MoePlan:
+    """Owns a tst_moe_plan*; destroyed with the object (or explicitly via destroy())."""
+
+    def __init__(self, handle: int, max_tokens: int, experts: int, top_k: int):
+        self.handle = handle
+        self.max_tokens, self.experts, self.top_k = max_tokens, experts, top_k
+
+    def destroy(self):
+        if self.handle:
+            _check(lib.moe_plan_destroy(ctypes.c_void_p(self.handle)), "moe_plan_destroy")
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+    @property
+    def _h(self):
+        if not self.handle:
+            raise ValueError("plan was destroyed")
+        return self.handle
+
+
+def moe_plan_create(max_tokens: int, experts: int, top_k: int, normalize: bool = True, balance_coef: float = 0.01,
+                    host_only: bool = False) -> MoePlan:
+    """Plan the calls around a grouped GEMM whose groups are experts: up to max_tokens tokens per
+    call, each sent to top_k of `experts` experts.  normalize: a token's weights are divided by
+    their sum; balance_coef: factor of the balance loss."""
+    opts = _capi.tst_moe_options(int(bool(normalize)), float(balance_coef), int(bool(host_only)))
+    h = ctypes.c_void_p()
+    _check(lib.moe_plan_create(ctypes.byref(h), int(max_tokens), int(experts), int(top_k), ctypes.byref(opts)),
+           "moe_plan_create")
+    return MoePlan(h.value, int(max_tokens), int(experts), int(top_k))
+
+
+def moe_plan_get_info(plan: MoePlan):
+    info = _capi.tst_moe_plan_info()
+    _check(lib.moe_plan_get_info(plan._h, ctypes.byref(info)), "moe_plan_get_info")
+    return info
+
+
+def moe_plan_destroy(plan: MoePlan):
+    plan.destroy()
+
+
+def moe_status_query(plan: MoePlan) -> int:
+    """TST_OK, or TST_ERR_DEVICE_CHECK when a run since the last query met a row index outside its
+    matrix; synchronises the last run's stream."""
+    return lib.moe_status_query(plan._h)
+
+
+_OUT_OF = {"torch.float32": TST_OUT_F32, "torch.bfloat16": TST_OUT_BF16, "torch.float8_e4m3fn": TST_OUT_E4M3,
+           "torch.uint8": TST_OUT_E4M3}
+_out_cache = {}   # torch dtype -> tst_out_dtype, so that a call does not print a dtype's name each time
+
+
+def _out_of(x, what: str) -> int:
+    code = _out_cache.get(x.dtype)
+    if code is None:
+        code = _OUT_OF.get(str(x.dtype))
+        if code is None:
+            raise ValueError(f"{what}: {x.dtype} is not one of {sorted(_OUT_OF)}")
+        _out_cache[x.dtype] = code
+    return code
+
+
+def _matrix(x, what: str, rows=None, cols=None):
+    """(pointer, rows, columns, row stride) of a 2-D CUDA tensor whose columns are adjacent."""
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor (no host fallback)")
+    if x.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions, not {x.dim()}")
+    m, n = x.shape
+    if (rows is not None and m != rows) or (cols is not None and n != cols):
+        raise ValueError(f"{what} must be {'any' if rows is None else rows} x {'any' if cols is None else cols}, "
+                         f"not {m} x {n}")
+    sr, sc = x.stride()
+    if (sc != 1 and n > 1) or (sr < n and m > 1):
+        raise ValueError(f"{what}: a row's elements must be adjacent and its rows apart (strides {sr}, {sc})")
+    return x.data_ptr(), m, n, (sr if m > 1 else n)
+
+
+_type_names = {}   # torch dtype -> its name without "torch."
+
+
+def _array(x, what: str, dtype: str, size: int):
+    """Pointer of a contiguous CUDA tensor of `size` elements."""
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor (no host fallback)")
+    name = _type_names.get(x.dtype)
+    if name is None:
+        name = _type_names[x.dtype] = str(x.dtype)[6:]
+    if name != dtype:
+        raise ValueError(f"{what} must hold {dtype}, not {name}")
+    if x.numel() != size or not x.is_contiguous():
+        raise ValueError(f"{what} must hold {size} elements, contiguous")
+    return x.data_ptr()
+
+
+def _token_mask(mask, tokens: int):
+    if mask is None:
+        return None
+    if not mask.is_cuda or mask.numel() != tokens or mask.element_size() != 1 or not mask.is_contiguous():
+        raise ValueError(f"mask must be a contiguous CUDA tensor of {tokens} bytes (uint8 or bool)")
+    return mask.data_ptr()
+
+
+def moe_route(plan: MoePlan, logits, expert, weight, row, counts, totals, loss, mask=None, stream=None):
+    """Route each row of logits (tokens x experts, FP32 or BF16) to its top_k experts.  Written:
+    expert, row (int32) and weight (FP32), tokens x top_k; counts (int32, per expert: the grouped
+    GEMM's group_rows); totals (int32 {rows in all, tokens routed}); loss (FP32, one element).  mask:
+    one byte per token, 0 for a token that is not routed."""
+    ptr, t, _, ld = _matrix(logits, "logits", cols=plan.experts)
+    n = t * plan.top_k
+    _check(lib.moe_route(plan._h, t, ptr, _out_of(logits, "logits"), ld, _token_mask(mask, t),
+                         _array(expert, "expert", "int32", n), _array(weight, "weight", "float32", n),
+                         _array(row, "row", "int32", n), _array(counts, "counts", "int32", plan.experts),
+                         _array(totals, "totals", "int32", 2), _array(loss, "loss", "float32", 1),
+                         _stream(stream)), "moe_route")
+
+
+def moe_route_backward(plan: MoePlan, logits, expert, counts, totals, d_logits, d_weight=None, d_loss=None, mask=None,
+                       stream=None):
+    """The logits' gradient (d_logits, of the logits' type) from those of the weights (d_weight) and of
+    the loss (d_loss, one FP32 element on the device); the other arguments as moe_route had and gave
+    them."""
+    ptr, t, _, ld = _matrix(logits, "logits", cols=plan.experts)
+    dptr, _, _, d_ld = _matrix(d_logits, "d_logits", t, plan.experts)
+    if d_logits.dtype != logits.dtype:
+        raise ValueError(f"d_logits must have the logits' type, {logits.dtype}")
+    n = t * plan.top_k
+    _check(lib.moe_route_backward(plan._h, t, ptr, _out_of(logits, "logits"), ld, _token_mask(mask, t),
+                                  _array(expert, "expert", "int32", n), _array(counts, "counts", "int32", plan.experts),
+                                  _array(totals, "totals", "int32", 2),
+                                  None if d_weight is None else _array(d_weight, "d_weight", "float32", n),
+                                  None if d_loss is None else _array(d_loss, "d_loss", "float32", 1),
+                                  dptr, d_ld, _stream(stream)), "moe_route_backward")
+
+
+def _whole_rows(x, what: str, cols=None):
+    """(pointer, rows, columns) of a contiguous 2-D CUDA tensor."""
+    ptr, m, n, _ = _matrix(x, what, cols=cols)
+    if not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return ptr, m, n
+
+
+def moe_dispatch(plan: MoePlan, x, row, rows, scales=None, stream=None):
+    """rows[row[t][j]] = x[t].  rows of x's type: copied; rows of float8_e4m3fn (or uint8): quantized
+    with one FP32 scale per 128 elements, written to scales (rows x ceil(hidden / 128)).  row None:
+    row t is token t."""
+    ptr, t, h, ld = _matrix(x, "x")
+    out, n, _ = _whole_rows(rows, "rows", h)
+    code = _out_of(rows, "rows")
+    if code == TST_OUT_E4M3:
+        if scales is None:
+            raise ValueError("e4m3 rows need scales")
+        sptr = _array(scales, "scales", "float32", n * -(-h // 128))
+    else:
+        sptr = None
+    _check(lib.moe_dispatch(plan._h, t, h, ptr, _out_of(x, "x"), ld,
+                            None if row is None else _array(row, "row", "int32", t * plan.top_k), out, code, n, sptr,
+                            _stream(stream)), "moe_dispatch")
+
+
+def moe_combine(plan: MoePlan, rows, row, out, weight=None, stream=None):
+    """out[t] = sum_j weight[t][j] * rows[row[t][j]] (weight None: 1), in FP32."""
+    ptr, n, h = _whole_rows(rows, "rows")
+    optr, t, _, ld = _matrix(out, "out", cols=h)
+    k = t * plan.top_k
+    _check(lib.moe_combine(plan._h, t, h, ptr, _out_of(rows, "rows"), n, _array(row, "row", "int32", k),
+                           None if weight is None else _array(weight, "weight", "float32", k), optr,
+                           _out_of(out, "out"), ld, _stream(stream)), "moe_combine")
+
+
+def moe_combine_backward(plan: MoePlan, rows, row, weight, d_out, d_rows, d_weight, stream=None):
+    """d_rows[row[t][j]] = weight[t][j] * d_out[t] (of rows' type) and d_weight[t][j] =
+    <d_out[t], rows[row[t][j]]> (FP32)."""
+    ptr, n, h = _whole_rows(rows, "rows")
+    dptr, m, _ = _whole_rows(d_rows, "d_rows", h)
+    if m != n or d_rows.dtype != rows.dtype:
+        raise ValueError(f"d_rows must be {n} x {h} of rows' type, {rows.dtype}")
+    optr, t, _, ld = _matrix(d_out, "d_out", cols=h)
+    k = t * plan.top_k
+    _check(lib.moe_combine_backward(plan._h, t, h, ptr, _out_of(rows, "rows"), n, _array(row, "row", "int32", k),
+                                    _array(weight, "weight", "float32", k), optr, _out_of(d_out, "d_out"), ld, dptr,
+                                    _array(d_weight, "d_weight", "float32", k), _stream(stream)),
+           "moe_combine_backward")

@@ -86,7 +86,18 @@ class tst_work_item(ctypes.Structure):
                 ("k_begin", ctypes.c_int32), ("k_count", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
+class tst_moe_options(ctypes.Structure):
+    _fields_ = [("normalize", ctypes.c_int32), ("balance_coef", ctypes.c_float), ("host_only", ctypes.c_int32)]
+
+
+class tst_moe_plan_info(ctypes.Structure):
+    _fields_ = [("max_tokens", ctypes.c_int64), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("balance_coef", ctypes.c_float),
+                ("workspace_bytes", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
 _SIGNATURES = {
     "gemm_plan_create": (ctypes.c_int, [ctypes.POINTER(_P), ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                         ctypes.c_int, ctypes.c_int, tst_mapping, ctypes.c_int,
@@ -126,6 +137,15 @@ _SIGNATURES = {
     "gemm_streamk_noalloc": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                             tst_mapping, ctypes.c_int, ctypes.POINTER(tst_epilogue),
                                             ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_plan_create": (ctypes.c_int, [ctypes.POINTER(_P), _I64, _I32, _I32, ctypes.POINTER(tst_moe_options)]),
+    "moe_plan_get_info": (ctypes.c_int, [_P, ctypes.POINTER(tst_moe_plan_info)]),
+    "moe_plan_destroy": (ctypes.c_int, [_P]),
+    "moe_status_query": (ctypes.c_int, [_P]),
+    "moe_route": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_route_backward": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "moe_dispatch": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _I64, _P, _P, _I32, _I64, _P, _P]),
+    "moe_combine": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _I64, _P, _P, _P, _I32, _I64, _P]),
+    "moe_combine_backward": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _I64, _P, _P, _P, _I32, _I64, _P, _P, _P]),
 }
 
 TST_NOALLOC_SCRATCH_BYTES = 16 << 20

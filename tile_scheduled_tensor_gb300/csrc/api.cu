@@ -310,12 +310,12 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
   tst_plan_options o{};
   if (opts) o = *opts;
   // block-scaled FP8 operands: their own kernel, single CTAs with 128 x 128 tiles and one-atom
-  // k-tiles, the basic epilogue, whole tiles (static or persistent)
+  // k-tiles, the basic epilogue, whole tiles (static, persistent, or grouped with shared N and K)
   const bool bs = epi->ab_block_k != 0;
   if (bs) {
     if (epi->ab_block_k != 32 && epi->ab_block_k != 64 && epi->ab_block_k != 128) return TST_ERR_INVALID_ARG;
     if (epi->ab_block_rows < 1 || epi->ab_block_rows_b < 0) return TST_ERR_INVALID_ARG;
-    if (dtype == TST_BF16 || needs_ext(*epi) || groups > 0 || (schedule != TST_STATIC && schedule != TST_PERSISTENT) ||
+    if (dtype == TST_BF16 || needs_ext(*epi) || shapes != nullptr || (schedule != TST_STATIC && schedule != TST_PERSISTENT) ||
         (o.bn != 0 && o.bn != 128) || (o.cta_group != 0 && o.cta_group != 1) || (o.bk != 0 && o.bk != 128) ||
         o.cluster_n == 2 || o.pdl || o.epilogue_store == TST_STORE_TMA || o.l2_prefetch)
       return TST_ERR_UNSUPPORTED;
@@ -941,6 +941,7 @@ tst_status launch(tst_plan* p, const void* A, const void* B, void* C, const tst_
     kp.bs_rows_b = bs_rows_b(e);
     kp.bs_k = e.ab_block_k;
     kp.bs_kblocks = static_cast<int32_t>(ceil_div(p->K, e.ab_block_k));
+    kp.bs_group_rows = static_cast<int32_t>(ceil_div(p->N, kp.bs_rows_b));
   }
   kp.box3d = p->box3d ? 1 : 0;
   if (p->ext_on) {

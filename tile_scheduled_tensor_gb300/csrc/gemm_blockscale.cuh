@@ -29,8 +29,8 @@
 //               alpha, the column bias and ReLU, cast and store.  The same warps copy the
 //               scales into shared memory a window of k-blocks ahead (cp.async), so no
 //               scale load waits on the critical path.
-// The schedules are the static and persistent ones (whole tiles; each work item starts
-// at k = 0).  Every wait is bounded as in the plain kernel.
+// The schedules are the static and persistent ones and the grouped GEMM of shared N and K
+// (whole tiles; each work item starts at k = 0).  Every wait is bounded as in the plain kernel.
 #pragma once
 #include "gemm_kernel.cuh"
 
@@ -156,7 +156,9 @@ __device__ __forceinline__ void bs_stage_window(const KernelParams& p, const Wor
   const int32_t lim = is_a ? p.M : p.N;
   int32_t idx = is_a ? w.row0 + e : w.col0 + (e - 128);
   idx = idx < lim ? idx : lim - 1;   // rows and columns past the matrix carry zero partials
-  const float* src = (is_a ? p.bs_a : p.bs_b) + static_cast<int64_t>(idx / (is_a ? p.bs_rows : p.bs_rows_b)) * p.bs_kblocks;
+  // each group of a grouped GEMM has its own rows of B's scales
+  const int64_t first = is_a ? 0 : static_cast<int64_t>(w.group) * p.bs_group_rows;
+  const float* src = (is_a ? p.bs_a : p.bs_b) + (first + idx / (is_a ? p.bs_rows : p.bs_rows_b)) * p.bs_kblocks;
 #pragma unroll
   for (int i = 0; i < kBsWindow; ++i) {
     int32_t kb = kb0 + i;

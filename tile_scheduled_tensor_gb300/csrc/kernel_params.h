@@ -106,6 +106,7 @@ struct KernelParams {
   const float* bs_b;
   int32_t bs_rows, bs_k, bs_kblocks;
   int32_t bs_rows_b;
+  int32_t bs_group_rows;    // grouped: scale rows per group of B, ceil(N / bs_rows_b)
   int32_t box3d;            // A and B maps are 3-D (atom elements, rows, atoms): one box per operand
                             // and stage brings all KA atom columns (HyTiS half-width B stays 2-D)
   int32_t staging_offset;   // SK_TMA: byte offset of the staging buffers from the aligned shared base
