@@ -47,8 +47,12 @@ int32_t route_chunk(int64_t tokens) {
   return 256;
 }
 
-size_t route_smem(int32_t experts, int32_t chunk) {
-  return (static_cast<size_t>(experts) * (chunk / 32) + static_cast<size_t>(tst::kRouteWarps) * experts + 4) * 4;
+// shared memory of a routing block: RouteShared, and the small kernel's staged choices
+size_t route_smem(int32_t experts, int32_t top_k, int32_t chunk) {
+  const bool small = experts <= tst::kRouteThreadRow;
+  const size_t warps = small ? chunk / 32 : tst::kRouteWarps;
+  const size_t staged = small ? 2 * static_cast<size_t>(chunk) * (top_k | 1) : 0;
+  return (static_cast<size_t>(experts) * (chunk / 32 + warps + 1) + 1 + staged) * 4;
 }
 
 tst_status launched() {
@@ -56,40 +60,72 @@ tst_status launched() {
   return TST_OK;
 }
 
-// One kernel instance per number of logits that a lane holds.
-#define TST_BY_EXPERTS(E, CALL)      \
-  do {                               \
-    if ((E) <= 32) { CALL(1); }      \
-    else if ((E) <= 64) { CALL(2); } \
-    else if ((E) <= 128) { CALL(4); }\
-    else if ((E) <= 256) { CALL(8); }\
-    else if ((E) <= 512) { CALL(16); }\
-    else { CALL(32); }               \
+// The kernels' instances by the number of experts: a thread's row of 8, 16 or 32 logits, or a
+// warp's with 2 to 32 per lane.
+#define TST_BY_EXPERTS(E, SMALL, WARP)   \
+  do {                                   \
+    if ((E) <= 8) { SMALL(8); }          \
+    else if ((E) <= 16) { SMALL(16); }   \
+    else if ((E) <= tst::kRouteThreadRow) { SMALL(32); } \
+    else if ((E) <= 64) { WARP(2); }     \
+    else if ((E) <= 128) { WARP(4); }    \
+    else if ((E) <= 256) { WARP(8); }    \
+    else if ((E) <= 512) { WARP(16); }   \
+    else { WARP(32); }                   \
   } while (0)
 
+// whether rows of `ld` elements at `p` can be read W elements at a time (moe_route.cuh's RowMap)
+template <typename T, int VPL>
+bool whole_packs(const void* p, int64_t ld, int32_t experts) {
+  constexpr int W = tst::RowMap<T, VPL>::W;
+  return aligned(p, W * sizeof(T)) && ld % W == 0 && experts % W == 0;
+}
+
 template <typename T>
-const void* rows_kernel(int32_t experts) {
+const void* route_kernel(const RouteParams& p) {
   const void* f = nullptr;
-#define TST_PICK(V) f = reinterpret_cast<const void*>(&tst::route_rows_kernel<T, V>)
-  TST_BY_EXPERTS(experts, TST_PICK);
-#undef TST_PICK
+#define TST_SMALL(EM) f = reinterpret_cast<const void*>(&tst::route_rows_small_kernel<T, EM>)
+#define TST_WARP(V)                                                                                      \
+  f = whole_packs<T, V>(p.logits, p.ld, p.experts) ? reinterpret_cast<const void*>(&tst::route_rows_kernel<T, V, true>) \
+                                                   : reinterpret_cast<const void*>(&tst::route_rows_kernel<T, V, false>)
+  TST_BY_EXPERTS(p.experts, TST_SMALL, TST_WARP);
+#undef TST_SMALL
+#undef TST_WARP
   return f;
 }
 
 template <typename T>
-void launch_route(const RouteParams& p, cudaStream_t s) {
-  const size_t smem = route_smem(p.experts, p.chunk);
-#define TST_CALL(V) tst::route_rows_kernel<T, V><<<p.chunks, tst::kRouteThreads, smem, s>>>(p)
-  TST_BY_EXPERTS(p.experts, TST_CALL);
-#undef TST_CALL
+const void* grad_kernel(const RouteGradParams& p) {
+  const void* f = nullptr;
+#define TST_SMALL(EM) f = reinterpret_cast<const void*>(&tst::route_grad_small_kernel<T, EM>)
+#define TST_WARP(V)                                                                                       \
+  f = whole_packs<T, V>(p.logits, p.ld, p.experts) && whole_packs<T, V>(p.d_logits, p.d_ld, p.experts)    \
+          ? reinterpret_cast<const void*>(&tst::route_grad_kernel<T, V, true>)                            \
+          : reinterpret_cast<const void*>(&tst::route_grad_kernel<T, V, false>)
+  TST_BY_EXPERTS(p.experts, TST_SMALL, TST_WARP);
+#undef TST_SMALL
+#undef TST_WARP
+  return f;
 }
 
-template <typename T>
-void launch_grad(const RouteGradParams& p, int32_t grid, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(p.experts) * 4;
-#define TST_CALL(V) tst::route_grad_kernel<T, V><<<grid, tst::kRouteThreads, smem, s>>>(p)
-  TST_BY_EXPERTS(p.experts, TST_CALL);
-#undef TST_CALL
+// Launch f(params); `after`: it may start while the kernel before it on the stream finishes, and
+// waits for that kernel itself (griddepcontrol.wait).
+template <typename P>
+bool launch(const void* f, int64_t grid, int32_t threads, size_t smem, cudaStream_t s, P& params, bool after = false) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (after) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  void* args[] = {&params};
+  return cudaLaunchKernelExC(&cfg, f, args) == cudaSuccess;
 }
 
 // What every run checks of its plan and token count.
@@ -152,13 +188,18 @@ tst_status moe_plan_create(tst_moe_plan** out, int64_t max_tokens, int32_t exper
     if (major != 10 || minor != 3) { delete p; return TST_ERR_UNSUPPORTED; }  // built for sm_103a only
     p->device = dev;
     p->num_sms = sms;
-    const int smem = static_cast<int>(route_smem(experts, 256));
-    if (cudaFuncSetAttribute(rows_kernel<float>(experts), cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(rows_kernel<__nv_bfloat16>(experts), cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess) {
-      cudaGetLastError();
-      delete p;
-      return TST_ERR_CUDA;
+    // each instance that a call of this plan may take, with and without whole packs
+    const int smem = static_cast<int>(route_smem(experts, top_k, 256));
+    RouteParams a{};
+    a.experts = experts;
+    for (int64_t ld : {int64_t(1024), int64_t(1025)}) {
+      a.ld = ld;
+      for (const void* f : {route_kernel<float>(a), route_kernel<__nv_bfloat16>(a)})
+        if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+          cudaGetLastError();
+          delete p;
+          return TST_ERR_CUDA;
+        }
     }
     if (cudaMalloc(&p->dev_block, p->dev_bytes) != cudaSuccess) {
       cudaGetLastError();
@@ -245,12 +286,22 @@ tst_status moe_route(tst_moe_plan* p, int64_t tokens, const void* logits, int32_
   a.chunks = static_cast<int32_t>(ceil_div(tokens, a.chunk));
   a.normalize = p->normalize;
   a.coef = p->coef;
+  bool ok = true;
   if (tokens > 0) {
-    if (dtype == TST_OUT_F32) launch_route<float>(a, s);
-    else launch_route<__nv_bfloat16>(a, s);
+    const void* f = dtype == TST_OUT_F32 ? route_kernel<float>(a) : route_kernel<__nv_bfloat16>(a);
+    ok = launch(f, a.chunks, a.experts <= tst::kRouteThreadRow ? a.chunk : tst::kRouteThreads,
+                route_smem(a.experts, a.top_k, a.chunk), s, a);
   }
-  tst::route_scan_kernel<<<static_cast<unsigned>(ceil_div(a.experts + 1, tst::kRouteWarps)), tst::kRouteThreads, 0, s>>>(a);
-  tst::route_place_kernel<<<std::max(a.chunks, 1), tst::kRouteThreads, static_cast<size_t>(a.experts) * 4, s>>>(a);
+  if (a.chunks != 1)   // one chunk finishes by itself
+    ok = ok &&
+         launch(reinterpret_cast<const void*>(&tst::route_scan_kernel), ceil_div(a.experts + 1, tst::kRouteWarps),
+                tst::kRouteThreads, 0, s, a, true) &&
+         launch(reinterpret_cast<const void*>(&tst::route_place_kernel), std::max(a.chunks, 1), tst::kRouteThreads,
+                static_cast<size_t>(a.experts) * 4, s, a, true);
+  if (!ok) {
+    cudaGetLastError();
+    return TST_ERR_CUDA;
+  }
   return finish(p, s);
 }
 
@@ -285,9 +336,16 @@ tst_status moe_route_backward(tst_moe_plan* p, int64_t tokens, const void* logit
   a.top_k = p->top_k;
   a.normalize = p->normalize;
   a.coef = p->coef;
-  const int32_t grid = static_cast<int32_t>(std::min<int64_t>(ceil_div(tokens, tst::kRouteWarps), 8 * p->num_sms));
-  if (dtype == TST_OUT_F32) launch_grad<float>(a, grid, s);
-  else launch_grad<__nv_bfloat16>(a, grid, s);
+  const void* f = dtype == TST_OUT_F32 ? grad_kernel<float>(a) : grad_kernel<__nv_bfloat16>(a);
+  const bool small = a.experts <= tst::kRouteThreadRow;
+  // a thread per row, in blocks small enough to spread few rows; or warps, four blocks per SM's worth
+  const int32_t threads = small ? (tokens <= 64 * p->num_sms ? 64 : tst::kRouteThreads) : tst::kRouteThreads;
+  const int64_t grid = small ? ceil_div(tokens, threads)
+                             : std::min<int64_t>(ceil_div(tokens, tst::kRouteWarps), 4 * p->num_sms);
+  if (!launch(f, grid, threads, 0, s, a)) {
+    cudaGetLastError();
+    return TST_ERR_CUDA;
+  }
   return finish(p, s);
 }
 

@@ -9,17 +9,19 @@
 //   L = coef E sum_e (c_e / R) (1 / n) sum_t p_te
 //   row_tj = sum_{e' < S_tj} c_e' + #{t' < t: S_tj in S_t'}
 //
-// Three launches.  route_rows_kernel reads the logits once: a warp holds a row's logits in
-// registers, its maximum is the first chosen logit, and a block leaves per expert the count and
-// the probability sum of its chunk of tokens, and each choice's rank inside the chunk.  Ranks come
-// from a bitmap (experts x tokens of the chunk) in shared memory: the population count of the
-// bits before the token's, so the order never depends on which warp got there first.
-// route_scan_kernel turns the chunks' counts into prefix sums, a warp per expert.
-// route_place_kernel adds the experts' and the chunk's offsets to the ranks.  Every floating
-// sum has a fixed order, so a call is repeatable bit for bit.
+// The logits are read once, by blocks of `chunk` tokens.  Each block leaves per expert the count
+// and the probability sum of its tokens, and each choice's rank inside the chunk, from a bitmap
+// (experts x tokens of the chunk) in shared memory: the population count of the bits before the
+// token's, so the order does not depend on which warp got there first.  Then
+// route_scan_kernel turns the chunks' counts into prefix sums, a warp per expert, and
+// route_place_kernel adds the experts' and the chunks' offsets to the ranks; a call of one chunk
+// does all of it in its one block.  Every floating sum has a fixed order, so a call is repeatable
+// bit for bit.
 #pragma once
 #include <cuda_bf16.h>
 #include <stdint.h>
+
+#include "ptx.cuh"
 
 namespace tst {
 
@@ -27,6 +29,8 @@ constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 32;
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteCandidates = 32;
+constexpr int kRouteThreadRow = 32;   // up to this many experts a thread holds a whole row
 constexpr uint32_t kFullMask = 0xFFFFFFFFu;
 
 struct RouteParams {
@@ -70,150 +74,457 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 constexpr uint32_t kKeyClosed = 0x007FFFFFu;   // order_key(-inf); lower keys stand for no expert
-__device__ __forceinline__ float key_value(uint32_t k) {
+__device__ __forceinline__ float key_value(uint32_t k) {   // a NaN for the NaNs' key
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
+__device__ __forceinline__ float closed_logit() { return __uint_as_float(0xFF800000u); }
 
-template <typename T>
-__device__ __forceinline__ float load_logit(const T* p);
-template <>
-__device__ __forceinline__ float load_logit<float>(const float* p) { return *p; }
-template <>
-__device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
   return v;
 }
 
-// __expf: its argument here is x - max <= 0; its relative error, 2^-22 and a term growing as
-// |x| 2^-24, stays below 1e-6 for every term that a sum of at most 1024 of them can notice.
-__device__ __forceinline__ float exp_shifted(float x, float top) { return __expf(x - top); }
+// e^(x - top).  Between kPlainTop and -kPlainTop, 2^(x log2 e - top log2 e) with one fused step:
+// the rounding of top log2 e is a factor common to the row, which the division by the row's sum
+// takes out, and the step's own rounding is |x - top| 2^-24 relative.  Beyond, where top log2 e
+// may overflow, and for infinities and NaN: __expf of the difference.
+constexpr float kPlainTop = 1.26765060e30f;   // 2^100
+constexpr float kLog2e = 1.44269504088896341f;
+struct RowExp {
+  float top, shift;
+  bool plain;
+  __device__ __forceinline__ explicit RowExp(float t) : top(t), shift(-t * kLog2e), plain(fabsf(t) < kPlainTop) {}
+  __device__ __forceinline__ float fast(float x) const { return exp2_approx(fmaf(x, kLog2e, shift)); }
+  __device__ __forceinline__ float any(float x) const { return plain ? fast(x) : __expf(x - top); }
+  static __device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+  }
+};
 
-// VPL: logits per lane; expert e of a row is slot e / 32 of lane e % 32.
+// A row in a warp's registers: lane l holds W adjacent logits in each run of 32 W, so that a lane's
+// loads are up to 16 bytes.  VEC: rows and their starts are multiples of W elements.
 template <typename T, int VPL>
-__global__ void __launch_bounds__(kRouteThreads) route_rows_kernel(const RouteParams p) {
-  extern __shared__ uint32_t route_smem[];
-  const int E = p.experts, k = p.top_k, words = p.chunk / 32;
-  uint32_t* bitmap = route_smem;                                       // E x words
-  float* prob = reinterpret_cast<float*>(bitmap + E * words);          // warps x E
-  int* live_rows = reinterpret_cast<int*>(prob + kRouteWarps * E);     // 1
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.chunk;
-  const int rows = static_cast<int>(p.tokens - t0 < p.chunk ? p.tokens - t0 : p.chunk);
+struct RowMap {
+  static constexpr int W = VPL < static_cast<int>(16 / sizeof(T)) ? VPL : static_cast<int>(16 / sizeof(T));
+  struct alignas(W * sizeof(T)) Pack { T v[W]; };
+  static __device__ __forceinline__ int expert(int v, int lane) { return (v / W) * 32 * W + lane * W + v % W; }
+};
 
-  for (int i = threadIdx.x; i < E * words; i += kRouteThreads) bitmap[i] = 0u;
-  if (threadIdx.x == 0) *live_rows = 0;
-  __syncthreads();
+template <typename T>
+__device__ __forceinline__ float logit_value(T v);
+template <>
+__device__ __forceinline__ float logit_value<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float logit_value<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-  float acc[VPL];
+template <typename T, int VPL, bool VEC>
+__device__ __forceinline__ void load_row(const T* src, int E, int lane, bool on, float (&x)[VPL]) {
+  using Map = RowMap<T, VPL>;
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) acc[v] = 0.0f;
-  for (int r = warp; r < rows; r += kRouteWarps) {
-    const int64_t t = t0 + r;
-    const bool on = p.mask == nullptr || p.mask[t] != 0;
-    const T* src = static_cast<const T*>(p.logits) + t * p.ld;
-    uint32_t key[VPL];
-    float e[VPL];
+  for (int q = 0; q < VPL / Map::W; ++q) {
+    const int e0 = Map::expert(q * Map::W, lane);
+    if (VEC) {
+      typename Map::Pack pk;
+      const bool in = on && e0 < E;
+      if (in) pk = *reinterpret_cast<const typename Map::Pack*>(src + e0);
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int x = v * 32 + lane;
-      e[v] = (on && x < E) ? load_logit(src + x) : __uint_as_float(0xFF800000u);
-      key[v] = x < E ? order_key(e[v]) : 0u;
-    }
-    int chosen = -1;           // lane j: the j-th expert, its logit's key
-    uint32_t chosen_key = 0u;
-    uint32_t top_key = 0u;
-    for (int j = 0; j < k; ++j) {
-      uint32_t best = 0u;
-      int at = 0;
+      for (int i = 0; i < Map::W; ++i) x[q * Map::W + i] = in ? logit_value<T>(pk.v[i]) : closed_logit();
+    } else {
 #pragma unroll
-      for (int v = 0; v < VPL; ++v)
-        if (key[v] > best) { best = key[v]; at = v; }
-      const uint32_t m = __reduce_max_sync(kFullMask, best);
-      if (j == 0) top_key = m;
-      if (m <= kKeyClosed) break;
-      const uint32_t who = __reduce_min_sync(kFullMask, best == m ? static_cast<uint32_t>(at * 32 + lane) : 0xFFFFu);
-      if (lane == j) { chosen = static_cast<int>(who); chosen_key = m; }
-#pragma unroll
-      for (int v = 0; v < VPL; ++v)
-        if (static_cast<uint32_t>(v * 32 + lane) == who) key[v] = 0u;
-    }
-    const bool live = top_key > kKeyClosed;
-    float w = 0.0f;
-    if (live) {
-      const float top = top_key == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : key_value(top_key);
-      float sum = 0.0f;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        e[v] = v * 32 + lane < E ? exp_shifted(e[v], top) : 0.0f;
-        sum += e[v];
-      }
-      sum = warp_sum(sum);
-      const float inv = 1.0f / sum;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) acc[v] = fmaf(e[v], inv, acc[v]);
-      if (chosen >= 0)
-        w = exp_shifted(chosen_key == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : key_value(chosen_key), top);
-      const float over = p.normalize ? warp_sum(w) : sum;
-      w = w / over;
-      if (chosen < 0) w = 0.0f;
-      if (lane == 0) atomicAdd(live_rows, 1);
-      if (chosen >= 0) atomicOr(&bitmap[chosen * words + (r >> 5)], 1u << (r & 31));
-    }
-    if (lane < k) {
-      p.expert[t * k + lane] = chosen;
-      p.weight[t * k + lane] = w;
+      for (int i = 0; i < Map::W; ++i)
+        x[q * Map::W + i] = (on && e0 + i < E) ? logit_value<T>(src[e0 + i]) : closed_logit();
     }
   }
-#pragma unroll
-  for (int v = 0; v < VPL; ++v)
-    if (v * 32 + lane < E) prob[warp * E + v * 32 + lane] = acc[v];
-  __syncthreads();
+}
 
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+template <typename T, int VPL, bool VEC>
+__device__ __forceinline__ void store_row(T* dst, int E, int lane, const float (&x)[VPL]) {
+  using Map = RowMap<T, VPL>;
+#pragma unroll
+  for (int q = 0; q < VPL / Map::W; ++q) {
+    const int e0 = Map::expert(q * Map::W, lane);
+    if (VEC) {
+      typename Map::Pack pk;
+#pragma unroll
+      for (int i = 0; i < Map::W; ++i) pk.v[i] = static_cast<T>(x[q * Map::W + i]);
+      if (e0 < E) *reinterpret_cast<typename Map::Pack*>(dst + e0) = pk;
+    } else {
+#pragma unroll
+      for (int i = 0; i < Map::W; ++i)
+        if (e0 + i < E) dst[e0 + i] = static_cast<T>(x[q * Map::W + i]);
+    }
+  }
+}
+
+// Shared memory of a routing block: the bitmap, each warp's probability sums, the experts' first
+// rows (one-chunk calls), the count of live rows.
+struct RouteShared {
+  uint32_t* bitmap;   // E x words
+  float* prob;        // warps x E
+  int32_t* first;     // E
+  int* live;          // 1
+  __device__ __forceinline__ RouteShared(uint32_t* base, int E, int words, int warps) {
+    bitmap = base;
+    prob = reinterpret_cast<float*>(bitmap + E * words);
+    first = reinterpret_cast<int32_t*>(prob + warps * E);
+    live = first + E;
+  }
+};
+
+// What a block does once its tokens' choices are in the bitmap (and in p.expert, written by this
+// block): the chunk's counts and sums, and the ranks; or, alone, the final rows and totals.
+__device__ __forceinline__ void finish_chunk(const RouteParams& p, const RouteShared& s, int words, int warps, int64_t t0,
+                                             int rows) {
+  const int E = p.experts, k = p.top_k;
+  const bool alone = p.chunks == 1;
+  __syncthreads();
+  if (!alone) ptx::griddep_launch_dependents();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int c = 0;
-    for (int i = 0; i < words; ++i) c += __popc(bitmap[e * words + i]);
-    float s = 0.0f;
-    for (int i = 0; i < kRouteWarps; ++i) s += prob[i * E + e];
-    p.part_count[static_cast<int64_t>(e) * p.chunks + blockIdx.x] = c;
-    p.part_prob[static_cast<int64_t>(e) * p.chunks + blockIdx.x] = s;
+    for (int i = 0; i < words; ++i) c += __popc(s.bitmap[e * words + i]);
+    float sum = 0.0f;
+    for (int i = 0; i < warps; ++i) sum += s.prob[i * E + e];
+    if (alone) {
+      s.first[e] = c;
+      s.prob[e] = sum;   // this thread alone reads column e
+      p.counts[e] = c;
+    } else {
+      p.part_count[static_cast<int64_t>(e) * p.chunks + blockIdx.x] = c;
+      p.part_prob[static_cast<int64_t>(e) * p.chunks + blockIdx.x] = sum;
+    }
   }
-  if (threadIdx.x == 0) p.part_count[static_cast<int64_t>(E) * p.chunks + blockIdx.x] = *live_rows;
-  // this block's own writes of p.expert, read back after the barrier
-  for (int i = threadIdx.x; i < rows * k; i += kRouteThreads) {
+  if (!alone && threadIdx.x == 0) p.part_count[static_cast<int64_t>(E) * p.chunks + blockIdx.x] = *s.live;
+  if (alone) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      int32_t before = 0;
+      float dot = 0.0f;
+      for (int b = 0; b < E; b += 32) {
+        const int e = b + lane;
+        const int32_t c = e < E ? s.first[e] : 0;
+        if (e < E) dot = fmaf(static_cast<float>(c), s.prob[e], dot);
+        int32_t incl = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int32_t o = __shfl_up_sync(kFullMask, incl, d);
+          if (lane >= d) incl += o;
+        }
+        if (e < E) s.first[e] = before + incl - c;
+        before += __shfl_sync(kFullMask, incl, 31);
+      }
+      dot = warp_sum(dot);
+      if (lane == 0) {
+        const int live = *s.live;
+        p.totals[0] = before;
+        p.totals[1] = live;
+        *p.loss = before > 0 ? p.coef * static_cast<float>(E) * (dot / static_cast<float>(before) / static_cast<float>(live))
+                             : 0.0f;
+      }
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < rows * k; i += blockDim.x) {
     const int r = i / k;
     const int e = p.expert[t0 * k + i];
     int rank = -1;
     if (e >= 0) {
-      rank = __popc(bitmap[e * words + (r >> 5)] & ((1u << (r & 31)) - 1u));
-      for (int q = 0; q < (r >> 5); ++q) rank += __popc(bitmap[e * words + q]);
+      rank = __popc(s.bitmap[e * words + (r >> 5)] & ((1u << (r & 31)) - 1u));
+      for (int q = 0; q < (r >> 5); ++q) rank += __popc(s.bitmap[e * words + q]);
+      if (alone) rank += s.first[e];
     }
     p.row[t0 * k + i] = rank;
   }
 }
 
+// The choice by k rounds of a warp maximum over integer keys: every value, any number of ties.
+// The row is read again (it was just read).  Lane j gets the j-th choice.
+template <typename T, int VPL, bool VEC>
+__device__ __forceinline__ void choose_by_rounds(const T* src, int E, int k, int lane, bool on, int& chosen, float& value) {
+  using Map = RowMap<T, VPL>;
+  float x[VPL];
+  load_row<T, VPL, VEC>(src, E, lane, on, x);
+  uint32_t key[VPL];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) key[v] = Map::expert(v, lane) < E ? order_key(x[v]) : 0u;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0u;
+    int at = 0;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      if (key[v] > best) { best = key[v]; at = Map::expert(v, lane); }   // a lane's experts rise with v
+    const uint32_t m = __reduce_max_sync(kFullMask, best);
+    if (m <= kKeyClosed) break;
+    const int who = static_cast<int>(__reduce_min_sync(kFullMask, best == m ? static_cast<uint32_t>(at) : 0xFFFFu));
+    if (lane == j) { chosen = who; value = key_value(m); }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      if (Map::expert(v, lane) == who) key[v] = 0u;
+  }
+}
+
+// A warp per row, rows dealt to the block's warps in turn.  The choice: k - 1 rounds of a warp
+// maximum over the lanes' own maxima leave a bound that at least k logits reach; those that do,
+// seldom more than a few over k, go to a list in shared memory with their experts in the low word,
+// and each finds its rank by comparing itself with the others.  That takes a third of the
+// instructions of k rounds over all logits, which remain for rows with more than 32 on the list,
+// NaN, infinities or magnitudes over 2^100.  The bound is issue slots, about 200 a row of 256
+// logits, not the 1 KB that it reads.
+template <typename T, int VPL, bool VEC>
+__global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) route_rows_kernel(const RouteParams p) {
+  using Map = RowMap<T, VPL>;
+  extern __shared__ uint32_t route_smem[];
+  __shared__ uint64_t list[kRouteWarps][kRouteCandidates];
+  const int E = p.experts, k = p.top_k, words = p.chunk / 32;
+  const RouteShared s(route_smem, E, words, kRouteWarps);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t below = (1u << lane) - 1u;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.chunk;
+  const int rows = static_cast<int>(p.tokens - t0 < p.chunk ? p.tokens - t0 : p.chunk);
+
+  for (int i = threadIdx.x; i < E * words; i += kRouteThreads) s.bitmap[i] = 0u;
+  if (threadIdx.x == 0) *s.live = 0;
+  __syncthreads();
+
+  float acc[VPL], next[VPL];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) acc[v] = 0.0f;
+  int live = 0;
+  auto source = [&](int r) { return static_cast<const T*>(p.logits) + (t0 + r) * p.ld; };
+  auto routed = [&](int r) { return p.mask == nullptr || p.mask[t0 + r] != 0; };
+  if (warp < rows) load_row<T, VPL, VEC>(source(warp), E, lane, routed(warp), next);
+  for (int r = warp; r < rows; r += kRouteWarps) {
+    float x[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) x[v] = next[v];
+    if (r + kRouteWarps < rows)   // the next row's loads fly while this one is worked on
+      load_row<T, VPL, VEC>(source(r + kRouteWarps), E, lane, routed(r + kRouteWarps), next);
+    float best = x[0];
+#pragma unroll
+    for (int v = 1; v < VPL; ++v) best = max_nan(best, x[v]);
+    const RowExp ex(warp_max_nan(best));
+    int chosen = -1, at = lane;   // this lane's choice and its place among the row's
+    float w = 0.0f;
+    if (ex.top != closed_logit()) {
+      ++live;
+      float e[VPL], sum = 0.0f;
+      if (ex.plain) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) { e[v] = ex.fast(x[v]); sum += e[v]; }
+      } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) { e[v] = ex.any(x[v]); sum += Map::expert(v, lane) < E ? e[v] : 0.0f; }
+      }
+      sum = warp_sum(sum);
+      const float inv = __fdividef(1.0f, sum);   // 1 <= sum <= 1024, or NaN
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) acc[v] = fmaf(e[v], inv, acc[v]);
+
+      bool listed = ex.plain;
+      if (listed) {
+        float bound = ex.top, own = best;
+        for (int j = 1; j < k; ++j) {
+          own = own == bound ? closed_logit() : own;
+          bound = warp_max(own);
+        }
+        int n = 0;
+        for (;;) {
+          const bool has = best >= bound && best > closed_logit();
+          const uint32_t who = __ballot_sync(kFullMask, has);
+          if (who == 0u) break;
+          const int slot = n + __popc(who & below);
+          n += __popc(who);
+          if (n > kRouteCandidates) { listed = false; break; }
+          if (has) {   // list this lane's best, and find the next
+            int v0 = 0;
+#pragma unroll
+            for (int v = VPL - 1; v >= 0; --v)
+              if (x[v] == best) v0 = v;
+            list[warp][slot] = (static_cast<uint64_t>(order_key(best)) << 32) |
+                               (0xFFFFFFFFu - static_cast<uint32_t>(Map::expert(v0, lane)));
+            best = closed_logit();
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) {
+              if (v == v0) x[v] = closed_logit();
+              best = fmaxf(best, x[v]);
+            }
+          }
+        }
+        __syncwarp();
+        if (listed) {
+          // two lanes per listed logit share the comparisons when at most 16 are listed
+          const bool halves = n <= 16;
+          const int mine = halves ? lane & 15 : lane;
+          const uint64_t c = mine < n ? list[warp][mine] : 0u;
+          const int share = halves ? (n + 1) >> 1 : n;
+          const int from = halves && lane >= 16 ? share : 0;
+          int rank = 0;
+          for (int i = 0; i < share; ++i)
+            if (from + i < n && list[warp][from + i] > c) ++rank;
+          if (halves) rank += __shfl_xor_sync(kFullMask, rank, 16);
+          if (lane < n) {
+            at = rank;   // from the k-th on: no place; the other lanes keep theirs, -1 where fewer than k are open
+            if (rank < k) {
+              chosen = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(c));
+              w = ex.fast(key_value(static_cast<uint32_t>(c >> 32)));
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (!listed) {
+        float value = 0.0f;
+        choose_by_rounds<T, VPL, VEC>(source(r), E, k, lane, true, chosen, value);
+        if (chosen >= 0) w = ex.any(value);
+      }
+      const float over = p.normalize ? warp_sum(w) : sum;
+      w = chosen >= 0 ? w / over : 0.0f;
+      if (chosen >= 0) atomicOr(&s.bitmap[chosen * words + (r >> 5)], 1u << (r & 31));
+    }
+    if (at < k) {
+      p.expert[(t0 + r) * k + at] = chosen;
+      p.weight[(t0 + r) * k + at] = w;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < VPL; ++v)
+    if (Map::expert(v, lane) < E) s.prob[warp * E + Map::expert(v, lane)] = acc[v];
+  if (lane == 0 && live > 0) atomicAdd(s.live, live);
+  finish_chunk(p, s, words, kRouteWarps, t0, rows);
+}
+
+// A thread per row, for up to 32 experts: the logits, their keys and the k rounds stay in one
+// thread's registers, with no exchange between lanes but for the probability sums.  A block has a
+// thread per token of its chunk; choices pass through shared memory so that they leave in order.
+template <typename T, int EM>
+__global__ void __launch_bounds__(kRouteThreads) route_rows_small_kernel(const RouteParams p) {
+  extern __shared__ uint32_t route_smem[];
+  const int E = p.experts, k = p.top_k, words = p.chunk / 32, warps = words;
+  const RouteShared s(route_smem, E, words, warps);
+  const int pitch = k | 1;   // odd: a warp's threads write distinct banks
+  int32_t* out_expert = reinterpret_cast<int32_t*>(s.live + 1);
+  float* out_weight = reinterpret_cast<float*>(out_expert + p.chunk * pitch);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.chunk;
+  const int rows = static_cast<int>(p.tokens - t0 < p.chunk ? p.tokens - t0 : p.chunk);
+  const int r = threadIdx.x;
+  if (threadIdx.x == 0) *s.live = 0;
+  __syncthreads();
+
+  const bool on = r < rows && (p.mask == nullptr || p.mask[t0 + r] != 0);
+  const T* src = static_cast<const T*>(p.logits) + (t0 + r) * p.ld;
+  float x[EM];
+  uint32_t key[EM], top_key = 0u;
+#pragma unroll
+  for (int e = 0; e < EM; ++e) {
+    x[e] = (on && e < E) ? logit_value<T>(src[e]) : closed_logit();
+    key[e] = e < E ? order_key(x[e]) : 0u;
+    top_key = key[e] > top_key ? key[e] : top_key;
+  }
+  const bool live = top_key > kKeyClosed;
+  const RowExp ex(key_value(top_key));
+  float sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < EM; ++e) {
+    x[e] = live && e < E ? ex.any(x[e]) : 0.0f;
+    sum += x[e];
+  }
+  uint32_t taken = 0u;
+  float chosen_sum = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = kKeyClosed;
+    int at = -1;
+#pragma unroll
+    for (int e = 0; e < EM; ++e)
+      if (key[e] > best) { best = key[e]; at = e; }
+    float w = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EM; ++e)
+      if (e == at) { key[e] = 0u; w = x[e]; }
+    if (at >= 0) taken |= 1u << at;
+    chosen_sum += w;
+    out_expert[r * pitch + j] = at;
+    out_weight[r * pitch + j] = w;
+  }
+  const float inv = live ? 1.0f / sum : 0.0f;
+  const float over = live ? 1.0f / (p.normalize ? chosen_sum : sum) : 0.0f;
+  const uint32_t live_rows = __ballot_sync(kFullMask, live);
+  if (lane == 0 && live_rows != 0u) atomicAdd(s.live, __popc(live_rows));
+  for (int j = 0; j < k; ++j) out_weight[r * pitch + j] *= over;
+#pragma unroll
+  for (int e = 0; e < EM; ++e) {
+    if (e < E) {
+      const uint32_t bits = __ballot_sync(kFullMask, (taken >> e) & 1u);
+      const float q = warp_sum(x[e] * inv);
+      if (lane == 0) {
+        s.bitmap[e * words + warp] = bits;
+        s.prob[warp * E + e] = q;
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * k; i += blockDim.x) {
+    const int row = i / k, j = i - row * k;
+    const int e = out_expert[row * pitch + j];
+    p.expert[t0 * k + i] = e;
+    p.weight[t0 * k + i] = e >= 0 ? out_weight[row * pitch + j] : 0.0f;
+  }
+  finish_chunk(p, s, words, warps, t0, rows);
+}
+
 // A warp per expert (and one for the live rows): the chunks' counts become exclusive prefix
-// sums, their total counts[e]; the probability sums are added in a fixed order.
+// sums, their total counts[e]; the probability sums are added in a fixed order.  A lane takes 8
+// values, 32 apart, in flight at once.
 __global__ void __launch_bounds__(kRouteThreads) route_scan_kernel(const RouteParams p) {
+  constexpr int PER = 8;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   const int e = blockIdx.x * kRouteWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (e > p.experts) return;
   int32_t* count = p.part_count + static_cast<int64_t>(e) * p.chunks;
+  const float* part = p.part_prob + static_cast<int64_t>(e) * p.chunks;
   int32_t before = 0;
   float s = 0.0f;
-  for (int b = 0; b < p.chunks; b += 32) {
-    const bool in = b + lane < p.chunks;
-    const int32_t c = in ? count[b + lane] : 0;
-    if (e < p.experts && in) s += p.part_prob[static_cast<int64_t>(e) * p.chunks + b + lane];
-    int32_t incl = c;
+  for (int b = 0; b < p.chunks; b += 32 * PER) {
+    int32_t c[PER];
+    float q[PER];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int32_t o = __shfl_up_sync(kFullMask, incl, d);
-      if (lane >= d) incl += o;
+    for (int i = 0; i < PER; ++i) {
+      const int at = b + i * 32 + lane;
+      c[i] = at < p.chunks ? count[at] : 0;
+      q[i] = (at < p.chunks && e < p.experts) ? part[at] : 0.0f;
     }
-    if (in) count[b + lane] = before + incl - c;
-    before += __shfl_sync(kFullMask, incl, 31);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = b + i * 32 + lane;
+      s += q[i];
+      int32_t incl = c[i];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(kFullMask, incl, d);
+        if (lane >= d) incl += o;
+      }
+      if (at < p.chunks) count[at] = before + incl - c[i];
+      before += __shfl_sync(kFullMask, incl, 31);
+    }
   }
   s = warp_sum(s);
   if (lane == 0) {
@@ -227,7 +538,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_scan_kernel(const RoutePa
 }
 
 // Rows of a chunk's choices: the rank inside the chunk, the chunk's offset inside the expert and
-// the expert's first row.  The last block writes R and the loss too.
+// the expert's first row.  The last block writes R and the loss too.  (No chunks: counts, totals
+// and loss of no tokens.)
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteParams p) {
   extern __shared__ uint32_t route_smem[];
   int32_t* first = reinterpret_cast<int32_t*>(route_smem);   // E: first row of each expert
@@ -235,6 +547,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteP
   __shared__ float warp_loss[kRouteWarps];
   const int E = p.experts, k = p.top_k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::griddep_wait();
   int32_t before = 0;
   for (int b = 0; b < E; b += kRouteThreads) {
     const int e = b + static_cast<int>(threadIdx.x);
@@ -252,16 +565,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteP
       if (w < warp) add += warp_total[w];
       all += warp_total[w];
     }
-    if (e < E) first[e] = add + incl - c;
+    if (e < E) first[e] = add + incl - c + (p.chunks > 0 ? p.part_count[static_cast<int64_t>(e) * p.chunks + blockIdx.x] : 0);
     before += all;
     __syncthreads();
   }
   if (blockIdx.x == gridDim.x - 1) {
     const int32_t live = p.totals[1];
     float s = 0.0f;
-    for (int e = threadIdx.x; e < E; e += kRouteThreads)
-      s += (static_cast<float>(p.counts[e]) / static_cast<float>(before > 0 ? before : 1)) *
-           (p.prob[e] / static_cast<float>(live > 0 ? live : 1));
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) s = fmaf(static_cast<float>(p.counts[e]), p.prob[e], s);
     s = warp_sum(s);
     if (lane == 0) warp_loss[warp] = s;
     __syncthreads();
@@ -269,7 +580,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteP
       float all = 0.0f;
       for (int w = 0; w < kRouteWarps; ++w) all += warp_loss[w];
       p.totals[0] = before;
-      *p.loss = p.coef * static_cast<float>(E) * all;
+      *p.loss = before > 0 ? p.coef * static_cast<float>(E) * (all / static_cast<float>(before) / static_cast<float>(live)) : 0.0f;
     }
   }
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.chunk;
@@ -277,87 +588,162 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteP
   const int rows = static_cast<int>(left < p.chunk ? left : p.chunk);
   for (int i = threadIdx.x; i < rows * k; i += kRouteThreads) {
     const int e = p.expert[t0 * k + i];
-    if (e >= 0) p.row[t0 * k + i] += first[e] + p.part_count[static_cast<int64_t>(e) * p.chunks + blockIdx.x];
+    if (e >= 0) p.row[t0 * k + i] += first[e];
   }
 }
 
 // d_l = p (g - <p, g>) with g_e = dL coef E c_e / (R n), the counts held fixed, plus the weights'
 // part: without normalisation dw joins g at the chosen experts; with it the weights are a softmax
-// over the chosen logits alone, so w (dw - <w, dw>) is added there.  A warp per row; the
-// probabilities are computed again from the logits, which costs less than reading them would.
-template <typename T, int VPL>
-__global__ void __launch_bounds__(kRouteThreads) route_grad_kernel(const RouteGradParams p) {
-  extern __shared__ uint32_t route_smem[];
-  float* g_shared = reinterpret_cast<float*>(route_smem);
+// over the chosen logits alone, so w (dw - <w, dw>) is added there.  The probabilities are
+// computed again from the logits, which costs less than reading them would.
+__device__ __forceinline__ float grad_scale(const RouteGradParams& p) {
+  if (p.d_loss == nullptr) return 0.0f;
+  const float rows = static_cast<float>(p.totals[0] > 0 ? p.totals[0] : 1);
+  const float live = static_cast<float>(p.totals[1] > 0 ? p.totals[1] : 1);
+  return *p.d_loss * (p.coef * static_cast<float>(p.experts)) / (rows * live);
+}
+
+// A warp per row; the chosen experts' parts pass through a row of shared memory to the lanes that
+// hold those experts.  Bound by memory: the logits in, the gradient out.
+template <typename T, int VPL, bool VEC>
+__global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) route_grad_kernel(const RouteGradParams p) {
+  using Map = RowMap<T, VPL>;
+  __shared__ alignas(16) float part_all[kRouteWarps][32 * VPL];
   const int E = p.experts, k = p.top_k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float rows_total = static_cast<float>(p.totals[0] > 0 ? p.totals[0] : 1);
-  const float live_total = static_cast<float>(p.totals[1] > 0 ? p.totals[1] : 1);
-  const float scale = p.d_loss ? *p.d_loss * (p.coef * static_cast<float>(E)) / (rows_total * live_total) : 0.0f;
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) g_shared[e] = static_cast<float>(p.counts[e]) * scale;
-  __syncthreads();
+  float* part = part_all[warp];
+  const float scale = grad_scale(p);
+  float g[VPL];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const int e = Map::expert(v, lane);
+    g[v] = e < E ? static_cast<float>(p.counts[e]) * scale : 0.0f;
+    part[v * 32 + lane] = 0.0f;
+  }
+  __syncwarp();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < p.tokens; t += step) {
-    const bool on = p.mask == nullptr || p.mask[t] != 0;
+  auto routed = [&](int64_t t) { return p.mask == nullptr || p.mask[t] != 0; };
+  float next[VPL];
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+  if (t < p.tokens) load_row<T, VPL, VEC>(static_cast<const T*>(p.logits) + t * p.ld, E, lane, routed(t), next);
+  for (; t < p.tokens; t += step) {
     const T* src = static_cast<const T*>(p.logits) + t * p.ld;
     T* dst = static_cast<T*>(p.d_logits) + t * p.d_ld;
     float e[VPL];
-    uint32_t key = 0u;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int x = v * 32 + lane;
-      e[v] = (on && x < E) ? load_logit(src + x) : __uint_as_float(0xFF800000u);
-      const uint32_t kv = order_key(e[v]);
-      key = kv > key ? kv : key;
-    }
-    key = __reduce_max_sync(kFullMask, key);
-    if (key <= kKeyClosed) {   // nothing was routed: the row has no part in any output
+    for (int v = 0; v < VPL; ++v) e[v] = next[v];
+    int chosen = lane < k ? p.expert[t * k + lane] : -1;
+    float dw = (lane < k && p.d_weight != nullptr) ? p.d_weight[t * k + lane] : 0.0f;
+    if (t + step < p.tokens)
+      load_row<T, VPL, VEC>(static_cast<const T*>(p.logits) + (t + step) * p.ld, E, lane, routed(t + step), next);
+    float best = e[0];
 #pragma unroll
-      for (int v = 0; v < VPL; ++v)
-        if (v * 32 + lane < E) dst[v * 32 + lane] = static_cast<T>(0.0f);
+    for (int v = 1; v < VPL; ++v) best = max_nan(best, e[v]);
+    const RowExp ex(warp_max_nan(best));
+    if (ex.top == closed_logit()) {   // nothing was routed: the row has no part in any output
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) e[v] = 0.0f;
+      store_row<T, VPL, VEC>(dst, E, lane, e);
       continue;
     }
-    const float top = key == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : key_value(key);
-    int chosen = lane < k ? p.expert[t * k + lane] : -1;
     if (chosen >= E) chosen = -1;
-    float dw = (chosen >= 0 && p.d_weight) ? p.d_weight[t * k + lane] : 0.0f;
-    const float ew = chosen >= 0 ? exp_shifted(load_logit(src + chosen), top) : 0.0f;
-    if (p.normalize) {
-      const float w = ew / warp_sum(ew);
-      dw = w * (dw - warp_sum(w * dw));   // already the gradient of the chosen logits
-    }
+    float ew = 0.0f;
+    if (chosen >= 0) ew = ex.any(logit_value<T>(src[chosen]));
+    else dw = 0.0f;
     float sum = 0.0f, dot = 0.0f;
-    float g[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const int x = v * 32 + lane;
-      e[v] = x < E ? exp_shifted(e[v], top) : 0.0f;
-      g[v] = x < E ? g_shared[x] : 0.0f;
+      e[v] = ex.any(e[v]);
+      if (!ex.plain && Map::expert(v, lane) >= E) e[v] = 0.0f;
       sum += e[v];
       dot = fmaf(e[v], g[v], dot);
     }
     sum = warp_sum(sum);
-    dot = warp_sum(dot);
-    if (!p.normalize) dot += warp_sum(ew * dw);
-    const float inv = 1.0f / sum;
-    dot *= inv;
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) e[v] *= inv;
-    float add[VPL];
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) add[v] = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      const int x = __shfl_sync(kFullMask, chosen, j);
-      const float d = __shfl_sync(kFullMask, dw, j);
-#pragma unroll
-      for (int v = 0; v < VPL; ++v)
-        if (x == v * 32 + lane) add[v] = d;
+    if (p.normalize) {
+      const float w = ew * __fdividef(1.0f, warp_sum(ew));
+      dw = w * (dw - warp_sum(w * dw));   // already the gradient of the chosen logits
+    } else {
+      dot = fmaf(ew, dw, dot);
     }
+    const float inv = __fdividef(1.0f, sum);
+    dot = warp_sum(dot) * inv;
+    if (chosen >= 0) part[chosen] = dw;
+    __syncwarp();
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int x = v * 32 + lane;
-      if (x < E)
-        dst[x] = static_cast<T>(p.normalize ? fmaf(e[v], g[v] - dot, add[v]) : e[v] * (g[v] + add[v] - dot));
+    for (int q = 0; q < VPL / Map::W; ++q) {
+      struct alignas(4 * Map::W) Parts { float v[Map::W]; };
+      const Parts add = *reinterpret_cast<const Parts*>(part + Map::expert(q * Map::W, lane));
+#pragma unroll
+      for (int i = 0; i < Map::W; ++i) {
+        const int v = q * Map::W + i;
+        const float pe = e[v] * inv;
+        e[v] = p.normalize ? fmaf(pe, g[v] - dot, add.v[i]) : pe * (g[v] + add.v[i] - dot);
+      }
+    }
+    __syncwarp();
+    if (chosen >= 0) part[chosen] = 0.0f;
+    __syncwarp();
+    store_row<T, VPL, VEC>(dst, E, lane, e);
+  }
+}
+
+// A thread per row, for up to 32 experts.
+template <typename T, int EM>
+__global__ void __launch_bounds__(kRouteThreads) route_grad_small_kernel(const RouteGradParams p) {
+  __shared__ float g[EM];
+  const int E = p.experts, k = p.top_k;
+  const float scale = grad_scale(p);
+  for (int e = threadIdx.x; e < E; e += blockDim.x) g[e] = static_cast<float>(p.counts[e]) * scale;
+  __syncthreads();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (t >= p.tokens) return;
+  const bool on = p.mask == nullptr || p.mask[t] != 0;
+  const T* src = static_cast<const T*>(p.logits) + t * p.ld;
+  T* dst = static_cast<T*>(p.d_logits) + t * p.d_ld;
+  float x[EM];
+  float top = closed_logit();
+#pragma unroll
+  for (int e = 0; e < EM; ++e) {
+    x[e] = (on && e < E) ? logit_value<T>(src[e]) : closed_logit();
+    top = max_nan(top, x[e]);
+  }
+  const RowExp ex(top);
+  const bool live = top != closed_logit();
+  float sum = 0.0f, dot = 0.0f, chosen_sum = 0.0f, chosen_dot = 0.0f;
+#pragma unroll
+  for (int e = 0; e < EM; ++e) {
+    x[e] = live && e < E ? ex.any(x[e]) : 0.0f;
+    sum += x[e];
+    dot = fmaf(x[e], e < E ? g[e] : 0.0f, dot);
+  }
+  // each chosen expert's dw where that expert's logit is
+  float add[EM];
+  uint32_t taken = 0u;
+#pragma unroll
+  for (int e = 0; e < EM; ++e) add[e] = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    const int c = live ? p.expert[t * k + j] : -1;
+    const float d = (c >= 0 && p.d_weight != nullptr) ? p.d_weight[t * k + j] : 0.0f;
+    if (c >= 0 && c < EM) taken |= 1u << c;
+#pragma unroll
+    for (int e = 0; e < EM; ++e)
+      if (e == c) {
+        add[e] = d;
+        chosen_sum += x[e];
+        chosen_dot = fmaf(x[e], d, chosen_dot);
+      }
+  }
+  const float inv = live ? 1.0f / sum : 0.0f;
+  const float over = (live && taken != 0u) ? 1.0f / chosen_sum : 0.0f;
+  dot = (p.normalize ? dot : dot + chosen_dot) * inv;
+  chosen_dot *= over;
+#pragma unroll
+  for (int e = 0; e < EM; ++e) {
+    if (e < E) {
+      const float pe = x[e] * inv;
+      float d = p.normalize ? pe * (g[e] - dot) : pe * (g[e] + add[e] - dot);
+      if (p.normalize && ((taken >> e) & 1u)) d = fmaf(x[e] * over, add[e] - chosen_dot, d);
+      dst[e] = static_cast<T>(live ? d : 0.0f);
     }
   }
 }
