@@ -29,7 +29,7 @@ def _scales(seed, shape, pow2):
 
 
 def _case(rows, N, K, ab, *, out="f32", dtype="e4m3", dist="int:4", pow2=True, alpha=1.0, bias=False, relu=False, spare=0,
-          seed=0, run=None, **plan_kw):
+          seed=0, run=None, fault=False, **plan_kw):
     """(got, z, absolute sums) of the groups' rows; `spare` rows of capacity past them."""
     br, bk, br_b = (tuple(ab) + (ab[0],))[:3]
     M, G = sum(rows) + spare, len(rows)
@@ -43,10 +43,15 @@ def _case(rows, N, K, ab, *, out="f32", dtype="e4m3", dist="int:4", pow2=True, a
     plan = tst.gemm_grouped_plan_create(G, M, N, K, dtype=dtype, out_dtype=out, alpha=alpha, has_bias=bias, relu=relu, ab_block=ab,
                                         **plan_kw)
     D = torch.full((M, N), float("nan"), dtype=torch.float32 if out == "f32" else torch.bfloat16, device="cuda")
-    for counts in (rows if run is None else run,):
-        tst.gemm_grouped_run(plan, torch.tensor(counts, dtype=torch.int32, device="cuda"), device_codes(A), device_codes(B), D,
-                             bias=None if bv is None else torch.from_numpy(bv).cuda(),
-                             a_block_scales=torch.from_numpy(sA).cuda(), b_block_scales=torch.from_numpy(sB).cuda())
+    counts = torch.tensor(rows if run is None else run, dtype=torch.int32, device="cuda")
+    dA, dB, d_bias = device_codes(A), device_codes(B), None if bv is None else torch.from_numpy(bv).cuda()
+    scales = dict(a_block_scales=torch.from_numpy(sA).cuda(), b_block_scales=torch.from_numpy(sB).cuda())
+    if fault:
+        tst.gemm_plan_set_debug(plan, tst.TST_DEBUG_FAULT_SKIP_LOAD, None, 0, timeout_ns=20_000_000)
+        tst.gemm_grouped_run(plan, counts, dA, dB, D, bias=d_bias, **scales)
+        assert tst.gemm_status_query(plan)[0] == tst.TST_ERR_TIMEOUT
+        tst.gemm_plan_set_debug(plan, 0, None, 0)
+    tst.gemm_grouped_run(plan, counts, dA, dB, D, bias=d_bias, **scales)
     st, word = tst.gemm_status_query(plan)
     a, b = oracle.decode(A, fa), oracle.decode(B, fb)
     z, size = np.zeros((sum(rows), N)), np.zeros((sum(rows), N))
@@ -105,6 +110,46 @@ def test_many_groups_exact():
     rows = [int(v) for v in (synthetic.splitmix64(77, 150) % np.uint64(4))]
     rows[10:60] = [0] * 50
     _exact(rows, 136, 256, (1, 128, 128), seed=8)
+
+
+def test_more_groups_than_the_table_exact():
+    rows = [int(v) for v in (synthetic.splitmix64(78, 600) % np.uint64(3))]
+    _exact(rows, 40, 144, (1, 128, 128), seed=9)
+
+
+# capacities that make the plan take each tile height
+@pytest.mark.parametrize("spare", [0, 100, 400, 2000])
+@pytest.mark.parametrize("ab", [(1, 128, 128), (1, 128, 1), (128, 128)])
+def test_every_tile_height_exact(spare, ab):
+    _exact([5, 0, 17, 1, 33, 2, 70], 264, 784, ab, seed=spare + ab[0], spare=spare)
+
+
+@pytest.mark.parametrize("rows,cap", [([3, 0, 5, 1], 9), ([40, 0, 20, 61], 121), ([300, 1, 0, 513], 900)])
+def test_the_device_walks_the_enumerated_items(rows, cap):
+    N, K, G = 520, 256, len(rows)
+    plan = tst.gemm_grouped_plan_create(G, cap, N, K, dtype="e4m3", ab_block=(1, 128, 128), num_ctas=7)
+    info = tst.gemm_plan_get_info(plan)
+    trace = torch.full((info.grid * info.max_items_per_cta * 8,), -1, dtype=torch.int32, device="cuda")
+    tst.gemm_plan_set_debug(plan, tst.TST_DEBUG_TRACE, trace, trace.numel())
+    z = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    tst.gemm_grouped_run(plan, torch.tensor(rows, dtype=torch.int32, device="cuda"), z(cap, K), z(G * N, K),
+                         torch.empty(cap, N, dtype=torch.bfloat16, device="cuda"), a_block_scales=torch.zeros(cap, 2, device="cuda"),
+                         b_block_scales=torch.zeros(G, 5, 2, device="cuda"))
+    assert tst.gemm_status_query(plan)[0] == tst.TST_OK
+    rec = trace.cpu().numpy().reshape(info.grid, info.max_items_per_cta, 8)
+    for u in range(info.grid):
+        want = tst.gemm_grouped_work_items(plan, rows, u)
+        got = [tuple(r[2:8]) for r in rec[u] if r[0] >= 0]
+        assert got == want, u
+
+
+@pytest.mark.parametrize("cap", [20, 2000])
+def test_a_missing_load_times_out_and_the_plan_recovers(cap):
+    # the producer skips one load (a host-set flag): the issuer's bounded wait runs out, the run
+    # ends with TST_ERR_TIMEOUT, and the next one is right
+    rows, N, K = [4, 0, 9], 200, 512
+    got, z, _, st, _ = _case(rows, N, K, (1, 128, 128), spare=cap - 13, seed=4, fault=True)
+    assert st == tst.TST_OK and np.array_equal(got[:13], z)
 
 
 def test_no_rows_at_all():

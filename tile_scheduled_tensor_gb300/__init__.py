@@ -287,10 +287,17 @@ def _ptr(x):
     raise TypeError(f"expected a CUDA tensor or a device pointer, got {type(x)}")
 
 
+_torch = None   # torch, once a call has needed its current stream
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle: making torch's Stream object costs 2.7 us a call, as much as a kernel launch
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -439,11 +446,10 @@ def _out_of(x, what: str) -> int:
 
 def _matrix(x, what: str, rows=None, cols=None):
     """(pointer, rows, columns, row stride) of a 2-D CUDA tensor whose columns are adjacent."""
-    if not x.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor (no host fallback)")
-    if x.dim() != 2:
-        raise ValueError(f"{what} must have two dimensions, not {x.dim()}")
-    m, n = x.shape
+    shape = x.shape
+    if not x.is_cuda or len(shape) != 2:
+        raise ValueError(f"{what} must be a CUDA tensor of two dimensions (no host fallback)")
+    m, n = shape
     if (rows is not None and m != rows) or (cols is not None and n != cols):
         raise ValueError(f"{what} must be {'any' if rows is None else rows} x {'any' if cols is None else cols}, "
                          f"not {m} x {n}")
@@ -458,15 +464,12 @@ _type_names = {}   # torch dtype -> its name without "torch."
 
 def _array(x, what: str, dtype: str, size: int):
     """Pointer of a contiguous CUDA tensor of `size` elements."""
-    if not x.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor (no host fallback)")
-    name = _type_names.get(x.dtype)
-    if name is None:
+    if _type_names.get(x.dtype) != dtype:
         name = _type_names[x.dtype] = str(x.dtype)[6:]
-    if name != dtype:
-        raise ValueError(f"{what} must hold {dtype}, not {name}")
-    if x.numel() != size or not x.is_contiguous():
-        raise ValueError(f"{what} must hold {size} elements, contiguous")
+        if name != dtype:
+            raise ValueError(f"{what} must hold {dtype}, not {name}")
+    if x.numel() != size or not x.is_contiguous() or not x.is_cuda:
+        raise ValueError(f"{what} must be a contiguous CUDA tensor of {size} elements (no host fallback)")
     return x.data_ptr()
 
 
@@ -512,10 +515,13 @@ def moe_route_backward(plan: MoePlan, logits, expert, counts, totals, d_logits, 
 
 def _whole_rows(x, what: str, cols=None):
     """(pointer, rows, columns) of a contiguous 2-D CUDA tensor."""
-    ptr, m, n, _ = _matrix(x, what, cols=cols)
-    if not x.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return ptr, m, n
+    shape = x.shape
+    if not x.is_cuda or len(shape) != 2 or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA tensor of two dimensions (no host fallback)")
+    m, n = shape
+    if cols is not None and n != cols:
+        raise ValueError(f"{what} must have {cols} columns, not {n}")
+    return x.data_ptr(), m, n
 
 
 def moe_dispatch(plan: MoePlan, x, row, rows, scales=None, stream=None):

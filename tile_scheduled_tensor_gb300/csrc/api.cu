@@ -67,6 +67,8 @@ struct tst_plan {
   int32_t sk_mode = 0;         // tst::SkFixup
   int32_t staging_offset = 0;  // SK_TMA staging buffers in shared memory
   bool bs = false;             // block-scaled FP8 operands (gemm_bs_kernel)
+  int32_t narrow = 0;          // ... grouped, of few rows: rows of a tile of gemm_bs_narrow_kernel
+  int32_t threads = 0;         // threads per CTA
   bool tma_store = false;      // the basic epilogue stores D by TMA from shared staging
   int32_t store_offset = 0;    // ... at this offset of the aligned shared base
   int32_t sk_slots = 1;        // partial slots per split-tile half
@@ -227,6 +229,12 @@ TileChoice choose_tile(int64_t M, int64_t N, int64_t K, int64_t sizeof_ab, int64
   return best;
 }
 
+// Rows per tile of a grouped block-scaled plan whose groups have `rows` rows on average at most: 16, 32
+// or 64 in the narrow kernel, 0 for the 128-row one.
+int32_t narrow_rows(int64_t rows) {
+  return rows <= 12 ? 16 : rows <= 48 ? 32 : 0;
+}
+
 // Hybrid rule: split only the tail wave, and only when it is at most half full.
 int64_t hybrid_split_tiles(int64_t T, int64_t P) {
   const int64_t tail = T % P;
@@ -380,6 +388,8 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
     p->cg = o.cta_group != 0 ? o.cta_group : tc.cg;
   }
   p->bm = tst::kBlockM * p->cg;
+  if (bs && groups > 0 && epi->ab_block_k == 128) p->narrow = narrow_rows(ceil_div(M, groups));
+  if (p->narrow) p->bm = p->narrow;
   // A multicast across two side-by-side single-CTA tiles: the multicast kernel instance
   // covers the basic epilogue of one GEMM with two-atom k-tiles
   if (o.cluster_n < 0 || o.cluster_n > 2) { delete p; return TST_ERR_INVALID_ARG; }
@@ -411,15 +421,22 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
   if (T >= (int64_t(1) << 30) || T * kt >= (int64_t(1) << 62)) { delete p; return TST_ERR_INVALID_ARG; }
   p->stages = tst_kernel_stages(p->bn, p->cg, p->ka);
   if (p->bs) p->stages -= 1;   // the last stage's A slot holds the block-scaled kernel's scale windows
+  // one scale of B per 128-column tile and k-block
+  const bool bs_shared = bs && epi->ab_block_k == 128 && bs_rows_b(*epi) % 128 == 0;
+  const TstNarrow narrow = p->narrow ? tst_bs_narrow(p->narrow, kernel_out(*p), bs_shared) : TstNarrow{};
+  if (p->narrow) p->stages = narrow.stages;
   if (o.stages != 0) {
     if (o.stages < 2 || o.stages > p->stages) { delete p; return TST_ERR_UNSUPPORTED; }
     p->stages = o.stages;
   }
-  p->smem_bytes = tst_kernel_smem_bytes(p->bn, p->cg, p->ka);
+  p->smem_bytes = p->narrow ? narrow.smem_bytes : tst_kernel_smem_bytes(p->bn, p->cg, p->ka);
+  p->threads = p->narrow ? narrow.threads : p->bs ? kBsThreads : tst_kernel_threads(p->bn, p->ka, p->ext_on);
   if (!p->host_only) {
     // the extended epilogue has its own instance (two epilogue warpgroups, typed stores of D)
     const int kdt = dtype == TST_BF16 ? tst::DT_BF16 : tst::DT_E4M3;
-    p->kernel = p->bs       ? tst_bs_kernel(kernel_out(*p), bs_rows_b(*epi) % 32 != 0)
+    p->kernel = p->narrow   ? narrow.kernel
+                : bs_shared ? tst_bs_tile_kernel(kernel_out(*p))
+                : p->bs     ? tst_bs_kernel(kernel_out(*p), bs_rows_b(*epi) % 32 != 0)
                 : p->ext_on ? tst_kernel_ext(kdt, p->bn, p->cg, p->ka)
                             : tst_kernel(kdt, p->bn, kernel_out(*p), p->cg, p->ka, p->mc);
     if (!p->kernel ||
@@ -434,13 +451,13 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
   // scheduling units that can be resident at once: one CTA per SM, or clusters of
   // cg x mc CTAs placed together
   const int csize = p->cg * p->mc;
-  int64_t resident = p->num_sms;
+  int64_t resident = p->narrow ? 2 * p->num_sms : p->num_sms;
   if (csize > 1) {
     resident = p->num_sms / csize;
     if (!p->host_only) {
       cudaLaunchConfig_t qc = {};
       qc.gridDim = dim3(static_cast<unsigned>(csize * resident), 1, 1);
-      qc.blockDim = dim3(tst_kernel_threads(p->bn, p->ka, p->ext_on), 1, 1);
+      qc.blockDim = dim3(p->threads, 1, 1);
       qc.dynamicSmemBytes = static_cast<size_t>(p->smem_bytes);
       cudaLaunchAttribute ca[1];
       ca[0].id = cudaLaunchAttributeClusterDimension;
@@ -868,7 +885,7 @@ tst_status launch(tst_plan* p, const void* A, const void* B, void* C, const tst_
   const int box_k = p->bk / p->ka;
   if (!array_mode && A != p->tm_A) {
     // the multicast instance loads A by one 2-D box per atom (each CTA sends one atom)
-    if (!encode_operand(&p->tmap_a, A, p->dtype, p->M, p->K, box_k, tst::kBlockM, p->box3d && p->mc == 1 ? p->ka : 0))
+    if (!encode_operand(&p->tmap_a, A, p->dtype, p->M, p->K, box_k, p->narrow ? p->narrow : tst::kBlockM, p->box3d && p->mc == 1 ? p->ka : 0))
       return TST_ERR_CUDA;
     p->tm_A = A;
   }
@@ -981,7 +998,7 @@ tst_status launch(tst_plan* p, const void* A, const void* B, void* C, const tst_
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p->sched.grid * p->cg * p->mc), 1, 1);
-  cfg.blockDim = dim3(p->bs ? kBsThreads : tst_kernel_threads(p->bn, p->ka, p->ext_on), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(p->threads), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(p->smem_bytes);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

@@ -40,6 +40,13 @@ constexpr int kBsBuffers = 4;   // k-block partials in TMEM, 128 columns each (t
 constexpr int kBsPairSlots = 2; // partial slots (pairs of buffers)
 constexpr int kBsWarps = 8;     // the accumulating (epilogue) warps, 2-9
 
+struct PlainWalk {
+  const Sched& s;
+  WorkIter it;
+  __device__ __forceinline__ PlainWalk(const Sched& sched, int32_t unit) : s(sched) { work_begin(s, unit, it); }
+  __device__ __forceinline__ bool next(WorkItem& w) { return work_next(s, it, w); }
+};
+
 // MMA issuer r (0 or 1).  The k-blocks of each work item pair up from its first (an odd
 // last one alone); pair q of this CTA (counted over its items) uses slot q & 1, whose two
 // partial buffers are TMEM columns (2 (q & 1) + {0, 1}) * 128.  Both issuers work on every
@@ -53,8 +60,9 @@ constexpr int kBsWarps = 8;     // the accumulating (epilogue) warps, 2-9
 // (below 128-wide k-blocks both issuers read every stage, so the plan's EMPTY barriers then
 // count two commits).  Every other k-block keeps an issuer's FULL waits at most two k-tiles
 // apart, so a ring of two stages keeps them unambiguous.  PB = bk / 32 MMAs per k-block.
-template <int PB>
-__device__ __forceinline__ void run_mma_bs(const KernelParams& p, const Ctx& c, int r, uint32_t tmem_base,
+// walk: the CTA's work list (next(WorkItem&) as work_next).
+template <int PB, typename W>
+__device__ __forceinline__ void run_mma_bs(const KernelParams& p, const Ctx& c, W walk, int r, uint32_t tmem_base,
                                            uint32_t smem_a, uint32_t smem_b, uint32_t bar_full, uint32_t bar_empty,
                                            uint32_t bar_pfull, uint32_t bar_pempty, uint32_t bar_drain) {
   using Cfg = TileCfg<128, 1, 1>;
@@ -71,10 +79,8 @@ __device__ __forceinline__ void run_mma_bs(const KernelParams& p, const Ctx& c, 
   bool ok = true;
   long long wait_full = 0, wait_pempty = 0, kblocks = 0;   // role-cycle counters (debug)
   const bool stats = p.stats != nullptr && r == 0;
-  WorkIter it;
-  work_begin(p.sched, c.unit, it);
   WorkItem w;
-  while (ok && work_next(p.sched, it, w)) {
+  while (ok && walk.next(w)) {
     const int nkb = w.k_count * PER_ATOM;
     const int npairs = (nkb + 1) >> 1;
     // this issuer's k-blocks of the item: j = first, first + 2, ...
@@ -371,12 +377,13 @@ __global__ void __launch_bounds__(kBsThreads, 1) gemm_bs_kernel(const __grid_con
   } else if (warp == 1 || warp == 10) {
     if (lane == 0) {
       const int r = warp == 1 ? 0 : 1;
+      const PlainWalk walk(p.sched, c.unit);
       if (p.bs_k == 32)
-        run_mma_bs<1>(p, c, r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
+        run_mma_bs<1>(p, c, walk, r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
       else if (p.bs_k == 64)
-        run_mma_bs<2>(p, c, r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
+        run_mma_bs<2>(p, c, walk, r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
       else
-        run_mma_bs<4>(p, c, r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
+        run_mma_bs<4>(p, c, walk, r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
     }
   } else {
     run_epilogue_bs<OUT, PER_COL>(p, c, tmem_base, bar_pfull, bar_pempty, ptx::smem_addr(win),

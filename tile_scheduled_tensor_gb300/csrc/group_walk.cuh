@@ -1,0 +1,119 @@
+// The work list of a grouped GEMM from a table in shared memory.
+//
+// work_next (tile_sched.h) finds the group of the next tile by reading the groups' row counts
+// from global memory one after another, in 64-bit sums: 2000 to 2900 cycles per tile in a warp of
+// a block-scaled kernel, whose whole tile takes 15000.  Here each CTA first sums the counts
+// into a table of every group's first tile, first row and rows, once, and each role finds the next tile's
+// group in it by comparisons.  The items are those of work_next.  A plan whose groups do not fit the table, or
+// that is not grouped, walks with work_next.
+#pragma once
+#include <stdint.h>
+
+#include "kernel_params.h"
+#include "tile_sched.h"
+
+namespace tst {
+
+constexpr int kWalkGroups = 512;   // groups that a table holds
+constexpr int kWalkBytes = (3 * kWalkGroups + 4) * 4;
+
+struct GroupTable {
+  int32_t* tile0;   // groups + 1: first linear tile of each group, then all tiles
+  int32_t* row0;    // groups: first row, at most INT32_MAX
+  int32_t* rows;    // groups
+  __device__ __forceinline__ explicit GroupTable(void* base)
+      : tile0(static_cast<int32_t*>(base)), row0(tile0 + kWalkGroups + 1), rows(row0 + kWalkGroups) {}
+};
+
+__device__ __forceinline__ bool walk_by_table(const Sched& s) {
+  return s.groups > 0 && s.groups <= kWalkGroups && s.group_shapes == nullptr;
+}
+
+// One whole warp fills the table; the CTA's barrier makes it visible.
+__device__ __forceinline__ void fill_group_table(const Sched& s, const GroupTable& t) {
+  const int lane = threadIdx.x & 31;
+  constexpr int64_t most = 0x7FFFFFFF, most_tiles = int64_t(1) << 30;
+  int64_t tiles = 0, row = 0;
+  for (int32_t b = 0; b < s.groups; b += 32) {
+    const int32_t g = b + lane;
+    const int64_t r = g < s.groups ? group_row_count(s, g) : 0;
+    const int64_t n = g < s.groups ? group_tile_count(s, g, r) : 0;
+    int64_t sum_n = n, sum_r = r;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t on = __shfl_up_sync(0xFFFFFFFFu, sum_n, d);
+      const int64_t orow = __shfl_up_sync(0xFFFFFFFFu, sum_r, d);
+      if (lane >= d) { sum_n += on; sum_r += orow; }
+    }
+    if (g < s.groups) {
+      const int64_t first = tiles + sum_n - n, first_row = row + sum_r - r;
+      t.tile0[g] = static_cast<int32_t>(first < most_tiles ? first : most_tiles);
+      t.row0[g] = static_cast<int32_t>(first_row < most ? first_row : most);
+      t.rows[g] = static_cast<int32_t>(r);
+    }
+    tiles += __shfl_sync(0xFFFFFFFFu, sum_n, 31);
+    row += __shfl_sync(0xFFFFFFFFu, sum_r, 31);
+  }
+  if (lane == 0) t.tile0[s.groups] = static_cast<int32_t>(tiles < most_tiles ? tiles : most_tiles);
+}
+
+// A role's walk, by one thread or (next_warp) by a converged warp.
+struct Walk {
+  const Sched& s;
+  GroupTable t;
+  bool table;
+  int32_t at, g;   // table: the next linear tile, the current group
+  WorkIter it;
+  __device__ __forceinline__ Walk(const Sched& sched, const GroupTable& tab, int32_t unit)
+      : s(sched), t(tab), table(walk_by_table(sched)), at(unit), g(0) {
+    if (!table) work_begin(s, unit, it);
+  }
+  __device__ __forceinline__ void item(WorkItem& w) {
+    const int32_t rows = t.rows[g];
+    Sched sg;
+    sg.map_kind = s.map_kind;
+    sg.mt = (rows + s.bm - 1) / s.bm;
+    sg.nt = s.nt;
+    sg.group = s.group;
+    sg.order = nullptr;
+    w.tile = at;
+    tile_coord(sg, at - t.tile0[g], w.m, w.n);
+    w.k_begin = 0;
+    w.k_count = s.kt;
+    w.flags = ITEM_FINAL;
+    w.group = g;
+    w.col0 = w.n * s.bn;
+    w.col_end = s.cols;
+    const int64_t row0 = static_cast<int64_t>(t.row0[g]) + static_cast<int64_t>(w.m) * s.bm;
+    const int64_t end = static_cast<int64_t>(t.row0[g]) + rows;
+    if (end > s.rows) w.flags |= ITEM_CLAMPED;
+    w.row0 = static_cast<int32_t>(row0 < s.rows ? row0 : s.rows);
+    w.row_end = static_cast<int32_t>(end < s.rows ? end : s.rows);
+    w.b_row0 = g * s.group_b_rows + w.col0;
+    at += s.grid;
+  }
+  __device__ __forceinline__ bool next(WorkItem& w) {
+    if (!table) return work_next(s, it, w);
+    if (at >= t.tile0[s.groups]) return false;
+    while (at >= t.tile0[g + 1]) ++g;
+    item(w);
+    return true;
+  }
+  __device__ __forceinline__ bool next_warp(WorkItem& w) {
+    if (!table) return work_next_warp(s, it, w);
+    if (at >= t.tile0[s.groups]) return false;
+    const int lane = threadIdx.x & 31;
+    for (;; g += 32) {
+      const int32_t e = g + 1 + lane;
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, e <= s.groups && t.tile0[e] > at);
+      if (past != 0u) {
+        g += __ffs(past) - 1;
+        break;
+      }
+    }
+    item(w);
+    return true;
+  }
+};
+
+}  // namespace tst

@@ -289,6 +289,19 @@ const void* tst_reduce_kernel(int out_type);
 constexpr int kBsThreads = 352;
 const void* tst_bs_kernel(int out_type, bool per_col);
 
+// The form for one scale of B per tile and k-block (gemm_bst.cu): k-blocks of 128, B's scale
+// tiles a multiple of 128 rows high; tile, ring and threads as above.
+const void* tst_bs_tile_kernel(int out_type);
+
+// The narrow form for groups of few rows (gemm_bsn.cu): 128 columns of D by `rows` = 16, 32 or 64
+// rows of a group per tile, k-blocks of 128, two CTAs per SM.  shared: as the form above.
+constexpr int kBsNarrowThreads = 192;
+struct TstNarrow {
+  const void* kernel;
+  int stages, smem_bytes, threads;
+};
+TstNarrow tst_bs_narrow(int rows, int out_type, bool shared);
+
 inline int tst_kernel_threads(int bn, int ka, bool ext = false) {
   return ((bn == 128 && ka == 2) ? tst::kThreadsDual : tst::kThreads) + (ext ? 128 : 0);
 }
