@@ -388,7 +388,7 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
     p->cg = o.cta_group != 0 ? o.cta_group : tc.cg;
   }
   p->bm = tst::kBlockM * p->cg;
-  if (bs && groups > 0 && epi->ab_block_k == 128) p->narrow = narrow_rows(ceil_div(M, groups));
+  if (bs && groups > 0 && groups <= kBsWalkGroups && epi->ab_block_k == 128) p->narrow = narrow_rows(ceil_div(M, groups));
   if (p->narrow) p->bm = p->narrow;
   // A multicast across two side-by-side single-CTA tiles: the multicast kernel instance
   // covers the basic epilogue of one GEMM with two-atom k-tiles
@@ -422,7 +422,7 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
   p->stages = tst_kernel_stages(p->bn, p->cg, p->ka);
   if (p->bs) p->stages -= 1;   // the last stage's A slot holds the block-scaled kernel's scale windows
   // one scale of B per 128-column tile and k-block
-  const bool bs_shared = bs && epi->ab_block_k == 128 && bs_rows_b(*epi) % 128 == 0;
+  const bool bs_shared = bs && groups <= kBsWalkGroups && epi->ab_block_k == 128 && bs_rows_b(*epi) % 128 == 0;
   const TstNarrow narrow = p->narrow ? tst_bs_narrow(p->narrow, kernel_out(*p), bs_shared) : TstNarrow{};
   if (p->narrow) p->stages = narrow.stages;
   if (o.stages != 0) {
@@ -430,7 +430,7 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
     p->stages = o.stages;
   }
   p->smem_bytes = p->narrow ? narrow.smem_bytes : tst_kernel_smem_bytes(p->bn, p->cg, p->ka);
-  p->threads = p->narrow ? narrow.threads : p->bs ? kBsThreads : tst_kernel_threads(p->bn, p->ka, p->ext_on);
+  p->threads = p->narrow ? narrow.threads : bs_shared ? kBsTileThreads : p->bs ? kBsThreads : tst_kernel_threads(p->bn, p->ka, p->ext_on);
   if (!p->host_only) {
     // the extended epilogue has its own instance (two epilogue warpgroups, typed stores of D)
     const int kdt = dtype == TST_BF16 ? tst::DT_BF16 : tst::DT_E4M3;

@@ -44,7 +44,12 @@ struct PlainWalk {
   const Sched& s;
   WorkIter it;
   __device__ __forceinline__ PlainWalk(const Sched& sched, int32_t unit) : s(sched) { work_begin(s, unit, it); }
-  __device__ __forceinline__ bool next(WorkItem& w) { return work_next(s, it, w); }
+  __device__ __forceinline__ bool next(int32_t& k_count) {
+    WorkItem w;
+    const bool more = work_next(s, it, w);
+    k_count = more ? w.k_count : 0;
+    return more;
+  }
 };
 
 // MMA issuer r (0 or 1).  The k-blocks of each work item pair up from its first (an odd
@@ -60,7 +65,7 @@ struct PlainWalk {
 // (below 128-wide k-blocks both issuers read every stage, so the plan's EMPTY barriers then
 // count two commits).  Every other k-block keeps an issuer's FULL waits at most two k-tiles
 // apart, so a ring of two stages keeps them unambiguous.  PB = bk / 32 MMAs per k-block.
-// walk: the CTA's work list (next(WorkItem&) as work_next).
+// walk: the CTA's work list; next(k) tells whether there is another item and its k-tiles.
 template <int PB, typename W>
 __device__ __forceinline__ void run_mma_bs(const KernelParams& p, const Ctx& c, W walk, int r, uint32_t tmem_base,
                                            uint32_t smem_a, uint32_t smem_b, uint32_t bar_full, uint32_t bar_empty,
@@ -79,9 +84,9 @@ __device__ __forceinline__ void run_mma_bs(const KernelParams& p, const Ctx& c, 
   bool ok = true;
   long long wait_full = 0, wait_pempty = 0, kblocks = 0;   // role-cycle counters (debug)
   const bool stats = p.stats != nullptr && r == 0;
-  WorkItem w;
-  while (ok && walk.next(w)) {
-    const int nkb = w.k_count * PER_ATOM;
+  int32_t k_count = 0;
+  while (ok && walk.next(k_count)) {
+    const int nkb = k_count * PER_ATOM;
     const int npairs = (nkb + 1) >> 1;
     // this issuer's k-blocks of the item: j = first, first + 2, ...
     const int first = static_cast<int>((kb0 + static_cast<uint32_t>(r)) & 1u);
@@ -124,7 +129,7 @@ __device__ __forceinline__ void run_mma_bs(const KernelParams& p, const Ctx& c, 
     }
     q0 += static_cast<uint32_t>(npairs);
     kb0 += static_cast<uint32_t>(nkb);
-    kt_item += w.k_count;
+    kt_item += k_count;
   }
   if (stats) {
     p.stats[blockIdx.x * kStatSlots + STAT_MMA_WAIT_FULL] = wait_full;

@@ -58,9 +58,9 @@ __device__ __forceinline__ void narrow_mma(const KernelParams& p, const Ctx& c, 
   uint32_t phase = 0, buf_phase = 0;
   bool ok = true;
   long long wait_full = 0, wait_pempty = 0, kblocks = 0;
-  WorkItem w;
+  Tile w;
   while (ok && walk.next(w)) {
-    for (int32_t kb = 0; kb < w.k_count; ++kb) {
+    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
       const long long t0 = p.stats ? clock64() : 0;
       if (!wait_phase<1>(p, c, bar_pempty + 8 * buf, buf_phase ^ 1u, ROLE_MMA)) { ok = false; break; }
       const long long t1 = p.stats ? clock64() : 0;
@@ -127,7 +127,8 @@ __device__ __forceinline__ void narrow_epilogue(const KernelParams& p, const Ctx
   // table entry i of this thread: row (e + i EP_THREADS) / 8 of the tile, k-block of the window % 8
   const int entry_kb = e % kBsWindow;
   float na[PER], nb[SHARED ? 1 : kBsWindow];           // the next window's scales
-  auto load_window = [&](const WorkItem& w, int32_t kb0) {
+  const int32_t nkb = p.sched.kt;
+  auto load_window = [&](const Tile& w, int32_t kb0) {
     const int32_t last = p.bs_kblocks - 1;             // k-blocks past K are not folded
     const int32_t kb = kb0 + entry_kb < last ? kb0 + entry_kb : last;
 #pragma unroll
@@ -138,15 +139,15 @@ __device__ __forceinline__ void narrow_epilogue(const KernelParams& p, const Ctx
     }
     const int64_t first = static_cast<int64_t>(w.group) * p.bs_group_rows;
     if constexpr (SHARED) {
-      nb[0] = __ldg(p.bs_b + (first + w.col0 / p.bs_rows_b) * p.bs_kblocks + kb);
+      nb[0] = __ldg(p.bs_b + (first + w.n * 128 / p.bs_rows_b) * p.bs_kblocks + kb);
     } else {
-      const int32_t col = w.col0 + col_in_tile < p.N ? w.col0 + col_in_tile : p.N - 1;
+      const int32_t at = w.n * 128 + col_in_tile, col = at < p.N ? at : p.N - 1;
       const float* sb = p.bs_b + (first + col / p.bs_rows_b) * p.bs_kblocks;
 #pragma unroll
       for (int i = 0; i < kBsWindow; ++i) nb[i] = __ldg(sb + (kb0 + i < last ? kb0 + i : last));
     }
   };
-  WorkItem w, wn;
+  Tile w, wn;
   // every warp walks the same items and windows and meets the same barriers, after a failed wait too
   bool have = walk.next_warp(w);
   uint32_t g = 0;   // windows begun so far: window g uses table g & 1
@@ -156,7 +157,7 @@ __device__ __forceinline__ void narrow_epilogue(const KernelParams& p, const Ctx
     float r[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) r[j] = 0.0f;
-    for (int kb = 0; kb < w.k_count; kb += kBsWindow, ++g) {
+    for (int kb = 0; kb < nkb; kb += kBsWindow, ++g) {
       float* win = win_ptr + (g & 1u) * (Cfg::WINDOW_BYTES / 4);
 #pragma unroll
       for (int i = 0; i < PER; ++i)
@@ -167,11 +168,11 @@ __device__ __forceinline__ void narrow_epilogue(const KernelParams& p, const Ctx
         for (int i = 0; i < kBsWindow; ++i) sb[i] = nb[i];
       }
       ptx::named_bar_sync(kBsBarrier, EP_THREADS);   // table g is in place; table g - 1 is read
-      if (kb + kBsWindow < w.k_count) load_window(w, kb + kBsWindow);
+      if (kb + kBsWindow < nkb) load_window(w, kb + kBsWindow);
       else if (have_next) load_window(wn, 0);
 #pragma unroll(SHARED ? 1 : kBsWindow)
       for (int j = 0; j < kBsWindow; ++j) {
-        if (ok && kb + j < w.k_count) {
+        if (ok && kb + j < nkb) {
           const long long t0 = stat_thread ? clock64() : 0;
           ok = wait_phase_warp(p, c, bar_pfull + 8 * buf, buf_phase, ROLE_EPILOGUE);
           if (ok) {
@@ -201,8 +202,8 @@ __device__ __forceinline__ void narrow_epilogue(const KernelParams& p, const Ctx
         }
       }
     }
-    const int32_t col = w.col0 + col_in_tile;
-    if (ok && col < w.col_end) {
+    const int32_t col = w.n * 128 + col_in_tile;
+    if (ok && col < p.N) {
       // the basic epilogue: alpha, column bias, ReLU, cast; a warp stores 32 adjacent columns of each row
       const float b = p.has_bias ? __ldg(p.bias + col) : 0.0f;
 #pragma unroll
@@ -211,7 +212,7 @@ __device__ __forceinline__ void narrow_epilogue(const KernelParams& p, const Ctx
         if (row >= w.row_end) break;
         float z = fmaf(alpha, r[i], b);
         if (p.relu) z = fmaxf(z, 0.0f);
-        const int64_t at = static_cast<int64_t>(row) * w.col_end + col;
+        const int64_t at = static_cast<int64_t>(row) * p.N + col;
         if (OUT == OUT_BF16) reinterpret_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(z);
         else reinterpret_cast<float*>(p.C)[at] = z;
       }
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kBsNarrowThreads, 2) gemm_bs_narrow_kernel(con
     ptx::tmem_relinquish();
   }
   const GroupTable table(smem + Cfg::WALK_OFFSET);
-  if (warp == 2 && walk_by_table(p.sched)) fill_group_table(p.sched, table);
+  if (warp == 2) fill_group_table(p.sched, table);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();

@@ -1,11 +1,12 @@
-// The work list of a grouped GEMM from a table in shared memory.
+// The work list of the block-scaled kernels' persistent CTAs, light enough for registers: the next
+// tile and, grouped, its group, found in a table in shared memory.
 //
 // work_next (tile_sched.h) finds the group of the next tile by reading the groups' row counts
 // from global memory one after another, in 64-bit sums: 2000 to 2900 cycles per tile in a warp of
-// a block-scaled kernel, whose whole tile takes 15000.  Here each CTA first sums the counts
-// into a table of every group's first tile, first row and rows, once, and each role finds the next tile's
-// group in it by comparisons.  The items are those of work_next.  A plan whose groups do not fit the table, or
-// that is not grouped, walks with work_next.
+// a block-scaled kernel, whose whole tile takes 15000.  Here each CTA first sums the counts into a
+// table of every group's first tile, first row and rows, once, and each role finds the next tile's
+// group in it by comparisons.  The items are those of work_next for whole tiles (static, persistent
+// or grouped with shared N and K, at most kWalkGroups groups).
 #pragma once
 #include <stdint.h>
 
@@ -14,7 +15,7 @@
 
 namespace tst {
 
-constexpr int kWalkGroups = 512;   // groups that a table holds
+constexpr int kWalkGroups = kBsWalkGroups;   // groups that a table holds
 constexpr int kWalkBytes = (3 * kWalkGroups + 4) * 4;
 
 struct GroupTable {
@@ -24,10 +25,6 @@ struct GroupTable {
   __device__ __forceinline__ explicit GroupTable(void* base)
       : tile0(static_cast<int32_t*>(base)), row0(tile0 + kWalkGroups + 1), rows(row0 + kWalkGroups) {}
 };
-
-__device__ __forceinline__ bool walk_by_table(const Sched& s) {
-  return s.groups > 0 && s.groups <= kWalkGroups && s.group_shapes == nullptr;
-}
 
 // One whole warp fills the table; the CTA's barrier makes it visible.
 __device__ __forceinline__ void fill_group_table(const Sched& s, const GroupTable& t) {
@@ -57,61 +54,72 @@ __device__ __forceinline__ void fill_group_table(const Sched& s, const GroupTabl
   if (lane == 0) t.tile0[s.groups] = static_cast<int32_t>(tiles < most_tiles ? tiles : most_tiles);
 }
 
-// A role's walk, by one thread or (next_warp) by a converged warp.
+// What a tile needs of its work item (every tile takes the whole K, and N columns are the output's).
+struct Tile {
+  int32_t index, m, n;   // linear tile, its place in the group's grid
+  int32_t group;
+  int32_t row0, row_end; // first row in A and the output; rows from row_end on are not the tile's
+  bool clamped;          // the group's rows end past the matrix
+};
+
+// A role's walk, by one thread (next) or by a converged warp (next_warp).
 struct Walk {
   const Sched& s;
   GroupTable t;
-  bool table;
-  int32_t at, g;   // table: the next linear tile, the current group
-  WorkIter it;
-  __device__ __forceinline__ Walk(const Sched& sched, const GroupTable& tab, int32_t unit)
-      : s(sched), t(tab), table(walk_by_table(sched)), at(unit), g(0) {
-    if (!table) work_begin(s, unit, it);
-  }
-  __device__ __forceinline__ void item(WorkItem& w) {
-    const int32_t rows = t.rows[g];
-    Sched sg;
-    sg.map_kind = s.map_kind;
-    sg.mt = (rows + s.bm - 1) / s.bm;
-    sg.nt = s.nt;
-    sg.group = s.group;
-    sg.order = nullptr;
-    w.tile = at;
-    tile_coord(sg, at - t.tile0[g], w.m, w.n);
-    w.k_begin = 0;
-    w.k_count = s.kt;
-    w.flags = ITEM_FINAL;
+  int32_t at, g;   // the next linear tile, the current group
+  __device__ __forceinline__ Walk(const Sched& sched, const GroupTable& table, int32_t unit)
+      : s(sched), t(table), at(unit), g(0) {}
+  __device__ __forceinline__ void take(Tile& w) {
+    w.index = at;
     w.group = g;
-    w.col0 = w.n * s.bn;
-    w.col_end = s.cols;
-    const int64_t row0 = static_cast<int64_t>(t.row0[g]) + static_cast<int64_t>(w.m) * s.bm;
-    const int64_t end = static_cast<int64_t>(t.row0[g]) + rows;
-    if (end > s.rows) w.flags |= ITEM_CLAMPED;
-    w.row0 = static_cast<int32_t>(row0 < s.rows ? row0 : s.rows);
-    w.row_end = static_cast<int32_t>(end < s.rows ? end : s.rows);
-    w.b_row0 = g * s.group_b_rows + w.col0;
+    if (s.groups == 0) {
+      tile_coord(s, at, w.m, w.n);
+      w.row0 = w.m * s.bm;
+      w.row_end = s.rows;
+      w.clamped = false;
+    } else {
+      const int32_t rows = t.rows[g];
+      Sched sg;
+      sg.map_kind = s.map_kind;
+      sg.mt = (rows + s.bm - 1) / s.bm;
+      sg.nt = s.nt;
+      sg.group = s.group;
+      sg.order = nullptr;
+      tile_coord(sg, at - t.tile0[g], w.m, w.n);
+      const int64_t row0 = static_cast<int64_t>(t.row0[g]) + static_cast<int64_t>(w.m) * s.bm;
+      const int64_t end = static_cast<int64_t>(t.row0[g]) + rows;
+      w.clamped = end > s.rows;
+      w.row0 = static_cast<int32_t>(row0 < s.rows ? row0 : s.rows);
+      w.row_end = static_cast<int32_t>(end < s.rows ? end : s.rows);
+    }
     at += s.grid;
   }
-  __device__ __forceinline__ bool next(WorkItem& w) {
-    if (!table) return work_next(s, it, w);
-    if (at >= t.tile0[s.groups]) return false;
-    while (at >= t.tile0[g + 1]) ++g;
-    item(w);
+  __device__ __forceinline__ bool next(Tile& w) {
+    if (s.groups == 0) {
+      if (at >= s.dp_tiles) return false;
+    } else {
+      if (at >= t.tile0[s.groups]) return false;
+      while (at >= t.tile0[g + 1]) ++g;
+    }
+    take(w);
     return true;
   }
-  __device__ __forceinline__ bool next_warp(WorkItem& w) {
-    if (!table) return work_next_warp(s, it, w);
-    if (at >= t.tile0[s.groups]) return false;
-    const int lane = threadIdx.x & 31;
-    for (;; g += 32) {
-      const int32_t e = g + 1 + lane;
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, e <= s.groups && t.tile0[e] > at);
-      if (past != 0u) {
-        g += __ffs(past) - 1;
-        break;
+  __device__ __forceinline__ bool next_warp(Tile& w) {
+    if (s.groups == 0) {
+      if (at >= s.dp_tiles) return false;
+    } else {
+      if (at >= t.tile0[s.groups]) return false;
+      const int lane = threadIdx.x & 31;
+      for (;; g += 32) {
+        const int32_t e = g + 1 + lane;
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, e <= s.groups && t.tile0[e] > at);
+        if (past != 0u) {
+          g += __ffs(past) - 1;
+          break;
+        }
       }
     }
-    item(w);
+    take(w);
     return true;
   }
 };

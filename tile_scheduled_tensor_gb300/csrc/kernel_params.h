@@ -290,7 +290,10 @@ constexpr int kBsThreads = 352;
 const void* tst_bs_kernel(int out_type, bool per_col);
 
 // The form for one scale of B per tile and k-block (gemm_bst.cu): k-blocks of 128, B's scale
-// tiles a multiple of 128 rows high; tile, ring and threads as above.
+// tiles a multiple of 128 rows high; tile and ring as above, a warpgroup of single-thread roles
+// and two that accumulate.
+constexpr int kBsTileThreads = 384;
+constexpr int kBsWalkGroups = 512;   // most groups of a grouped plan in this form and the next
 const void* tst_bs_tile_kernel(int out_type);
 
 // The narrow form for groups of few rows (gemm_bsn.cu): 128 columns of D by `rows` = 16, 32 or 64
