@@ -202,10 +202,16 @@ typedef struct {
                             epilogue warps add (sA * sB) * partial in FP32 (the page's section
                             15.3 multi-stage accumulation).  Needs FP8 operands, FP32 or BF16 D,
                             alpha / tensor-wise scales / column bias / ReLU only, the static or
-                            persistent schedule, single CTAs with 128-column tiles and one-atom
-                            k-tiles (bn, cta_group, bk 0 or those values), stages 0 or 2 to 6
-                            (the ring's seventh stage holds the staged scales); else
-                            TST_ERR_UNSUPPORTED. */
+                            persistent schedule or a grouped plan whose groups share N and K (each
+                            group's B then has its own ceil(N / br_b) x ceil(K / bk) scales, one
+                            group after another; A's tiles are those of the whole M x K), single CTAs
+                            with 128-column tiles (256 too when bk is 128 and br_b a multiple of
+                            128) and one-atom k-tiles (bn, cta_group, bk 0 or those values), stages
+                            0 or 2 to the form's most (6; 4 with 256 columns, 5 in the narrow form);
+                            else TST_ERR_UNSUPPORTED.  A grouped plan of at most 512 groups with bn 0
+                            and k-blocks of 128 chooses its form by its sizes: tiles of 16 or 32 rows
+                            (bm in tst_plan_info) by 128 columns for at most 48 rows per group on
+                            average, else 128 rows by 128 or 256 columns. */
     int32_t ab_block_k;
     int32_t ab_block_rows_b; /* rows of B's scale tiles (0: ab_block_rows; else >= 1) */
 } tst_epilogue_ex;

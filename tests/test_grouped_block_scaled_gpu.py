@@ -124,6 +124,22 @@ def test_every_tile_height_exact(spare, ab):
     _exact([5, 0, 17, 1, 33, 2, 70], 264, 784, ab, seed=spare + ab[0], spare=spare)
 
 
+# wide tiles: asked for, ragged in N and K, with short last row tiles, odd k-block counts and two stages
+@pytest.mark.parametrize("N,K,kw", [(256, 128, {}), (300, 400, {}), (1416, 2064, {}), (520, 640, dict(stages=2, num_ctas=5)),
+                                    (100, 272, {}), (770, 1152, dict(num_ctas=2))])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_wide_tiles_exact(N, K, kw, out):
+    _exact([300, 0, 1, 130, 33, 256], N, K, (1, 128, 128), out, bn=256, alpha=0.5, bias=True, relu=out == "bf16", seed=N, spare=3,
+           **kw)
+
+
+def test_plans_choose_wide_tiles_for_many_rows():
+    big = tst.gemm_grouped_plan_create(16, 16384, 4096, 512, dtype="e4m3", ab_block=(1, 128, 128))
+    assert tst.gemm_plan_get_info(big).bn == 256
+    got, z, size, st, _ = _case([1500, 0, 900, 1696], 4096, 384, (1, 128, 128), out="bf16", seed=2)
+    assert st == tst.TST_OK and np.array_equal(got, oracle.decode(oracle.round_bf16(z), "bf16"))
+
+
 @pytest.mark.parametrize("rows,cap", [([3, 0, 5, 1], 9), ([40, 0, 20, 61], 121), ([300, 1, 0, 513], 900)])
 def test_the_device_walks_the_enumerated_items(rows, cap):
     N, K, G = 520, 256, len(rows)

@@ -104,8 +104,18 @@ def test_row_refusals():
 def test_grouped_block_scaled_plan_rules():
     kw = dict(dtype="e4m3", host_only=True, num_sms=152)
     p = tst.gemm_grouped_plan_create(8, 1000, 512, 1024, ab_block=(1, 128, 128), **kw)
-    assert (p.info.bn, p.info.cta_group, p.info.bk, p.info.tma_store) == (128, 1, 128, 0)
-    for bad, status in ((dict(dtype="bf16"), tst.TST_ERR_UNSUPPORTED), (dict(bn=256), tst.TST_ERR_UNSUPPORTED),
+    assert (p.info.bm, p.info.bn, p.info.cta_group, p.info.bk, p.info.tma_store) == (128, 128, 1, 128, 0)
+    # the form by the sizes: few rows per group, many, or k-blocks that only the general form has
+    for G, M, N, ab, bn, form in ((32, 64, 4096, (1, 128, 128), 0, (16, 128)), (32, 1024, 4096, (1, 128, 128), 0, (32, 128)),
+                                  (32, 1024, 4096, (1, 128, 1), 0, (32, 128)), (16, 16384, 4096, (1, 128, 128), 0, (128, 256)),
+                                  (16, 16384, 4096, (1, 128, 64), 0, (128, 128)), (16, 16384, 100, (1, 128, 128), 0, (128, 128)),
+                                  (32, 64, 4096, (1, 64, 128), 0, (128, 128)), (600, 600, 4096, (1, 128, 128), 0, (128, 128)),
+                                  (32, 64, 4096, (1, 128, 128), 128, (128, 128)), (4, 64, 4096, (1, 128, 128), 256, (128, 256))):
+        info = tst.gemm_grouped_plan_create(G, M, N, 1024, ab_block=ab, bn=bn, **kw).info
+        assert (info.bm, info.bn) == form, (G, M, N, ab, bn)
+    assert tst.gemm_plan_create(1000, 1000, 1024, schedule="persistent", ab_block=(1, 128, 128), bn=256, **kw).info.bn == 256
+    for bad, status in ((dict(dtype="bf16"), tst.TST_ERR_UNSUPPORTED), (dict(bn=512), tst.TST_ERR_UNSUPPORTED),
+                        (dict(bn=256, ab_block=(1, 128, 64)), tst.TST_ERR_UNSUPPORTED), (dict(stages=7), tst.TST_ERR_UNSUPPORTED),
                         (dict(cta_group=2), tst.TST_ERR_UNSUPPORTED), (dict(activation="gelu"), tst.TST_ERR_UNSUPPORTED),
                         (dict(out_dtype="e4m3"), tst.TST_ERR_UNSUPPORTED), (dict(ab_block=(1, 100)), tst.TST_ERR_INVALID_ARG)):
         with pytest.raises(tst.TstError) as e:

@@ -229,11 +229,11 @@ TileChoice choose_tile(int64_t M, int64_t N, int64_t K, int64_t sizeof_ab, int64
   return best;
 }
 
-// Rows per tile of a grouped block-scaled plan whose groups have `rows` rows on average at most: 16, 32
-// or 64 in the narrow kernel, 0 for the 128-row one.
-int32_t narrow_rows(int64_t rows) {
-  return rows <= 12 ? 16 : rows <= 48 ? 32 : 0;
-}
+// Rows per tile of a grouped block-scaled plan whose groups have `rows` rows on average at most: 16
+// or 32 in the narrow kernel, 0 for the 128-row ones.  Measured on 32 experts of 4096 x 4096 with
+// shares falling as 1 / sqrt(rank): 8 rows on average 86 us at 16 and 86 at 32, 16 rows 89 and 88,
+// 32 rows 105 and 90; 64 rows 120 at 32 and 101 on 128-row tiles.
+int32_t narrow_rows(int64_t rows) { return rows <= 12 ? 16 : rows <= 48 ? 32 : 0; }
 
 // Hybrid rule: split only the tail wave, and only when it is at most half full.
 int64_t hybrid_split_tiles(int64_t T, int64_t P) {
@@ -320,14 +320,18 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
   // block-scaled FP8 operands: their own kernel, single CTAs with 128 x 128 tiles and one-atom
   // k-tiles, the basic epilogue, whole tiles (static, persistent, or grouped with shared N and K)
   const bool bs = epi->ab_block_k != 0;
+  // ... with one scale of B per 128 columns and k-block
+  const bool bs_shared = bs && groups <= kBsWalkGroups && epi->ab_block_k == 128 && bs_rows_b(*epi) % 128 == 0;
+  bool bs_auto = false;   // the plan chooses the tile
   if (bs) {
     if (epi->ab_block_k != 32 && epi->ab_block_k != 64 && epi->ab_block_k != 128) return TST_ERR_INVALID_ARG;
     if (epi->ab_block_rows < 1 || epi->ab_block_rows_b < 0) return TST_ERR_INVALID_ARG;
     if (dtype == TST_BF16 || needs_ext(*epi) || shapes != nullptr || (schedule != TST_STATIC && schedule != TST_PERSISTENT) ||
-        (o.bn != 0 && o.bn != 128) || (o.cta_group != 0 && o.cta_group != 1) || (o.bk != 0 && o.bk != 128) ||
+        (o.bn != 0 && o.bn != 128 && !(o.bn == 256 && bs_shared)) || (o.cta_group != 0 && o.cta_group != 1) || (o.bk != 0 && o.bk != 128) ||
         o.cluster_n == 2 || o.pdl || o.epilogue_store == TST_STORE_TMA || o.l2_prefetch)
       return TST_ERR_UNSUPPORTED;
-    o.bn = 128;
+    bs_auto = o.bn == 0;
+    if (bs_auto) o.bn = 128;
     o.cta_group = 1;
     o.bk = 128;
     o.tma_boxes = TST_BOXES_2D;
@@ -388,8 +392,13 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
     p->cg = o.cta_group != 0 ? o.cta_group : tc.cg;
   }
   p->bm = tst::kBlockM * p->cg;
-  if (bs && groups > 0 && groups <= kBsWalkGroups && epi->ab_block_k == 128) p->narrow = narrow_rows(ceil_div(M, groups));
+  if (bs_auto && groups > 0 && groups <= kBsWalkGroups && epi->ab_block_k == 128)
+    p->narrow = narrow_rows(ceil_div(M, groups));
   if (p->narrow) p->bm = p->narrow;
+  // 256 columns where they leave tiles enough for the SMs: 4096 rows over 32 experts of 4096 x 4096
+  // 122 us at 128 columns, 113 at 256; 16384 over 16 330 and 261
+  else if (bs_auto && groups > 0 && bs_shared && ceil_div(M, tst::kBlockM) * ceil_div(N, 256) >= p->num_sms)
+    p->bn = 256;
   // A multicast across two side-by-side single-CTA tiles: the multicast kernel instance
   // covers the basic epilogue of one GEMM with two-atom k-tiles
   if (o.cluster_n < 0 || o.cluster_n > 2) { delete p; return TST_ERR_INVALID_ARG; }
@@ -421,20 +430,19 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
   if (T >= (int64_t(1) << 30) || T * kt >= (int64_t(1) << 62)) { delete p; return TST_ERR_INVALID_ARG; }
   p->stages = tst_kernel_stages(p->bn, p->cg, p->ka);
   if (p->bs) p->stages -= 1;   // the last stage's A slot holds the block-scaled kernel's scale windows
-  // one scale of B per 128-column tile and k-block
-  const bool bs_shared = bs && groups <= kBsWalkGroups && epi->ab_block_k == 128 && bs_rows_b(*epi) % 128 == 0;
-  const TstNarrow narrow = p->narrow ? tst_bs_narrow(p->narrow, kernel_out(*p), bs_shared) : TstNarrow{};
-  if (p->narrow) p->stages = narrow.stages;
+  const TstBsKernel own = p->narrow ? tst_bs_narrow(p->narrow, kernel_out(*p), bs_shared)
+                          : bs && p->bn == 256 ? tst_bs_wide(kernel_out(*p)) : TstBsKernel{};
+  if (own.kernel) p->stages = own.stages;
   if (o.stages != 0) {
     if (o.stages < 2 || o.stages > p->stages) { delete p; return TST_ERR_UNSUPPORTED; }
     p->stages = o.stages;
   }
-  p->smem_bytes = p->narrow ? narrow.smem_bytes : tst_kernel_smem_bytes(p->bn, p->cg, p->ka);
-  p->threads = p->narrow ? narrow.threads : bs_shared ? kBsTileThreads : p->bs ? kBsThreads : tst_kernel_threads(p->bn, p->ka, p->ext_on);
+  p->smem_bytes = own.kernel ? own.smem_bytes : tst_kernel_smem_bytes(p->bn, p->cg, p->ka);
+  p->threads = own.kernel ? own.threads : bs_shared ? kBsTileThreads : p->bs ? kBsThreads : tst_kernel_threads(p->bn, p->ka, p->ext_on);
   if (!p->host_only) {
     // the extended epilogue has its own instance (two epilogue warpgroups, typed stores of D)
     const int kdt = dtype == TST_BF16 ? tst::DT_BF16 : tst::DT_E4M3;
-    p->kernel = p->narrow   ? narrow.kernel
+    p->kernel = own.kernel  ? own.kernel
                 : bs_shared ? tst_bs_tile_kernel(kernel_out(*p))
                 : p->bs     ? tst_bs_kernel(kernel_out(*p), bs_rows_b(*epi) % 32 != 0)
                 : p->ext_on ? tst_kernel_ext(kdt, p->bn, p->cg, p->ka)

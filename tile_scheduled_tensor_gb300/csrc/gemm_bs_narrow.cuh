@@ -5,7 +5,7 @@
 //
 // with the operands' places exchanged.  A 128-row tensor-core tile over a group of a few rows
 // would hold mostly rows of other groups; here the 128 rows (TMEM lanes) are 128 columns of D,
-// i.e. rows of B, and the instruction's N are NT = 16, 32 or 64 rows of the group.  What bounds
+// i.e. rows of B, and the instruction's N are NT = 16 or 32 rows of the group.  What bounds
 // such groups is reading B once, so the ring holds little of A and the promotion adds NT sums per
 // thread and k-block instead of 64 per thread of twice as many threads.
 //
@@ -30,7 +30,7 @@ struct NarrowCfg {
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-  static constexpr int BUFS = NT == 64 ? 4 : 8;             // k-block partials in TMEM
+  static constexpr int BUFS = 8;                            // k-block partials in TMEM
   static constexpr int TMEM_COLS = BUFS * NT;
   static constexpr int WINDOW_BYTES = kBsWindow * NT * 4;
   static constexpr int LIMIT = (228 * 1024 - 2 * 1024) / 2;   // dynamic shared memory of one of two CTAs per SM
@@ -179,23 +179,17 @@ __device__ __forceinline__ void narrow_epilogue(const KernelParams& p, const Ctx
             const long long t1 = stat_thread ? clock64() : 0;
             if (stat_thread) wait_pfull += t1 - t0;
             ptx::tc_fence_after();
-            constexpr int CHUNK = NT < 32 ? NT : 32;
+            float v[NT];
+            if constexpr (NT == 16) ptx::tmem_load_16cols(taddr0 + static_cast<uint32_t>(buf * NT), v);
+            else ptx::tmem_load_32cols(taddr0 + static_cast<uint32_t>(buf * NT), v);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_pempty + 8 * buf);   // the partials are in registers
+            if constexpr (!SHARED) {
 #pragma unroll
-            for (int h = 0; h < NT / CHUNK; ++h) {
-              float v[CHUNK];
-              if constexpr (NT == 16) ptx::tmem_load_16cols(taddr0 + static_cast<uint32_t>(buf * NT), v);
-              else ptx::tmem_load_32cols(taddr0 + static_cast<uint32_t>(buf * NT + h * CHUNK), v);
-              if (h == NT / CHUNK - 1) {   // the buffer's last partials are in registers
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(bar_pempty + 8 * buf);
-              }
-              if constexpr (!SHARED) {
-#pragma unroll
-                for (int i = 0; i < CHUNK; i += 2) ptx::mul_f32x2(v[i], v[i + 1], sb[j], sb[j], v[i], v[i + 1]);
-              }
-              narrow_fold(win + j * NT + h * CHUNK, v, r + h * CHUNK);
+              for (int i = 0; i < NT; i += 2) ptx::mul_f32x2(v[i], v[i + 1], sb[j], sb[j], v[i], v[i + 1]);
             }
+            narrow_fold(win + j * NT, v, r);
             if (++buf == Cfg::BUFS) { buf = 0; buf_phase ^= 1u; }
             if (stat_thread) busy += clock64() - t1;
           }

@@ -18,12 +18,12 @@
 
 namespace tst {
 
-// TMA producer by one thread: A_ROWS x 128 bytes of A and 128 x 128 of B per stage, at smem_a and
+// TMA producer by one thread: A_ROWS x 128 bytes of A and B_ROWS x 128 of B per stage, at smem_a and
 // smem_b + stage * their strides.
-template <int A_ROWS>
+template <int A_ROWS, int B_ROWS = 128>
 __device__ __forceinline__ void bs_producer(const KernelParams& p, const Ctx& c, Walk walk, uint32_t smem_a, uint32_t stride_a,
                                             uint32_t smem_b, uint32_t stride_b, uint32_t bar_full, uint32_t bar_empty) {
-  constexpr uint32_t STAGE_BYTES = (A_ROWS + 128) * 128;
+  constexpr uint32_t STAGE_BYTES = (A_ROWS + B_ROWS) * 128;
   int stage = 0;
   uint32_t phase = 0, issued = 0, issued_parity = 0;
   bool ok = true;
@@ -45,7 +45,7 @@ __device__ __forceinline__ void bs_producer(const KernelParams& p, const Ctx& c,
       rec[4] = w.n; rec[5] = 0; rec[6] = nkb; rec[7] = ITEM_FINAL | (w.clamped ? ITEM_CLAMPED : 0);
     }
     if (w.clamped) record_status(p, ST_DEVICE_CHECK, ROLE_PRODUCER);
-    const int32_t b_row0 = w.group * p.sched.group_b_rows + w.n * 128;
+    const int32_t b_row0 = w.group * p.sched.group_b_rows + w.n * B_ROWS;
     for (int32_t kb = 0; kb < nkb; ++kb) {
       const long long t0 = p.stats ? clock64() : 0;
       if (!wait_phase<1>(p, c, bar_empty + 8 * stage, phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
@@ -188,8 +188,7 @@ __device__ __forceinline__ void run_epilogue_tile(const KernelParams& p, const C
   };
   auto fold = [&](float s, const uint32_t (&v)[32], float* r) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2)
-      ptx::fma_f32x2(r[i], r[i + 1], s, s, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+    for (int i = 0; i < 32; i += 2) ptx::fma_f32x2_after(r[i], r[i + 1], s, v[i], v[i + 1]);
   };
   Tile w, wn;
   bool have = walk.next_warp(w);
@@ -239,17 +238,17 @@ __device__ __forceinline__ void run_epilogue_tile(const KernelParams& p, const C
         for (int j = 0; j < kTileWindow; j += 2) {
           const int left = nkb - kb - j;   // k-blocks from this pair on; an odd last one is alone
           if (left <= 0 || !ok) break;
-          ptx::tmem_wait_loads(va);
+          ptx::tmem_wait_loads();
           load(q, 0, 1, vb);
           fold(s[j], va, r);
-          ptx::tmem_wait_loads(vb);
+          ptx::tmem_wait_loads();
           if (left > 1) {
             load(q, 1, 0, va);
             fold(s[j], vb, r + 32);
-            ptx::tmem_wait_loads(va);
+            ptx::tmem_wait_loads();
             load(q, 1, 1, vb);
             fold(s[j + 1], va, r);
-            ptx::tmem_wait_loads(vb);
+            ptx::tmem_wait_loads();
           }
           release(q);   // the slot's last partials are in registers
           ++q;

@@ -1,4 +1,4 @@
-// Instantiations of the narrow block-scaled grouped kernel: 16, 32 or 64 rows of a group per
+// Instantiations of the narrow block-scaled grouped kernel: 16 or 32 rows of a group per
 // tile, FP32 or BF16 output, one scale of B per tile and k-block (shared) or one per column.
 #include "gemm_bs_narrow.cuh"
 
@@ -15,12 +15,12 @@ const void* kernel_of(int out_type, bool shared) {
   return nullptr;
 }
 template <int NT>
-TstNarrow narrow_of(int out_type, bool shared) {
+TstBsKernel narrow_of(int out_type, bool shared) {
   using Cfg = tst::NarrowCfg<NT>;
   return {kernel_of<NT>(out_type, shared), Cfg::STAGES, Cfg::SMEM_BYTES, kBsNarrowThreads};
 }
 }  // namespace
 
-TstNarrow tst_bs_narrow(int rows, int out_type, bool shared) {
-  return rows == 16 ? narrow_of<16>(out_type, shared) : rows == 32 ? narrow_of<32>(out_type, shared) : narrow_of<64>(out_type, shared);
+TstBsKernel tst_bs_narrow(int rows, int out_type, bool shared) {
+  return rows == 16 ? narrow_of<16>(out_type, shared) : narrow_of<32>(out_type, shared);
 }

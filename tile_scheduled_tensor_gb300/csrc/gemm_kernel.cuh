@@ -121,7 +121,9 @@ __device__ __forceinline__ unsigned long long lock_value(const KernelParams& p, 
 template <int CG>
 __device__ __forceinline__ bool wait_phase(const KernelParams& p, const Ctx& c, uint32_t bar, uint32_t parity,
                                            uint32_t role) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
+  // most waits end within a few tries, which cost less than reading the timer once
+  for (uint32_t spin = 0; spin < 32u; ++spin)
+    if (ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer();
   for (uint32_t spin = 1;; ++spin) {
     if (ptx::mbar_try_wait(bar, parity)) return true;

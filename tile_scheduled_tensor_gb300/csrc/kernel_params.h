@@ -296,14 +296,17 @@ constexpr int kBsTileThreads = 384;
 constexpr int kBsWalkGroups = 512;   // most groups of a grouped plan in this form and the next
 const void* tst_bs_tile_kernel(int out_type);
 
-// The narrow form for groups of few rows (gemm_bsn.cu): 128 columns of D by `rows` = 16, 32 or 64
-// rows of a group per tile, k-blocks of 128, two CTAs per SM.  shared: as the form above.
+// Forms of the block-scaled kernel with their own ring and threads: 128 x 256 tiles under the same
+// conditions (gemm_bsw.cu); and, grouped, for groups of few rows, 128 columns of D by `rows` = 16
+// or 32 rows of a group per tile, k-blocks of 128, two CTAs per SM, shared as the form above
+// (gemm_bsn.cu).
 constexpr int kBsNarrowThreads = 192;
-struct TstNarrow {
+struct TstBsKernel {
   const void* kernel;
   int stages, smem_bytes, threads;
 };
-TstNarrow tst_bs_narrow(int rows, int out_type, bool shared);
+TstBsKernel tst_bs_wide(int out_type);
+TstBsKernel tst_bs_narrow(int rows, int out_type, bool shared);
 
 inline int tst_kernel_threads(int bn, int ka, bool ext = false) {
   return ((bn == 128 && ka == 2) ? tst::kThreadsDual : tst::kThreads) + (ext ? 128 : 0);

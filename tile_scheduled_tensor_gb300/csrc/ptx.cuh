@@ -253,14 +253,9 @@ __device__ __forceinline__ void tmem_load_32cols_async(uint32_t taddr, uint32_t*
       : "r"(taddr)
       : "memory");
 }
-// Wait for every load in flight of this thread; the 32 registers at r pass through, so that no use
-// of them moves before the wait
-__device__ __forceinline__ void tmem_wait_loads(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
+// Wait for every tensor-memory load in flight of this thread.  Nothing ties the loaded registers to
+// it (operands passed through would be copied), so only volatile asm (fma_f32x2_after) may use them.
+__device__ __forceinline__ void tmem_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Registers per thread of this warpgroup from here on: `dec` gives some back, `inc` waits for its
 // share of what the block was launched with
@@ -396,6 +391,19 @@ __device__ __forceinline__ void fma_f32x2(float& d0, float& d1, float a0, float 
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(f32x2(a0, a1)), "l"(f32x2(b0, b1)), "l"(f32x2(d0, d1)));
   f32x2_split(d, d0, d1);
+}
+// (d0, d1) += (a, a) * (b0, b1), the same operation, kept in program order with the other volatile
+// statements: for operands of a load that a wait statement before it completes
+__device__ __forceinline__ void fma_f32x2_after(float& d0, float& d1, float a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "mov.b64 d, {%0, %1};\n\t"
+      "fma.rn.f32x2 d, a, b, d;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a), "r"(b0), "r"(b1));
 }
 // (d0, d1) = (a0, a1) * (b0, b1), round to nearest
 __device__ __forceinline__ void mul_f32x2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
