@@ -28,11 +28,12 @@ def route(logits, top_k, normalize, coef, mask=None):
     prob = np.zeros(E)
     live = 0
     for t in range(T):
-        open_ = [e for e in range(E) if not l[t, e] == -np.inf]
-        if not open_:
+        open_ = np.flatnonzero(l[t] != -np.inf)   # a NaN is not -inf
+        if open_.size == 0:
             continue
         live += 1
-        order = sorted(open_, key=lambda e: (0, 0.0, e) if np.isnan(l[t, e]) else (1, -l[t, e], e))[:top_k]
+        nan = np.isnan(l[t, open_])
+        order = open_[np.lexsort((open_, np.where(nan, 0.0, -l[t, open_]), ~nan))][:top_k]
         with np.errstate(invalid="ignore"):
             x = np.exp(l[t] - (np.nan if np.isnan(l[t]).any() else l[t].max()))
         p = x / x.sum()
@@ -43,13 +44,9 @@ def route(logits, top_k, normalize, coef, mask=None):
     counts = np.bincount(expert[expert >= 0], minlength=E).astype(np.int32)
     first = np.concatenate([[0], np.cumsum(counts)[:-1]])
     row = np.full((T, top_k), -1, dtype=np.int32)
-    seen = np.zeros(E, dtype=np.int64)
-    for t in range(T):
-        for j in range(top_k):
-            e = expert[t, j]
-            if e >= 0:
-                row[t, j] = first[e] + seen[e]
-                seen[e] += 1
+    for e in range(E):
+        at = np.argwhere(expert == e)   # by token: an expert occurs once in a row
+        row[at[:, 0], at[:, 1]] = first[e] + np.arange(len(at))
     R = int(counts.sum())
     loss = coef * E * float(np.sum(counts / max(R, 1) * (prob / max(live, 1))))
     return dict(expert=expert, weight=weight, row=row, counts=counts, totals=np.array([R, live], dtype=np.int32),

@@ -97,7 +97,7 @@ def test_route_equals_the_oracle(T, E, k, dtype):
         _check_route(o, moe.route(l, k, normalize, 0.02), l, normalize)
 
 
-@pytest.mark.parametrize("T", [31, 32, 33, 2000, 9728, 9729, 20000])
+@pytest.mark.parametrize("T", [31, 32, 33, 2000, 9728, 9729, 19456, 19457, 20000])
 def test_route_many_chunks(T):
     # token counts on both sides of the chunk sizes, uneven loads; a plan made for more tokens
     E, k = 12, 3
@@ -107,6 +107,56 @@ def test_route_many_chunks(T):
     want = moe.route(l, k, True, 1.0)
     for _ in range(2):
         _check_route(_route(plan, logits), want, l, True)
+
+
+# many tokens per block: both types, whole and ragged rows, few and many choices
+@pytest.mark.parametrize("T,E,k,dtype,kind", [
+    (19456, 256, 8, "f32", "normal"), (19457, 200, 5, "bf16", "normal"), (20001, 64, 16, "f32", "normal"),
+    (19999, 129, 8, "f32", "normal"), (19700, 255, 10, "bf16", "normal"), (19456, 40, 3, "bf16", "normal"),
+    (19456, 512, 10, "bf16", "normal"), (19456, 33, 1, "f32", "normal"), (19456, 96, 8, "f32", "masked"),
+    (19999, 130, 6, "bf16", "masked"), (19500, 128, 7, "f32", "ties"), (19500, 256, 8, "bf16", "ties"),
+    (19456, 64, 8, "f32", "equal"), (70000, 34, 2, "f32", "normal")])
+def test_route_of_many_tokens_equals_the_oracle(T, E, k, dtype, kind):
+    rng = np.random.default_rng(T + E)
+    l, mask = _normal(220 + T + E, T, E) * 2 + np.linspace(0, 1, E)[None, :], None
+    if kind == "ties":
+        l = np.round(l)
+    elif kind == "equal":
+        l[:] = 0.5
+    elif kind == "masked":
+        l[rng.random((T, E)) < 0.3] = -np.inf
+        l[rng.random(T) < 0.05] = -np.inf                      # nothing open
+        l[7:40, 2:] = -np.inf                                  # fewer open than k
+        l[100:130] = 3e38                                      # beyond the plain exponentials
+        mask = (rng.random(T) < 0.9).astype(np.uint8)
+    plan = tst.moe_plan_create(T, E, k, normalize=kind != "masked", balance_coef=0.5)
+    logits = _dev(l, dtype)
+    ll = _host(logits)
+    m = None if mask is None else torch.from_numpy(mask).cuda()
+    if m is not None:
+        logits[m == 0] = float("nan")
+        logits = _strided(logits, 8)
+    want = moe.route(ll, k, kind != "masked", 0.5, mask)
+    if mask is not None:
+        ll[mask == 0] = -np.inf
+    first = _route(plan, logits, m)
+    _check_route(first, want, ll, kind != "masked")
+    again = _route(plan, logits, m)
+    assert all(torch.equal(first[n], again[n]) for n in first)
+
+
+def test_route_of_many_tokens_keeps_nan_and_infinities_visible():
+    T, E, k = 19456, 64, 4
+    l = _normal(230, T, E)
+    l[11, 4] = np.nan
+    l[12, 63] = np.inf
+    l[13, 7] = l[13, 2] = np.nan
+    l[19000] = np.nan
+    plan = tst.moe_plan_create(T, E, k)
+    o = _route(plan, _dev(l))
+    want = moe.route(l.astype(np.float32).astype(np.float64), k, True, 0.01)
+    _check_route(o, want, l.astype(np.float32).astype(np.float64), True)
+    assert np.isnan(o["loss"].item()) and np.isnan(_host(o["weight"])[[11, 12, 13, 19000]]).all()
 
 
 def test_route_masks_ties_and_closed_experts():

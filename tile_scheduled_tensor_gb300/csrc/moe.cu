@@ -38,13 +38,12 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 bool float_type(int32_t t) { return t == TST_OUT_F32 || t == TST_OUT_BF16; }
 int64_t type_bytes(int32_t t) { return t == TST_OUT_F32 ? 4 : t == TST_OUT_BF16 ? 2 : 1; }
 
-// Tokens per block of the routing kernel: the smallest of 32, 64, 128 and 256 that gives at most
-// two blocks per SM's share of 304, so that small calls spread out and large ones keep few chunks.
-constexpr int64_t kFewChunks = 304;
+// Tokens per block of the routing kernel: the fewest multiple of 32 that keeps to four blocks per SM,
+// which are resident at once, up to 256 (whose bitmap is 8 words per expert).
+constexpr int64_t kResidentChunks = 4 * 152;
 int32_t route_chunk(int64_t tokens) {
-  for (int32_t c = 32; c < 256; c *= 2)
-    if (tokens <= c * kFewChunks) return c;
-  return 256;
+  const int64_t c = ceil_div(ceil_div(tokens, 32), kResidentChunks) * 32;
+  return static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(c, 32), 256));
 }
 
 // shared memory of a routing block: RouteShared, and the small kernel's staged choices
@@ -170,7 +169,7 @@ tst_status moe_plan_create(tst_moe_plan** out, int64_t max_tokens, int32_t exper
   p->coef = opts->balance_coef;
   p->host_only = opts->host_only != 0;
   // the most chunks that any call of up to max_tokens tokens has
-  const int64_t chunks = std::max(std::min(kFewChunks, ceil_div(max_tokens, 32)), ceil_div(max_tokens, 256));
+  const int64_t chunks = std::max(std::min(kResidentChunks, ceil_div(max_tokens, 32)), ceil_div(max_tokens, 256));
   const size_t prob = ((static_cast<size_t>(experts) * 4 + 255) / 256) * 256;
   const size_t part = ((static_cast<size_t>(experts + 1) * chunks * 4 + 255) / 256) * 256;
   p->dev_bytes = 256 + prob + 2 * part;

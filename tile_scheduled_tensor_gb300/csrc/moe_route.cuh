@@ -284,10 +284,12 @@ __device__ __forceinline__ void choose_by_rounds(const T* src, int E, int k, int
 // A warp per row, rows dealt to the block's warps in turn.  The choice: k - 1 rounds of a warp
 // maximum over the lanes' own maxima leave a bound that at least k logits reach; those that do,
 // seldom more than a few over k, go to a list in shared memory with their experts in the low word,
-// and each finds its rank by comparing itself with the others.  That takes a third of the
-// instructions of k rounds over all logits, which remain for rows with more than 32 on the list,
-// NaN, infinities or magnitudes over 2^100.  The bound is issue slots, about 200 a row of 256
-// logits, not the 1 KB that it reads.
+// and each finds its rank by comparing itself with the others.  Rounds over all logits remain for rows with
+// more than 32 on the list, NaN, infinities or magnitudes over 2^100.  What bounds it is issue slots
+// (about 69 % of them used, 450 instructions for a row of 256 logits), not the 1 KB that the row
+// reads: 131071 rows of 256, k = 8, in 92 us with the two launches after it, 235 by rounds alone;
+// their bytes take 22 us.  Threads that hold whole or half rows of a tile in shared memory need 230
+// to 300 instructions a row, but leave 5 to 10 warps on an SM and measured 128 and 99 us.
 template <typename T, int VPL, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) route_rows_kernel(const RouteParams p) {
   using Map = RowMap<T, VPL>;
@@ -345,29 +347,19 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
           own = own == bound ? closed_logit() : own;
           bound = warp_max(own);
         }
+        bound = fmaxf(bound, -3.4028235e38f);   // a closed logit reaches no bound
         int n = 0;
-        for (;;) {
-          const bool has = best >= bound && best > closed_logit();
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+          const bool has = x[v] >= bound;
           const uint32_t who = __ballot_sync(kFullMask, has);
-          if (who == 0u) break;
           const int slot = n + __popc(who & below);
+          if (has && slot < kRouteCandidates)
+            list[warp][slot] = (static_cast<uint64_t>(order_key(x[v])) << 32) |
+                               (0xFFFFFFFFu - static_cast<uint32_t>(Map::expert(v, lane)));
           n += __popc(who);
-          if (n > kRouteCandidates) { listed = false; break; }
-          if (has) {   // list this lane's best, and find the next
-            int v0 = 0;
-#pragma unroll
-            for (int v = VPL - 1; v >= 0; --v)
-              if (x[v] == best) v0 = v;
-            list[warp][slot] = (static_cast<uint64_t>(order_key(best)) << 32) |
-                               (0xFFFFFFFFu - static_cast<uint32_t>(Map::expert(v0, lane)));
-            best = closed_logit();
-#pragma unroll
-            for (int v = 0; v < VPL; ++v) {
-              if (v == v0) x[v] = closed_logit();
-              best = fmaxf(best, x[v]);
-            }
-          }
         }
+        listed = n <= kRouteCandidates;
         __syncwarp();
         if (listed) {
           // two lanes per listed logit share the comparisons when at most 16 are listed
@@ -396,7 +388,7 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
         if (chosen >= 0) w = ex.any(value);
       }
       const float over = p.normalize ? warp_sum(w) : sum;
-      w = chosen >= 0 ? w / over : 0.0f;
+      w = chosen >= 0 ? __fdividef(w, over) : 0.0f;   // 1 <= over <= 1024, or NaN
       if (chosen >= 0) atomicOr(&s.bitmap[chosen * words + (r >> 5)], 1u << (r & 31));
     }
     if (at < k) {
