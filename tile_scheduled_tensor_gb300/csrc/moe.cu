@@ -408,20 +408,44 @@ tst_status moe_dispatch(tst_moe_plan* p, int64_t tokens, int64_t hidden, const v
 
 namespace {
 
+// pieces of N elements per thread and, few of them, threads per token
+template <typename TI, typename TO, int N>
+tst_status launch_combine_of(RowsParams& a, cudaStream_t s) {
+  const int64_t pieces = ceil_div(a.hidden, N);
+#define TST_CALL(U, L)                                                                                       \
+  do {                                                                                                       \
+    a.slices = static_cast<int32_t>(ceil_div(pieces, (U) * (L)));                                            \
+    const int64_t grid = ceil_div(a.tokens * a.slices, tst::kTokenThreads / (L));                            \
+    if (grid >= (int64_t(1) << 31)) return TST_ERR_UNSUPPORTED;                                              \
+    tst::combine_kernel<TI, TO, N, U, L><<<static_cast<unsigned>(grid), tst::kTokenThreads, 0, s>>>(a);      \
+  } while (0)
+  if (pieces <= 32) TST_CALL(1, 32);
+  else if (pieces <= 128) TST_CALL(1, 128);
+  else if (pieces <= 256) TST_CALL(2, 128);
+  else TST_CALL(4, 128);
+#undef TST_CALL
+  return TST_OK;
+}
+
+// N: 16 bytes of the rows
 template <typename TI, typename TO>
 tst_status launch_combine(RowsParams& a, bool vec, cudaStream_t s) {
-  if (!slice(a, a.hidden, vec ? 256 : 32)) return TST_ERR_UNSUPPORTED;
-  const int32_t grid = row_grid(a.tokens * a.slices);
-  if (vec) tst::combine_kernel<TI, TO, 8, true><<<grid, tst::kRowsThreads, 0, s>>>(a);
-  else tst::combine_kernel<TI, TO, 1, false><<<grid, tst::kRowsThreads, 0, s>>>(a);
-  return TST_OK;
+  return vec ? launch_combine_of<TI, TO, 16 / sizeof(TI)>(a, s) : launch_combine_of<TI, TO, 1>(a, s);
+}
+
+template <typename TI, typename TO, int N>
+void launch_combine_grad_of(const RowsParams& a, cudaStream_t s) {
+  const int64_t pieces = ceil_div(a.hidden, N);
+  const unsigned grid = static_cast<unsigned>(a.tokens);
+  if (pieces <= 128) tst::combine_grad_kernel<TI, TO, N, 1><<<grid, tst::kTokenThreads, 0, s>>>(a);
+  else if (pieces <= 256) tst::combine_grad_kernel<TI, TO, N, 2><<<grid, tst::kTokenThreads, 0, s>>>(a);
+  else tst::combine_grad_kernel<TI, TO, N, 4><<<grid, tst::kTokenThreads, 0, s>>>(a);
 }
 
 template <typename TI, typename TO>
 tst_status launch_combine_grad(RowsParams& a, bool vec, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.tokens);
-  if (vec) tst::combine_grad_kernel<TI, TO, 8, true><<<grid, tst::kRowsThreads, 0, s>>>(a);
-  else tst::combine_grad_kernel<TI, TO, 1, false><<<grid, tst::kRowsThreads, 0, s>>>(a);
+  if (vec) launch_combine_grad_of<TI, TO, 16 / sizeof(TI)>(a, s);
+  else launch_combine_grad_of<TI, TO, 1>(a, s);
   return TST_OK;
 }
 

@@ -64,24 +64,6 @@ __device__ __forceinline__ void load_f32(const T* p, float (&v)[N]) {
   }
 }
 
-template <typename T, int N, bool VEC>
-__device__ __forceinline__ void store_f32(T* p, const float (&v)[N]) {
-  if constexpr (VEC) {
-    constexpr int PER = 16 / sizeof(T);
-#pragma unroll
-    for (int q = 0; q < N / PER; ++q) {
-      uint4 u;
-      T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) e[i] = static_cast<T>(v[q * PER + i]);
-      reinterpret_cast<uint4*>(p)[q] = u;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = static_cast<T>(v[i]);
-  }
-}
-
 // e4m3 rows with one FP32 scale per 128 elements: scale = amax / 448, value = x (448 / amax)
 // rounded to e4m3.  The largest magnitude is found on the absolute bits as integers, where NaN
 // and infinity stand above every number, so a block that holds one gets a NaN scale or an infinite
@@ -145,65 +127,114 @@ __global__ void __launch_bounds__(kRowsThreads) dispatch_copy_kernel(const RowsP
   }
 }
 
-// A thread sums N elements of one token over its rows in FP32, in the order of the choices.
-template <typename TI, typename TO, int N, bool VEC>
-__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const RowsParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5);
+// N adjacent elements as they lie in memory: one load or store of up to 16 bytes when aligned for it.
+template <typename T, int N>
+struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Piece {
+  T e[N];
+};
+template <typename T, int N>
+__device__ __forceinline__ Piece<T, N> load_piece(const T* p) {
+  Piece<T, N> v;
+  if constexpr (N * sizeof(T) == 16) *reinterpret_cast<uint4*>(&v) = __ldg(reinterpret_cast<const uint4*>(p));
+  else v = *reinterpret_cast<const Piece<T, N>*>(p);
+  return v;
+}
+
+// A block has L threads for each of its 128 / L tokens; a thread sums U pieces of N elements over
+// the token's rows in FP32, in the order of the choices.  The U pieces of one row are in flight
+// together, L pieces apart, and stay as they came until they are added, which keeps the registers
+// of many blocks free: rows of 8 KB, 8 per token, in 190 us where their bytes at the copy rate
+// are 178 (207 with one piece per thread, 288 with pieces of four rows in flight).
+constexpr int kTokenThreads = 128;
+template <typename TI, typename TO, int N, int U, int L>
+__global__ void __launch_bounds__(kTokenThreads) combine_kernel(const RowsParams p) {
+  const int lane = threadIdx.x % L;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kTokenThreads / L) + threadIdx.x / L;
   const int64_t t = item / p.slices;
-  const int h = (static_cast<int>(item - t * p.slices) * 32 + lane) * N;
-  if (t >= p.tokens || h >= p.hidden) return;
-  float acc[N];
+  if (t >= p.tokens) return;
+  const int h0 = (static_cast<int>(item - t * p.slices) * L * U + lane) * N;   // then every L N elements
+  float acc[U][N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[u][i] = 0.0f;
+#pragma unroll 1
   for (int j = 0; j < p.top_k; ++j) {
     const int64_t r = p.row[t * p.top_k + j];
     if (!row_ok(p, r)) continue;
     const float w = p.weight ? p.weight[t * p.top_k + j] : 1.0f;
-    float v[N];
-    load_f32<TI, N, VEC>(static_cast<const TI*>(p.rows) + r * p.hidden + h, v);
+    const TI* const row = static_cast<const TI*>(p.rows) + r * p.hidden + h0;
+    Piece<TI, N> v[U];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+    for (int u = 0; u < U; ++u)
+      if (h0 + u * L * N < p.hidden) v[u] = load_piece<TI, N>(row + u * L * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[u][i] = fmaf(w, to_f32<TI>(v[u].e[i]), acc[u][i]);   // past the row: not stored
   }
-  store_f32<TO, N, VEC>(static_cast<TO*>(p.out) + t * p.out_ld + h, acc);
+  TO* const out = static_cast<TO*>(p.out) + t * p.out_ld + h0;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (h0 + u * L * N < p.hidden) {
+      Piece<TO, N> o;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o.e[i] = static_cast<TO>(acc[u][i]);
+      *reinterpret_cast<Piece<TO, N>*>(out + u * L * N) = o;
+    }
 }
 
-// A block per token: d_out's elements times each weight go to the rows, and the dot products with
-// the rows are summed in FP32 by threads, lanes and warps, in a fixed order.
-template <typename TI, typename TO, int N, bool VEC>
-__global__ void __launch_bounds__(kRowsThreads) combine_grad_kernel(const RowsParams p) {
-  __shared__ float part[kRowsThreads / 32];
+// The same layout, with one token per block: d_out's pieces in registers, times each weight go to the
+// rows, and the dot products with the rows are summed in FP32 by threads, lanes and warps, in a fixed
+// order; the warps exchange theirs once, at the end.
+template <typename TI, typename TO, int N, int U>
+__global__ void __launch_bounds__(kTokenThreads) combine_grad_kernel(const RowsParams p) {
+  constexpr int WARPS = kTokenThreads / 32, STEP = kTokenThreads * N;
+  __shared__ float part[WARPS][32];   // top_k <= 32
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = blockIdx.x;
-  const TO* d_out = static_cast<const TO*>(p.x) + t * p.x_ld;
-  for (int j = 0; j < p.top_k; ++j) {
-    const int64_t r = p.row[t * p.top_k + j];
-    const bool has = row_ok(p, r);
-    float dot = 0.0f;
-    if (has) {
+  if (lane < p.top_k) part[warp][lane] = 0.0f;
+  __syncwarp();
+  for (int first = 0; first < p.hidden; first += U * STEP) {
+    const int h0 = first + static_cast<int>(threadIdx.x) * N;
+    const TO* const d_out = static_cast<const TO*>(p.x) + t * p.x_ld + h0;
+    Piece<TO, N> d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h0 + u * STEP < p.hidden) d[u] = load_piece<TO, N>(d_out + u * STEP);
+#pragma unroll 1
+    for (int j = 0; j < p.top_k; ++j) {
+      const int64_t r = p.row[t * p.top_k + j];
+      if (!row_ok(p, r)) continue;
       const float w = p.weight[t * p.top_k + j];
-      for (int h = static_cast<int>(threadIdx.x) * N; h < p.hidden; h += kRowsThreads * N) {
-        float d[N], v[N];
-        load_f32<TO, N, VEC>(d_out + h, d);
-        load_f32<TI, N, VEC>(static_cast<const TI*>(p.rows) + r * p.hidden + h, v);
+      const TI* const row = static_cast<const TI*>(p.rows) + r * p.hidden + h0;
+      TI* const d_row = static_cast<TI*>(p.out) + r * p.hidden + h0;
+      Piece<TI, N> v[U];
+      float dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          dot = fmaf(d[i], v[i], dot);
-          d[i] *= w;
+      for (int u = 0; u < U; ++u)
+        if (h0 + u * STEP < p.hidden) v[u] = load_piece<TI, N>(row + u * STEP);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h0 + u * STEP < p.hidden) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float x = to_f32<TO>(d[u].e[i]);
+            dot = fmaf(x, to_f32<TI>(v[u].e[i]), dot);
+            v[u].e[i] = static_cast<TI>(x * w);
+          }
+          *reinterpret_cast<Piece<TI, N>*>(d_row + u * STEP) = v[u];
         }
-        store_f32<TI, N, VEC>(static_cast<TI*>(p.out) + r * p.hidden + h, d);
-      }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-    if (lane == 0) part[warp] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float s = 0.0f;
-      for (int i = 0; i < kRowsThreads / 32; ++i) s += part[i];
-      p.scales[t * p.top_k + j] = s;
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+      if (lane == 0) part[warp][j] += dot;
     }
-    __syncthreads();
+  }
+  __syncthreads();
+  if (threadIdx.x < p.top_k) {
+    float s = 0.0f;
+    for (int i = 0; i < WARPS; ++i) s += part[i][threadIdx.x];
+    p.scales[t * p.top_k + threadIdx.x] = s;
   }
 }
 
