@@ -308,6 +308,30 @@ def test_route_backward_against_differences_of_the_forward():
             assert abs((a - b) / (2 * step) - d[t, e].item()) <= scale * (step * step * 4 / 6 + 64 * U / step)
 
 
+def test_calls_replay_from_a_cuda_graph():
+    # captured once, replayed on new contents of the same tensors
+    T, E, k, H = 300, 40, 3, 256
+    plan = tst.moe_plan_create(T, E, k)
+    logits, x = torch.empty(T, E, device="cuda"), torch.empty(T, H, device="cuda")
+    o = _route(plan, logits.normal_())
+    rows, out = torch.empty(T * k, H, device="cuda"), torch.empty(T, H, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        tst.moe_route(plan, logits, o["expert"], o["weight"], o["row"], o["counts"], o["totals"], o["loss"])
+        tst.moe_dispatch(plan, x, o["row"], rows)
+        tst.moe_combine(plan, rows, o["row"], out, weight=o["weight"])
+    for seed in (1, 2):
+        logits.copy_(_dev(_normal(240 + seed, T, E)))
+        x.copy_(_dev(_normal(250 + seed, T, H)))
+        graph.replay()
+        _check_route(o, moe.route(_host(logits), k, True, 0.01), _host(logits), True)
+        # the weights of a token add up to 1, so the copies come back as the token: k + 1 roundings
+        # of parts of it, and k of the weights' own
+        assert ((out - x).abs() <= (4 * k + 8) * 64 * U * x.abs()).all()
+
+
 def _assign(T, k, E, seed, masked=False):
     """row (T x k) as routing gives it, and the number of rows."""
     rng = np.random.default_rng(seed)

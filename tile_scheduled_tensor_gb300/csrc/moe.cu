@@ -46,11 +46,16 @@ int32_t route_chunk(int64_t tokens) {
   return static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(c, 32), 256));
 }
 
+// warps of a routing block: a warp per 32 threads' rows up to kRouteThreadRow experts; else 8, or 32 (a
+// row each) where blocks of 32 tokens leave SMs idle and the registers allow it
+int32_t route_warps(int32_t experts, int32_t chunk, int64_t chunks) {
+  if (experts <= tst::kRouteThreadRow) return chunk / 32;
+  return chunk == 32 && chunks <= 152 && experts <= 256 ? 32 : tst::kRouteWarps;
+}
+
 // shared memory of a routing block: RouteShared, and the small kernel's staged choices
-size_t route_smem(int32_t experts, int32_t top_k, int32_t chunk) {
-  const bool small = experts <= tst::kRouteThreadRow;
-  const size_t warps = small ? chunk / 32 : tst::kRouteWarps;
-  const size_t staged = small ? 2 * static_cast<size_t>(chunk) * (top_k | 1) : 0;
+size_t route_smem(int32_t experts, int32_t top_k, int32_t chunk, int32_t warps) {
+  const size_t staged = experts <= tst::kRouteThreadRow ? 2 * static_cast<size_t>(chunk) * (top_k | 1) : 0;
   return (static_cast<size_t>(experts) * (chunk / 32 + warps + 1) + 1 + staged) * 4;
 }
 
@@ -80,13 +85,31 @@ bool whole_packs(const void* p, int64_t ld, int32_t experts) {
   return aligned(p, W * sizeof(T)) && ld % W == 0 && experts % W == 0;
 }
 
+// the same, 16 bytes at a time
 template <typename T>
-const void* route_kernel(const RouteParams& p) {
+bool whole_units(const void* p, int64_t ld, int32_t experts) {
+  constexpr int V = 16 / sizeof(T);
+  return aligned(p, 16) && ld % V == 0 && experts % V == 0;
+}
+
+template <typename T>
+const void* route_kernel(const RouteParams& p, int32_t warps) {
   const void* f = nullptr;
-#define TST_SMALL(EM) f = reinterpret_cast<const void*>(&tst::route_rows_small_kernel<T, EM>)
-#define TST_WARP(V)                                                                                      \
-  f = whole_packs<T, V>(p.logits, p.ld, p.experts) ? reinterpret_cast<const void*>(&tst::route_rows_kernel<T, V, true>) \
-                                                   : reinterpret_cast<const void*>(&tst::route_rows_kernel<T, V, false>)
+#define TST_OF(...) reinterpret_cast<const void*>(&tst::__VA_ARGS__)
+#define TST_SMALL(EM)                                                                             \
+  f = whole_units<T>(p.logits, p.ld, p.experts) ? TST_OF(route_rows_small_kernel<T, EM, true>)    \
+                                                : TST_OF(route_rows_small_kernel<T, EM, false>)
+#define TST_WARP(V)                                                                                    \
+  do {                                                                                                 \
+    const bool vec = whole_packs<T, V>(p.logits, p.ld, p.experts);                                     \
+    if constexpr (V <= 8) {                                                                            \
+      if (warps == 32) {                                                                               \
+        f = vec ? TST_OF(route_rows_kernel<T, V, true, 32>) : TST_OF(route_rows_kernel<T, V, false, 32>); \
+        break;                                                                                         \
+      }                                                                                                \
+    }                                                                                                  \
+    f = vec ? TST_OF(route_rows_kernel<T, V, true, 8>) : TST_OF(route_rows_kernel<T, V, false, 8>);    \
+  } while (0)
   TST_BY_EXPERTS(p.experts, TST_SMALL, TST_WARP);
 #undef TST_SMALL
 #undef TST_WARP
@@ -96,16 +119,20 @@ const void* route_kernel(const RouteParams& p) {
 template <typename T>
 const void* grad_kernel(const RouteGradParams& p) {
   const void* f = nullptr;
-#define TST_SMALL(EM) f = reinterpret_cast<const void*>(&tst::route_grad_small_kernel<T, EM>)
+#define TST_SMALL(EM)                                                                                                   \
+  f = whole_units<T>(p.logits, p.ld, p.experts) && whole_units<T>(p.d_logits, p.d_ld, p.experts)                        \
+          ? TST_OF(route_grad_small_kernel<T, EM, true>)                                                                \
+          : TST_OF(route_grad_small_kernel<T, EM, false>)
 #define TST_WARP(V)                                                                                       \
   f = whole_packs<T, V>(p.logits, p.ld, p.experts) && whole_packs<T, V>(p.d_logits, p.d_ld, p.experts)    \
-          ? reinterpret_cast<const void*>(&tst::route_grad_kernel<T, V, true>)                            \
-          : reinterpret_cast<const void*>(&tst::route_grad_kernel<T, V, false>)
+          ? TST_OF(route_grad_kernel<T, V, true>)                                                         \
+          : TST_OF(route_grad_kernel<T, V, false>)
   TST_BY_EXPERTS(p.experts, TST_SMALL, TST_WARP);
 #undef TST_SMALL
 #undef TST_WARP
   return f;
 }
+#undef TST_OF
 
 // Launch f(params); `after`: it may start while the kernel before it on the stream finishes, and
 // waits for that kernel itself (griddepcontrol.wait).
@@ -188,18 +215,24 @@ tst_status moe_plan_create(tst_moe_plan** out, int64_t max_tokens, int32_t exper
     p->device = dev;
     p->num_sms = sms;
     // each instance that a call of this plan may take, with and without whole packs
-    const int smem = static_cast<int>(route_smem(experts, top_k, 256));
     RouteParams a{};
     a.experts = experts;
-    for (int64_t ld : {int64_t(1024), int64_t(1025)}) {
-      a.ld = ld;
-      for (const void* f : {route_kernel<float>(a), route_kernel<__nv_bfloat16>(a)})
-        if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-          cudaGetLastError();
-          delete p;
-          return TST_ERR_CUDA;
+    for (int64_t ld : {int64_t(1024), int64_t(1025)})
+      for (int32_t chunk : {32, 256}) {
+        a.ld = ld;
+        const int32_t warps = route_warps(experts, chunk, 1);
+        const int smem = static_cast<int>(route_smem(experts, top_k, chunk, warps));
+        for (const void* f : {route_kernel<float>(a, warps), route_kernel<__nv_bfloat16>(a, warps)}) {
+          cudaFuncAttributes have;
+          if (cudaFuncGetAttributes(&have, f) != cudaSuccess ||
+              (have.maxDynamicSharedSizeBytes < smem &&
+               cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)) {
+            cudaGetLastError();
+            delete p;
+            return TST_ERR_CUDA;
+          }
         }
-    }
+      }
     if (cudaMalloc(&p->dev_block, p->dev_bytes) != cudaSuccess) {
       cudaGetLastError();
       delete p;
@@ -287,16 +320,22 @@ tst_status moe_route(tst_moe_plan* p, int64_t tokens, const void* logits, int32_
   a.coef = p->coef;
   bool ok = true;
   if (tokens > 0) {
-    const void* f = dtype == TST_OUT_F32 ? route_kernel<float>(a) : route_kernel<__nv_bfloat16>(a);
-    ok = launch(f, a.chunks, a.experts <= tst::kRouteThreadRow ? a.chunk : tst::kRouteThreads,
-                route_smem(a.experts, a.top_k, a.chunk), s, a);
+    const int32_t warps = route_warps(a.experts, a.chunk, a.chunks);
+    const void* f = dtype == TST_OUT_F32 ? route_kernel<float>(a, warps) : route_kernel<__nv_bfloat16>(a, warps);
+    ok = launch(f, a.chunks, 32 * warps, route_smem(a.experts, a.top_k, a.chunk, warps), s, a);
   }
-  if (a.chunks != 1)   // one chunk finishes by itself
+  if (a.chunks == 1) {
+    // it has finished by itself
+  } else if (a.chunks > 1 && a.chunks <= tst::kFewChunks) {
+    ok = ok && launch(reinterpret_cast<const void*>(&tst::route_sum_place_kernel), a.chunks, tst::kRouteThreads,
+                      (3 * static_cast<size_t>(a.experts) + 1) * 4, s, a, true);
+  } else {
     ok = ok &&
          launch(reinterpret_cast<const void*>(&tst::route_scan_kernel), ceil_div(a.experts + 1, tst::kRouteWarps),
                 tst::kRouteThreads, 0, s, a, true) &&
          launch(reinterpret_cast<const void*>(&tst::route_place_kernel), std::max(a.chunks, 1), tst::kRouteThreads,
                 static_cast<size_t>(a.experts) * 4, s, a, true);
+  }
   if (!ok) {
     cudaGetLastError();
     return TST_ERR_CUDA;

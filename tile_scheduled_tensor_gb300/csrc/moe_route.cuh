@@ -14,8 +14,8 @@
 // (experts x tokens of the chunk) in shared memory: the population count of the bits before the
 // token's, so the order does not depend on which warp got there first.  Then
 // route_scan_kernel turns the chunks' counts into prefix sums, a warp per expert, and
-// route_place_kernel adds the experts' and the chunks' offsets to the ranks; a call of one chunk
-// does all of it in its one block.  Every floating sum has a fixed order, so a call is repeatable
+// route_place_kernel adds the experts' and the chunks' offsets to the ranks; few chunks are summed in
+// route_sum_place_kernel's blocks, and a call of one chunk does all of it in its one block.  Every floating sum has a fixed order, so a call is repeatable
 // bit for bit.
 #pragma once
 #include <cuda_bf16.h>
@@ -174,6 +174,46 @@ __device__ __forceinline__ void store_row(T* dst, int E, int lane, const float (
   }
 }
 
+// A row of up to EM logits in one thread's registers, 16 bytes at a time where VEC (rows of whole,
+// aligned 16-byte units).
+template <typename T, int EM, bool VEC>
+__device__ __forceinline__ void load_thread_row(const T* src, int E, bool on, float (&x)[EM]) {
+  constexpr int V = 16 / sizeof(T) < EM ? 16 / sizeof(T) : EM;
+  struct alignas(16) Pack { T v[16 / sizeof(T)]; };
+#pragma unroll
+  for (int q = 0; q < EM / V; ++q) {
+    if (VEC) {
+      Pack pk;
+      const bool in = on && q * V < E;
+      if (in) pk = *reinterpret_cast<const Pack*>(src + q * V);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[q * V + i] = in ? logit_value<T>(pk.v[i]) : closed_logit();
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[q * V + i] = (on && q * V + i < E) ? logit_value<T>(src[q * V + i]) : closed_logit();
+    }
+  }
+}
+
+template <typename T, int EM, bool VEC>
+__device__ __forceinline__ void store_thread_row(T* dst, int E, const float (&x)[EM]) {
+  constexpr int V = 16 / sizeof(T) < EM ? 16 / sizeof(T) : EM;
+  struct alignas(16) Pack { T v[16 / sizeof(T)]; };
+#pragma unroll
+  for (int q = 0; q < EM / V; ++q) {
+    if (VEC) {
+      Pack pk;
+#pragma unroll
+      for (int i = 0; i < V; ++i) pk.v[i] = static_cast<T>(x[q * V + i]);
+      if (q * V < E) *reinterpret_cast<Pack*>(dst + q * V) = pk;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (q * V + i < E) dst[q * V + i] = static_cast<T>(x[q * V + i]);
+    }
+  }
+}
+
 // Shared memory of a routing block: the bitmap, each warp's probability sums, the experts' first
 // rows (one-chunk calls), the count of live rows.
 struct RouteShared {
@@ -290,19 +330,21 @@ __device__ __forceinline__ void choose_by_rounds(const T* src, int E, int k, int
 // reads: 131071 rows of 256, k = 8, in 92 us with the two launches after it, 235 by rounds alone;
 // their bytes take 22 us.  Threads that hold whole or half rows of a tile in shared memory need 230
 // to 300 instructions a row, but leave 5 to 10 warps on an SM and measured 128 and 99 us.
-template <typename T, int VPL, bool VEC>
-__global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) route_rows_kernel(const RouteParams p) {
+// WARPS: 8, or 32 for chunks of 32 tokens that do not fill the SMs: a row's chain of steps, about a
+// microsecond, then passes once.
+template <typename T, int VPL, bool VEC, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) route_rows_kernel(const RouteParams p) {
   using Map = RowMap<T, VPL>;
   extern __shared__ uint32_t route_smem[];
-  __shared__ uint64_t list[kRouteWarps][kRouteCandidates];
+  __shared__ uint64_t list[WARPS][kRouteCandidates];
   const int E = p.experts, k = p.top_k, words = p.chunk / 32;
-  const RouteShared s(route_smem, E, words, kRouteWarps);
+  const RouteShared s(route_smem, E, words, WARPS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t below = (1u << lane) - 1u;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.chunk;
   const int rows = static_cast<int>(p.tokens - t0 < p.chunk ? p.tokens - t0 : p.chunk);
 
-  for (int i = threadIdx.x; i < E * words; i += kRouteThreads) s.bitmap[i] = 0u;
+  for (int i = threadIdx.x; i < E * words; i += 32 * WARPS) s.bitmap[i] = 0u;
   if (threadIdx.x == 0) *s.live = 0;
   __syncthreads();
 
@@ -313,12 +355,12 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
   auto source = [&](int r) { return static_cast<const T*>(p.logits) + (t0 + r) * p.ld; };
   auto routed = [&](int r) { return p.mask == nullptr || p.mask[t0 + r] != 0; };
   if (warp < rows) load_row<T, VPL, VEC>(source(warp), E, lane, routed(warp), next);
-  for (int r = warp; r < rows; r += kRouteWarps) {
+  for (int r = warp; r < rows; r += WARPS) {
     float x[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) x[v] = next[v];
-    if (r + kRouteWarps < rows)   // the next row's loads fly while this one is worked on
-      load_row<T, VPL, VEC>(source(r + kRouteWarps), E, lane, routed(r + kRouteWarps), next);
+    if (r + WARPS < rows)   // the next row's loads fly while this one is worked on
+      load_row<T, VPL, VEC>(source(r + WARPS), E, lane, routed(r + WARPS), next);
     float best = x[0];
 #pragma unroll
     for (int v = 1; v < VPL; ++v) best = max_nan(best, x[v]);
@@ -400,13 +442,13 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
   for (int v = 0; v < VPL; ++v)
     if (Map::expert(v, lane) < E) s.prob[warp * E + Map::expert(v, lane)] = acc[v];
   if (lane == 0 && live > 0) atomicAdd(s.live, live);
-  finish_chunk(p, s, words, kRouteWarps, t0, rows);
+  finish_chunk(p, s, words, WARPS, t0, rows);
 }
 
 // A thread per row, for up to 32 experts: the logits, their keys and the k rounds stay in one
 // thread's registers, with no exchange between lanes but for the probability sums.  A block has a
 // thread per token of its chunk; choices pass through shared memory so that they leave in order.
-template <typename T, int EM>
+template <typename T, int EM, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads) route_rows_small_kernel(const RouteParams p) {
   extern __shared__ uint32_t route_smem[];
   const int E = p.experts, k = p.top_k, words = p.chunk / 32, warps = words;
@@ -425,9 +467,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_rows_small_kernel(const R
   const T* src = static_cast<const T*>(p.logits) + (t0 + r) * p.ld;
   float x[EM];
   uint32_t key[EM], top_key = 0u;
+  load_thread_row<T, EM, VEC>(src, E, on, x);
 #pragma unroll
   for (int e = 0; e < EM; ++e) {
-    x[e] = (on && e < E) ? logit_value<T>(src[e]) : closed_logit();
     key[e] = e < E ? order_key(x[e]) : 0u;
     top_key = key[e] > top_key ? key[e] : top_key;
   }
@@ -529,21 +571,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_scan_kernel(const RoutePa
   }
 }
 
-// Rows of a chunk's choices: the rank inside the chunk, the chunk's offset inside the expert and
-// the expert's first row.  The last block writes R and the loss too.  (No chunks: counts, totals
-// and loss of no tokens.)
-__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteParams p) {
-  extern __shared__ uint32_t route_smem[];
-  int32_t* first = reinterpret_cast<int32_t*>(route_smem);   // E: first row of each expert
+// Exclusive sums of totals[0 .. E) added to first[0 .. E), by a whole block; returns their sum.
+__device__ __forceinline__ int32_t add_first_rows(const int32_t* totals, int32_t* first, int E) {
   __shared__ int32_t warp_total[kRouteWarps];
-  __shared__ float warp_loss[kRouteWarps];
-  const int E = p.experts, k = p.top_k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  ptx::griddep_wait();
   int32_t before = 0;
   for (int b = 0; b < E; b += kRouteThreads) {
     const int e = b + static_cast<int>(threadIdx.x);
-    const int32_t c = e < E ? p.counts[e] : 0;
+    const int32_t c = e < E ? totals[e] : 0;
     int32_t incl = c;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -557,24 +592,36 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteP
       if (w < warp) add += warp_total[w];
       all += warp_total[w];
     }
-    if (e < E) first[e] = add + incl - c + (p.chunks > 0 ? p.part_count[static_cast<int64_t>(e) * p.chunks + blockIdx.x] : 0);
+    if (e < E) first[e] += add + incl - c;
     before += all;
     __syncthreads();
   }
-  if (blockIdx.x == gridDim.x - 1) {
-    const int32_t live = p.totals[1];
-    float s = 0.0f;
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) s = fmaf(static_cast<float>(p.counts[e]), p.prob[e], s);
-    s = warp_sum(s);
-    if (lane == 0) warp_loss[warp] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float all = 0.0f;
-      for (int w = 0; w < kRouteWarps; ++w) all += warp_loss[w];
-      p.totals[0] = before;
-      *p.loss = before > 0 ? p.coef * static_cast<float>(E) * (all / static_cast<float>(before) / static_cast<float>(live)) : 0.0f;
-    }
+  return before;
+}
+
+// R and the loss from the counts and the probability sums, by a whole block.
+__device__ __forceinline__ void write_totals(const RouteParams& p, const int32_t* counts, const float* prob, int32_t rows,
+                                             int32_t live) {
+  __shared__ float warp_loss[kRouteWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float s = 0.0f;
+  for (int e = threadIdx.x; e < p.experts; e += kRouteThreads) s = fmaf(static_cast<float>(counts[e]), prob[e], s);
+  s = warp_sum(s);
+  if (lane == 0) warp_loss[warp] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float all = 0.0f;
+    for (int w = 0; w < kRouteWarps; ++w) all += warp_loss[w];
+    p.totals[0] = rows;
+    p.totals[1] = live;
+    *p.loss = rows > 0 ? p.coef * static_cast<float>(p.experts) * (all / static_cast<float>(rows) / static_cast<float>(live)) : 0.0f;
   }
+}
+
+// Rows of a chunk's choices: the rank inside the chunk and first[e], the first row of the chunk's part of
+// the expert.
+__device__ __forceinline__ void place_chunk(const RouteParams& p, const int32_t* first) {
+  const int k = p.top_k;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.chunk;
   const int64_t left = static_cast<int64_t>(p.tokens) - t0;
   const int rows = static_cast<int>(left < p.chunk ? left : p.chunk);
@@ -582,6 +629,56 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteP
     const int e = p.expert[t0 * k + i];
     if (e >= 0) p.row[t0 * k + i] += first[e];
   }
+}
+
+// After route_scan_kernel.  The last block writes R and the loss too.  (No chunks: counts, totals and
+// loss of no tokens.)
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteParams p) {
+  extern __shared__ uint32_t route_smem[];
+  int32_t* first = reinterpret_cast<int32_t*>(route_smem);   // E
+  ptx::griddep_wait();
+  for (int e = threadIdx.x; e < p.experts; e += kRouteThreads)
+    first[e] = p.chunks > 0 ? p.part_count[static_cast<int64_t>(e) * p.chunks + blockIdx.x] : 0;
+  const int32_t rows = add_first_rows(p.counts, first, p.experts);   // (a thread adds to what it wrote)
+  if (blockIdx.x == gridDim.x - 1) write_totals(p, p.counts, p.prob, rows, p.totals[1]);
+  place_chunk(p, first);
+}
+
+// Few chunks: every block sums the chunks' counts itself, a thread per expert, which costs less than a
+// launch of its own for the prefix sums.
+constexpr int kFewChunks = 16;
+__global__ void __launch_bounds__(kRouteThreads) route_sum_place_kernel(const RouteParams p) {
+  extern __shared__ uint32_t route_smem[];
+  const int E = p.experts;
+  int32_t* first = reinterpret_cast<int32_t*>(route_smem);            // E
+  int32_t* total = first + E;                                         // E + 1: counts, live rows
+  float* prob = reinterpret_cast<float*>(total + E + 1);              // E (the last block's)
+  const bool last = blockIdx.x == gridDim.x - 1;
+  ptx::griddep_wait();
+  for (int e = threadIdx.x; e <= E; e += kRouteThreads) {
+    const int32_t* count = p.part_count + static_cast<int64_t>(e) * p.chunks;
+    const float* part = p.part_prob + static_cast<int64_t>(e) * p.chunks;
+    int32_t before = 0, all = 0;
+    float s = 0.0f;
+#pragma unroll
+    for (int b = 0; b < kFewChunks; ++b) {
+      const bool in = b < p.chunks;
+      const int32_t c = in ? count[b] : 0;
+      all += c;
+      if (b < static_cast<int>(blockIdx.x)) before += c;
+      if (in && last && e < E) s += part[b];
+    }
+    total[e] = all;
+    if (e < E) {
+      first[e] = before;
+      prob[e] = s;
+      if (last) p.counts[e] = all;
+    }
+  }
+  __syncthreads();
+  const int32_t rows = add_first_rows(total, first, E);
+  if (last) write_totals(p, total, prob, rows, total[E]);
+  place_chunk(p, first);
 }
 
 // d_l = p (g - <p, g>) with g_e = dL coef E c_e / (R n), the counts held fixed, plus the weights'
@@ -680,7 +777,7 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
 }
 
 // A thread per row, for up to 32 experts.
-template <typename T, int EM>
+template <typename T, int EM, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads) route_grad_small_kernel(const RouteGradParams p) {
   __shared__ float g[EM];
   const int E = p.experts, k = p.top_k;
@@ -694,11 +791,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_grad_small_kernel(const R
   T* dst = static_cast<T*>(p.d_logits) + t * p.d_ld;
   float x[EM];
   float top = closed_logit();
+  load_thread_row<T, EM, VEC>(src, E, on, x);
 #pragma unroll
-  for (int e = 0; e < EM; ++e) {
-    x[e] = (on && e < E) ? logit_value<T>(src[e]) : closed_logit();
-    top = max_nan(top, x[e]);
-  }
+  for (int e = 0; e < EM; ++e) top = max_nan(top, x[e]);
   const RowExp ex(top);
   const bool live = top != closed_logit();
   float sum = 0.0f, dot = 0.0f, chosen_sum = 0.0f, chosen_dot = 0.0f;
@@ -735,9 +830,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_grad_small_kernel(const R
       const float pe = x[e] * inv;
       float d = p.normalize ? pe * (g[e] - dot) : pe * (g[e] + add[e] - dot);
       if (p.normalize && ((taken >> e) & 1u)) d = fmaf(x[e] * over, add[e] - chosen_dot, d);
-      dst[e] = static_cast<T>(live ? d : 0.0f);
+      x[e] = live ? d : 0.0f;
     }
   }
+  store_thread_row<T, EM, VEC>(dst, E, x);
 }
 
 }  // namespace tst
