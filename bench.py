@@ -96,8 +96,8 @@ L2_FLUSH_BYTES = 512 << 20
 L2_BYTES = 128 << 20      # GB300's L2 (126.5 MiB), rounded up
 MAX_SETS = 16             # more input sets than this: flush L2 before every launch instead
 KERNEL_SOURCES = ["gemm_kernel.cuh", "ptx.cuh", "kernel_params.h", "tile_sched.h", "epilogue_ext.cuh"]
-# the block-scaled kernel reuses the plain kernel's producer and helpers
-BS_KERNEL_SOURCES = KERNEL_SOURCES + ["gemm_blockscale.cuh", "gemm_bs.cu"]
+# the block-scaled kernels reuse the plain kernel's helpers
+BS_KERNEL_SOURCES = KERNEL_SOURCES + ["gemm_blockscale.cuh", "gemm_bs.cu", "group_walk.cuh", "gemm_bs_tile.cuh", "gemm_bst.cu"]
 
 
 PLAN_OPTION_KEYS = ("sk_groups", "bk", "stages", "num_ctas", "sk_forward", "sk_fixup", "l2_hint", "tma_boxes",
