@@ -9,8 +9,11 @@
 //   warps 0-3   producer, MMA issuers 0 and 1 (k-blocks of even and odd count, each into its own
 //               partial, so that one waits while the other's MMAs run), and a warp that fills the
 //               group table
-//   warps 4-11  accumulate: two per TMEM quadrant, 128 columns each, 32 at a time (a second load in
-//               flight spills: 640 cycles per 64 columns against 170)
+//   warps 4-11  accumulate: two per TMEM quadrant, 128 columns each, 16 at a time with the next 16's
+//               load in flight (32 and 32 spill: 640 cycles per 64 columns against 170)
+// 16384 rows over 16 experts of 4096 x 4096 (550 GFLOP): 257 us, 0.56 of twice the measured BF16 rate;
+// 330 with 128 x 128 tiles.  What bounds it now is the accumulating warps' chain per k-block (750
+// cycles: 340 adding, the rest waiting, handing over and storing) before the 768 of its loads.
 #pragma once
 #include "gemm_bs_tile.cuh"
 
@@ -137,12 +140,22 @@ __device__ __forceinline__ void run_epilogue_wide(const KernelParams& p, const C
       nb = __ldg(sb_row + kn);
       wait_partial();
       if (!ok) break;
+      const uint32_t taddr = taddr0 + (q & 1u) * 256u;
+      uint32_t va[16], vb[16];
+      auto fold = [&](const uint32_t (&v)[16], float* sum) {
 #pragma unroll
-      for (int chunk = 0; chunk < 4; ++chunk) {
-        float v[32];
-        ptx::tmem_load_32cols(taddr0 + (q & 1u) * 256u + static_cast<uint32_t>(32 * chunk), v);
-        if (chunk == 3) release();   // the partial's last columns are in registers
-        bs_fold_shared(s, v, r + 32 * chunk);
+        for (int i = 0; i < 16; i += 2) ptx::fma_f32x2_after(sum[i], sum[i + 1], s, v[i], v[i + 1]);
+      };
+      ptx::tmem_load_16cols_async(taddr, va);
+#pragma unroll
+      for (int chunk = 0; chunk < 8; chunk += 2) {
+        ptx::tmem_wait_loads();
+        ptx::tmem_load_16cols_async(taddr + static_cast<uint32_t>(16 * (chunk + 1)), vb);
+        fold(va, r + 16 * chunk);
+        ptx::tmem_wait_loads();
+        if (chunk < 6) ptx::tmem_load_16cols_async(taddr + static_cast<uint32_t>(16 * (chunk + 2)), va);
+        else release();   // the partial's last columns are in registers
+        fold(vb, r + 16 * (chunk + 1));
       }
       ++q;
     }
