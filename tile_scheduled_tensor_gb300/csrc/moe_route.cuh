@@ -693,7 +693,9 @@ __device__ __forceinline__ float grad_scale(const RouteGradParams& p) {
 }
 
 // A warp per row; the chosen experts' parts pass through a row of shared memory to the lanes that
-// hold those experts.  Bound by memory: the logits in, the gradient out.
+// hold those experts.  Bound by memory, the logits in and the gradient out, with a row's chain of loads,
+// exponentials and sums over the lanes hidden behind the other warps': 65536 x 256 float32 in 27.8 us,
+// 0.73 of the copy rate.  The sums over the lanes go together, one latency for all of them.
 template <typename T, int VPL, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) route_grad_kernel(const RouteGradParams p) {
   using Map = RowMap<T, VPL>;
@@ -712,17 +714,28 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
   __syncwarp();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps;
   auto routed = [&](int64_t t) { return p.mask == nullptr || p.mask[t] != 0; };
+  // Row t's choice of this lane, and that expert's logit: read a row ahead, where the registers for it
+  // are there (65536 x 256: in bf16 24.8 us with the spills it costs, 22.5 without; in float32 27.8 against
+  // 29.1; 65536 x 512: 49 us against 65 in bf16, 52 against 57 in float32).
+  constexpr bool kAhead = sizeof(T) == 4 || VPL != 8;
+  auto choice = [&](int64_t t) { return t < p.tokens && lane < k ? p.expert[t * k + lane] : -1; };
+  auto logit_of = [&](int64_t t, int c) {
+    return c >= 0 && c < E ? logit_value<T>(static_cast<const T*>(p.logits)[t * p.ld + c]) : 0.0f;
+  };
   float next[VPL];
   int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+  int chosen_next = kAhead ? choice(t) : -1;
+  float logit_next = logit_of(t, chosen_next);
   if (t < p.tokens) load_row<T, VPL, VEC>(static_cast<const T*>(p.logits) + t * p.ld, E, lane, routed(t), next);
   for (; t < p.tokens; t += step) {
-    const T* src = static_cast<const T*>(p.logits) + t * p.ld;
     T* dst = static_cast<T*>(p.d_logits) + t * p.d_ld;
     float e[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) e[v] = next[v];
-    int chosen = lane < k ? p.expert[t * k + lane] : -1;
-    float dw = (lane < k && p.d_weight != nullptr) ? p.d_weight[t * k + lane] : 0.0f;
+    int chosen = kAhead ? chosen_next : choice(t);
+    const float logit = kAhead ? logit_next : logit_of(t, chosen);
+    float dw = lane < k && p.d_weight != nullptr ? p.d_weight[t * k + lane] : 0.0f;
+    if constexpr (kAhead) chosen_next = choice(t + step);
     if (t + step < p.tokens)
       load_row<T, VPL, VEC>(static_cast<const T*>(p.logits) + (t + step) * p.ld, E, lane, routed(t + step), next);
     float best = e[0];
@@ -733,11 +746,12 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
 #pragma unroll
       for (int v = 0; v < VPL; ++v) e[v] = 0.0f;
       store_row<T, VPL, VEC>(dst, E, lane, e);
+      if constexpr (kAhead) logit_next = logit_of(t + step, chosen_next);
       continue;
     }
     if (chosen >= E) chosen = -1;
     float ew = 0.0f;
-    if (chosen >= 0) ew = ex.any(logit_value<T>(src[chosen]));
+    if (chosen >= 0) ew = ex.any(logit);
     else dw = 0.0f;
     float sum = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -747,16 +761,26 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
       sum += e[v];
       dot = fmaf(e[v], g[v], dot);
     }
-    sum = warp_sum(sum);
-    if (p.normalize) {
-      const float w = ew * __fdividef(1.0f, warp_sum(ew));
-      dw = w * (dw - warp_sum(w * dw));   // already the gradient of the chosen logits
-    } else {
-      dot = fmaf(ew, dw, dot);
+    // the sums that the row needs in one pass over the lanes, so that their latencies overlap
+    float kept = ew, kept_dot = ew * dw;
+    if (!p.normalize) dot += kept_dot;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+      sum += __shfl_xor_sync(kFullMask, sum, m);
+      dot += __shfl_xor_sync(kFullMask, dot, m);
+      if (p.normalize) {
+        kept += __shfl_xor_sync(kFullMask, kept, m);
+        kept_dot += __shfl_xor_sync(kFullMask, kept_dot, m);
+      }
     }
     const float inv = __fdividef(1.0f, sum);
-    dot = warp_sum(dot) * inv;
+    dot *= inv;
+    if (p.normalize) {
+      const float over = __fdividef(1.0f, kept);
+      dw = ew * over * (dw - kept_dot * over);   // already the gradient of the chosen logits
+    }
     if (chosen >= 0) part[chosen] = dw;
+    if constexpr (kAhead) logit_next = logit_of(t + step, chosen_next);
     __syncwarp();
 #pragma unroll
     for (int q = 0; q < VPL / Map::W; ++q) {
