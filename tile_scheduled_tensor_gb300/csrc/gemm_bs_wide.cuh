@@ -35,7 +35,9 @@ constexpr int kWideRoleRegs = 56, kWideSumRegs = 224;
 static_assert(128 * kWideRoleRegs + 256 * kWideSumRegs <= kBsTileThreads * kTileLaunchRegs, "the split fits the launch");
 
 // MMA issuer r, one thread: the k-blocks whose count over this CTA's tiles has parity r, each into
-// partial r.  Each stage has one reader, which commits EMPTY.
+// partial r.  Each stage has one reader, which commits EMPTY.  PEMPTY is waited for before FULL: it shows
+// that every k-block up to q - 2 has landed, without which a ring of three stages could take FULL's
+// parity for an earlier use's.
 __device__ __forceinline__ void wide_mma(const KernelParams& p, const Ctx& c, Walk walk, uint32_t r, uint32_t tmem_base,
                                          uint32_t smem_a, uint32_t smem_b, uint32_t bar_full, uint32_t bar_empty,
                                          uint32_t bar_pfull, uint32_t bar_pempty, uint32_t bar_drain) {
