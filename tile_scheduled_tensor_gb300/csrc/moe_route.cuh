@@ -321,13 +321,22 @@ __device__ __forceinline__ void choose_by_rounds(const T* src, int E, int k, int
   }
 }
 
+// A logit that may be among a row's k largest; none is NaN.
+struct alignas(8) Candidate {
+  float logit;
+  int32_t expert;
+  __device__ __forceinline__ bool before(const Candidate& c) const {
+    return logit > c.logit || (logit == c.logit && expert < c.expert);
+  }
+};
+
 // A warp per row, rows dealt to the block's warps in turn.  The choice: k - 1 rounds of a warp
 // maximum over the lanes' own maxima leave a bound that at least k logits reach; those that do,
-// seldom more than a few over k, go to a list in shared memory with their experts in the low word,
+// seldom more than a few over k, go to a list in shared memory with their experts,
 // and each finds its rank by comparing itself with the others.  Rounds over all logits remain for rows with
 // more than 32 on the list, NaN, infinities or magnitudes over 2^100.  What bounds it is issue slots
 // (about 69 % of them used, 450 instructions for a row of 256 logits), not the 1 KB that the row
-// reads: 131071 rows of 256, k = 8, in 92 us with the two launches after it, 235 by rounds alone;
+// reads: 131071 rows of 256, k = 8, in 83 us with the two launches after it, 235 by rounds alone;
 // their bytes take 22 us.  Threads that hold whole or half rows of a tile in shared memory need 230
 // to 300 instructions a row, but leave 5 to 10 warps on an SM and measured 128 and 99 us.
 // WARPS: 8, or 32 for chunks of 32 tokens that do not fill the SMs: a row's chain of steps, about a
@@ -336,7 +345,7 @@ template <typename T, int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) route_rows_kernel(const RouteParams p) {
   using Map = RowMap<T, VPL>;
   extern __shared__ uint32_t route_smem[];
-  __shared__ uint64_t list[WARPS][kRouteCandidates];
+  __shared__ alignas(16) Candidate list[WARPS][kRouteCandidates + 4];   // and up to 4 that come last
   const int E = p.experts, k = p.top_k, words = p.chunk / 32;
   const RouteShared s(route_smem, E, words, WARPS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -397,28 +406,31 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
           const uint32_t who = __ballot_sync(kFullMask, has);
           const int slot = n + __popc(who & below);
           if (has && slot < kRouteCandidates)
-            list[warp][slot] = (static_cast<uint64_t>(order_key(x[v])) << 32) |
-                               (0xFFFFFFFFu - static_cast<uint32_t>(Map::expert(v, lane)));
+            list[warp][slot] = {x[v], Map::expert(v, lane)};
           n += __popc(who);
         }
         listed = n <= kRouteCandidates;
+        if (lane < 4 && listed) list[warp][n + lane] = {closed_logit(), E};
         __syncwarp();
         if (listed) {
           // two lanes per listed logit share the comparisons when at most 16 are listed
           const bool halves = n <= 16;
           const int mine = halves ? lane & 15 : lane;
-          const uint64_t c = mine < n ? list[warp][mine] : 0u;
-          const int share = halves ? (n + 1) >> 1 : n;
-          const int from = halves && lane >= 16 ? share : 0;
+          const Candidate c = list[warp][mine];   // from the n-th on: not used
+          const int share = halves ? (n + 3) >> 2 : (n + 1) >> 1;   // pairs
+          const int4* pair = reinterpret_cast<const int4*>(list[warp]) + (halves && lane >= 16 ? share : 0);
           int rank = 0;
-          for (int i = 0; i < share; ++i)
-            if (from + i < n && list[warp][from + i] > c) ++rank;
+          for (int i = 0; i < share; ++i) {
+            const int4 two = pair[i];
+            if (Candidate{__int_as_float(two.x), two.y}.before(c)) ++rank;
+            if (Candidate{__int_as_float(two.z), two.w}.before(c)) ++rank;
+          }
           if (halves) rank += __shfl_xor_sync(kFullMask, rank, 16);
           if (lane < n) {
             at = rank;   // from the k-th on: no place; the other lanes keep theirs, -1 where fewer than k are open
             if (rank < k) {
-              chosen = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(c));
-              w = ex.fast(key_value(static_cast<uint32_t>(c >> 32)));
+              chosen = c.expert;
+              w = ex.fast(c.logit);
             }
           }
         }
