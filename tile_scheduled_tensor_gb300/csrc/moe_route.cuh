@@ -334,8 +334,8 @@ struct alignas(8) Candidate {
 // maximum over the lanes' own maxima leave a bound that at least k logits reach; those that do,
 // seldom more than a few over k, go to a list in shared memory with their experts,
 // and each finds its rank by comparing itself with the others.  Rounds over all logits remain for rows with
-// more than 32 on the list, NaN, infinities or magnitudes over 2^100.  What bounds it is issue slots
-// (about 69 % of them used, 450 instructions for a row of 256 logits), not the 1 KB that the row
+// more than 32 on the list, NaN, infinities or magnitudes over 2^100.  What bounds it is a row's chain of
+// steps and the issue slots (some 400 instructions for a row of 256 logits), not the 1 KB that the row
 // reads: 131071 rows of 256, k = 8, in 83 us with the two launches after it, 235 by rounds alone;
 // their bytes take 22 us.  Threads that hold whole or half rows of a tile in shared memory need 230
 // to 300 instructions a row, but leave 5 to 10 warps on an SM and measured 128 and 99 us.
