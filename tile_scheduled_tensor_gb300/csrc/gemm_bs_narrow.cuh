@@ -59,8 +59,7 @@ __device__ __forceinline__ void narrow_mma(const KernelParams& p, const Ctx& c, 
   uint32_t phase = 0, buf_phase = 0;
   bool ok = true;
   long long wait_full = 0, wait_pempty = 0, kblocks = 0;
-  Tile w;
-  while (ok && walk.next(w)) {
+  while (ok && walk.skip()) {
     for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
       const long long t0 = p.stats ? clock64() : 0;
       if (!wait_phase<1>(p, c, bar_pempty + 8 * buf, buf_phase ^ 1u, ROLE_MMA)) { ok = false; break; }

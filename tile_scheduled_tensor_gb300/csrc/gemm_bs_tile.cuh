@@ -86,9 +86,8 @@ struct WalkK {
   Walk walk;
   int32_t kt;
   __device__ __forceinline__ bool next(int32_t& k_count) {
-    Tile w;
     k_count = kt;
-    return walk.next(w);
+    return walk.skip();
   }
 };
 

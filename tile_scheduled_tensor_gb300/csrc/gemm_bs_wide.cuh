@@ -51,8 +51,7 @@ __device__ __forceinline__ void wide_mma(const KernelParams& p, const Ctx& c, Wa
   long long wait_full = 0, wait_pempty = 0;   // role-cycle counters (debug)
   const bool stats = p.stats != nullptr && r == 0;
   const int nkb = p.sched.kt;
-  Tile w;
-  while (ok && walk.next(w)) {
+  while (ok && walk.skip()) {
     for (int kb = 0; kb < nkb; ++kb, ++q) {
       if ((q & 1u) == r) {
         const long long t0 = stats ? clock64() : 0;

@@ -99,9 +99,21 @@ struct Walk {
       if (at >= s.dp_tiles) return false;
     } else {
       if (at >= t.tile0[s.groups]) return false;
-      while (at >= t.tile0[g + 1]) ++g;
+      int32_t past;
+      do {   // four groups' ends at once: their loads' latency passes once
+        past = 0;
+#pragma unroll
+        for (int32_t i = 1; i <= 4; ++i) past += at >= t.tile0[g + i < s.groups ? g + i : s.groups] ? 1 : 0;
+        g += past;
+      } while (past == 4);
     }
     take(w);
+    return true;
+  }
+  // for roles that count tiles only
+  __device__ __forceinline__ bool skip() {
+    if (at >= (s.groups == 0 ? s.dp_tiles : t.tile0[s.groups])) return false;
+    at += s.grid;
     return true;
   }
   __device__ __forceinline__ bool next_warp(Tile& w) {
