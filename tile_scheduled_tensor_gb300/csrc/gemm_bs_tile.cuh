@@ -13,7 +13,7 @@
 //     130 cycles there, 266 under a test of the lane number (measured; the 4 MMAs of a k-block
 //     are 256 cycles of tensor-core work).
 //
-// 8192 x 8192 x 8192 in 541 us, 0.53 of twice the measured BF16 rate (the general form: 789).  Bound by the
+// 8192 x 8192 x 8192 in 536 us, 0.54 of twice the measured BF16 rate (the general form: 789).  Bound by the
 // 32 KB per k-block that come in by TMA, 512 cycles, and the handshakes that the accumulation adds.
 #pragma once
 #include "gemm_blockscale.cuh"
