@@ -100,11 +100,14 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// e^(x - top).  Between kPlainTop and -kPlainTop, 2^(x log2 e - top log2 e) with one fused step:
-// the rounding of top log2 e is a factor common to the row, which the division by the row's sum
-// takes out, and the step's own rounding is |x - top| 2^-24 relative.  Beyond, where top log2 e
-// may overflow, and for infinities and NaN: __expf of the difference.
-constexpr float kPlainTop = 1.26765060e30f;   // 2^100
+// e^(x - top).  For |top| below kPlainTop, 2^(x log2 e - top log2 e) with one fused step: the rounding
+// of top log2 e, at most 2^-4 there (half a unit in the last place of what lies below 2^21), is a
+// factor between 0.95 and 1.05 common to the row, which the division by the row's sum takes out, and
+// the step's own rounding is |x - top| 2^-24 relative.  The bound keeps that factor near one: it is up
+// to 2^(|top| log2 e 2^-24), which overflows FP32 or vanishes from |top| = 2^30 on.  Beyond, and for
+// infinities and NaN: __expf of the difference, which is exact for logits within a factor of two of
+// the top.
+constexpr float kPlainTop = 1048576.0f;   // 2^20
 constexpr float kLog2e = 1.44269504088896341f;
 struct RowExp {
   float top, shift;
@@ -334,7 +337,7 @@ struct alignas(8) Candidate {
 // maximum over the lanes' own maxima leave a bound that at least k logits reach; those that do,
 // seldom more than a few over k, go to a list in shared memory with their experts,
 // and each finds its rank by comparing itself with the others.  Rounds over all logits remain for rows with
-// more than 32 on the list, NaN, infinities or magnitudes over 2^100.  What bounds it is a row's chain of
+// more than 32 on the list, NaN, infinities or a top of 2^20 or more in magnitude.  What bounds it is a row's chain of
 // steps and the issue slots (some 400 instructions for a row of 256 logits), not the 1 KB that the row
 // reads: 131071 rows of 256, k = 8, in 83 us with the two launches after it, 235 by rounds alone;
 // their bytes take 22 us.  Threads that hold whole or half rows of a tile in shared memory need 230
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
         for (int v = 0; v < VPL; ++v) { e[v] = ex.any(x[v]); sum += Map::expert(v, lane) < E ? e[v] : 0.0f; }
       }
       sum = warp_sum(sum);
-      const float inv = __fdividef(1.0f, sum);   // 1 <= sum <= 1024, or NaN
+      const float inv = __fdividef(1.0f, sum);   // 0.95 <= sum <= 1075 (RowExp), or NaN
 #pragma unroll
       for (int v = 0; v < VPL; ++v) acc[v] = fmaf(e[v], inv, acc[v]);
 
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
         if (chosen >= 0) w = ex.any(value);
       }
       const float over = p.normalize ? warp_sum(w) : sum;
-      w = chosen >= 0 ? __fdividef(w, over) : 0.0f;   // 1 <= over <= 1024, or NaN
+      w = chosen >= 0 ? __fdividef(w, over) : 0.0f;   // 0.95 <= over <= 1075, or NaN
       if (chosen >= 0) atomicOr(&s.bitmap[chosen * words + (r >> 5)], 1u << (r & 31));
     }
     if (at < k) {
