@@ -95,12 +95,18 @@ __device__ __forceinline__ void narrow_mma(const KernelParams& p, const Ctx& c, 
   }
 }
 
-// r[q] += f[q] * v[q], f read by broadcast four at a time
-template <int N>
-__device__ __forceinline__ void narrow_fold(const float* f, const float (&v)[N], float* r) {
+// r[q] += f[q] * v[q], or with one scale of B per column (f[q] * sb) * v[q]: the scales' product first,
+// as in the other forms, since either scale times a partial may leave FP32's range where the product does
+// not.  f is read by broadcast four at a time.
+template <int N, bool SHARED>
+__device__ __forceinline__ void narrow_fold(const float* f, float sb, const float (&v)[N], float* r) {
 #pragma unroll
   for (int q = 0; q < N; q += 4) {
-    const float4 a = *reinterpret_cast<const float4*>(f + q);
+    float4 a = *reinterpret_cast<const float4*>(f + q);
+    if constexpr (!SHARED) {
+      ptx::mul_f32x2(a.x, a.y, sb, sb, a.x, a.y);
+      ptx::mul_f32x2(a.z, a.w, sb, sb, a.z, a.w);
+    }
     ptx::fma_f32x2(r[q], r[q + 1], a.x, a.y, v[q], v[q + 1]);
     ptx::fma_f32x2(r[q + 2], r[q + 3], a.z, a.w, v[q + 2], v[q + 3]);
   }
@@ -185,11 +191,7 @@ __device__ __forceinline__ void narrow_epilogue(const KernelParams& p, const Ctx
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar_pempty + 8 * buf);   // the partials are in registers
-            if constexpr (!SHARED) {
-#pragma unroll
-              for (int i = 0; i < NT; i += 2) ptx::mul_f32x2(v[i], v[i + 1], sb[j], sb[j], v[i], v[i + 1]);
-            }
-            narrow_fold(win + j * NT, v, r);
+            narrow_fold<NT, SHARED>(win + j * NT, SHARED ? 1.0f : sb[j], v, r);
             if (++buf == Cfg::BUFS) { buf = 0; buf_phase ^= 1u; }
             if (stat_thread) busy += clock64() - t1;
           }
