@@ -59,6 +59,15 @@ size_t route_smem(int32_t experts, int32_t top_k, int32_t chunk, int32_t warps) 
   return (static_cast<size_t>(experts) * (chunk / 32 + warps + 1) + 1 + staged) * 4;
 }
 
+// Zero device memory before returning, on a stream of its own: cudaMemset is ordered with the default
+// stream alone and may run after this returns, when a run on another stream has written there.
+bool zero_now(void* p, size_t bytes) {
+  cudaStream_t s;
+  if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess) return false;
+  const bool ok = cudaMemsetAsync(p, 0, bytes, s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+  return cudaStreamDestroy(s) == cudaSuccess && ok;
+}
+
 tst_status launched() {
   if (cudaGetLastError() != cudaSuccess) return TST_ERR_CUDA;
   return TST_OK;
@@ -238,7 +247,8 @@ tst_status moe_plan_create(tst_moe_plan** out, int64_t max_tokens, int32_t exper
       delete p;
       return TST_ERR_OOM;
     }
-    if (cudaMemset(p->dev_block, 0, 256) != cudaSuccess) {
+    if (!zero_now(p->dev_block, 256)) {
+      cudaGetLastError();
       cudaFree(p->dev_block);
       delete p;
       return TST_ERR_CUDA;
@@ -280,7 +290,7 @@ tst_status moe_status_query(tst_moe_plan* p) {
   if (cudaStreamSynchronize(p->last_stream) != cudaSuccess ||
       cudaMemcpy(&word, p->d_status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
     return TST_ERR_CUDA;
-  if (word != 0 && cudaMemset(p->d_status, 0, sizeof(word)) != cudaSuccess) return TST_ERR_CUDA;
+  if (word != 0 && !zero_now(p->d_status, sizeof(word))) return TST_ERR_CUDA;   // before any later run
   return word == 0 ? TST_OK : TST_ERR_DEVICE_CHECK;
 }
 
