@@ -583,8 +583,9 @@ tst_status gemm_plan_set_debug(tst_plan *plan, int32_t flags, void *trace_buf, i
  * The gradient of moe_dispatch with respect to x is moe_combine of the rows' gradient
  * without weights.  Each call is asynchronous and ordered on its stream, allocates nothing,
  * and gives the same bits each time for the same inputs.  A plan is not re-entrant (its
- * workspace is per plan): do not run one plan on two streams at once.  Outputs may not
- * overlap inputs. */
+ * workspace is per plan): do not run one plan on two streams at once.  It belongs to the GPU
+ * that was current when it was made: a run with another current GPU is INVALID_ARG.  Outputs
+ * may not overlap inputs. */
 typedef struct tst_moe_plan tst_moe_plan;
 
 typedef struct {

@@ -163,10 +163,17 @@ bool launch(const void* f, int64_t grid, int32_t threads, size_t smem, cudaStrea
   return cudaLaunchKernelExC(&cfg, f, args) == cudaSuccess;
 }
 
-// What every run checks of its plan and token count.
+// What every run checks of its plan and token count; the plan's workspace, and the kernel attributes that
+// its creation raised, are those of one GPU, which has to be the current one.
 tst_status check_run(const tst_moe_plan* p, int64_t tokens, int64_t most) {
   if (p == nullptr || tokens < 0 || tokens > most) return TST_ERR_INVALID_ARG;
-  return TST_OK;
+  if (p->host_only) return TST_OK;
+  int now = -1;
+  if (cudaGetDevice(&now) != cudaSuccess) {
+    cudaGetLastError();
+    return TST_ERR_CUDA;
+  }
+  return now == p->device ? TST_OK : TST_ERR_INVALID_ARG;
 }
 
 tst_status finish(tst_moe_plan* p, cudaStream_t s) {
