@@ -207,8 +207,8 @@ typedef struct {
                             group after another; A's tiles are those of the whole M x K), single CTAs
                             with 128-column tiles (256 too when bk is 128 and br_b a multiple of
                             128) and one-atom k-tiles (bn, cta_group, bk 0 or those values), stages
-                            0 or 2 to the form's most (6; 4 with 256 columns, 5 in the narrow form);
-                            else TST_ERR_UNSUPPORTED.  A grouped plan of at most 512 groups with bn 0
+                            0 or 2 to the form's most (6; 4 with 256 columns, 5 in the narrow form),
+                            M and N at most 2^31 - 256; else TST_ERR_UNSUPPORTED.  A grouped plan of at most 512 groups with bn 0
                             and k-blocks of 128 chooses its form by its sizes: tiles of 16 or 32 rows
                             (bm in tst_plan_info) by 128 columns for at most 48 rows per group on
                             average, else 128 rows by 128 or 256 columns. */

@@ -235,6 +235,9 @@ TileChoice choose_tile(int64_t M, int64_t N, int64_t K, int64_t sizeof_ab, int64
 // 32 rows 105 and 90; 64 rows 120 at 32 and 101 on 128-row tiles.
 int32_t narrow_rows(int64_t rows) { return rows <= 12 ? 16 : rows <= 48 ? 32 : 0; }
 
+// most rows and columns of a block-scaled plan
+constexpr int64_t kBsMaxSize = (int64_t(1) << 31) - 256;
+
 // Hybrid rule: split only the tail wave, and only when it is at most half full.
 int64_t hybrid_split_tiles(int64_t T, int64_t P) {
   const int64_t tail = T % P;
@@ -326,6 +329,8 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
   if (bs) {
     if (epi->ab_block_k != 32 && epi->ab_block_k != 64 && epi->ab_block_k != 128) return TST_ERR_INVALID_ARG;
     if (epi->ab_block_rows < 1 || epi->ab_block_rows_b < 0) return TST_ERR_INVALID_ARG;
+    // a tile's rows and columns are 32-bit, past the matrix too: the last 128 x 256 tile has to end below 2^31
+    if (M > kBsMaxSize || N > kBsMaxSize) return TST_ERR_UNSUPPORTED;
     if (dtype == TST_BF16 || needs_ext(*epi) || shapes != nullptr || (schedule != TST_STATIC && schedule != TST_PERSISTENT) ||
         (o.bn != 0 && o.bn != 128 && !(o.bn == 256 && bs_shared)) || (o.cta_group != 0 && o.cta_group != 1) || (o.bk != 0 && o.bk != 128) ||
         o.cluster_n == 2 || o.pdl || o.epilogue_store == TST_STORE_TMA || o.l2_prefetch)
