@@ -449,7 +449,7 @@ tst_status create_plan(tst_plan** out, int64_t M, int64_t N, int64_t K, tst_dtyp
     const int kdt = dtype == TST_BF16 ? tst::DT_BF16 : tst::DT_E4M3;
     p->kernel = own.kernel  ? own.kernel
                 : bs_shared ? tst_bs_tile_kernel(kernel_out(*p))
-                : p->bs     ? tst_bs_kernel(kernel_out(*p), bs_rows_b(*epi) % 32 != 0)
+                : p->bs     ? tst_bs_kernel(kernel_out(*p), bs_rows_b(*epi) % 32 != 0, groups > 0)
                 : p->ext_on ? tst_kernel_ext(kdt, p->bn, p->cg, p->ka)
                             : tst_kernel(kdt, p->bn, kernel_out(*p), p->cg, p->ka, p->mc);
     if (!p->kernel ||

@@ -43,13 +43,10 @@ constexpr int kBsWarps = 8;     // the accumulating (epilogue) warps, 2-9
 struct PlainWalk {
   const Sched& s;
   WorkIter it;
+  WorkItem w;
   __device__ __forceinline__ PlainWalk(const Sched& sched, int32_t unit) : s(sched) { work_begin(s, unit, it); }
-  __device__ __forceinline__ bool next(int32_t& k_count) {
-    WorkItem w;
-    const bool more = work_next(s, it, w);
-    k_count = more ? w.k_count : 0;
-    return more;
-  }
+  __device__ __forceinline__ bool next() { return work_next(s, it, w); }
+  __device__ __forceinline__ int32_t k_count() const { return w.k_count; }
 };
 
 // MMA issuer r (0 or 1).  The k-blocks of each work item pair up from its first (an odd
@@ -65,7 +62,7 @@ struct PlainWalk {
 // (below 128-wide k-blocks both issuers read every stage, so the plan's EMPTY barriers then
 // count two commits).  Every other k-block keeps an issuer's FULL waits at most two k-tiles
 // apart, so a ring of two stages keeps them unambiguous.  PB = bk / 32 MMAs per k-block.
-// walk: the CTA's work list; next(k) tells whether there is another item and its k-tiles.
+// walk: the CTA's work list; next() moves to the next item, k_count() is its k-tiles.
 template <int PB, typename W>
 __device__ __forceinline__ void run_mma_bs(const KernelParams& p, const Ctx& c, W walk, int r, uint32_t tmem_base,
                                            uint32_t smem_a, uint32_t smem_b, uint32_t bar_full, uint32_t bar_empty,
@@ -84,9 +81,8 @@ __device__ __forceinline__ void run_mma_bs(const KernelParams& p, const Ctx& c, 
   bool ok = true;
   long long wait_full = 0, wait_pempty = 0, kblocks = 0;   // role-cycle counters (debug)
   const bool stats = p.stats != nullptr && r == 0;
-  int32_t k_count = 0;
-  while (ok && walk.next(k_count)) {
-    const int nkb = k_count * PER_ATOM;
+  while (ok && walk.next()) {
+    const int nkb = walk.k_count() * PER_ATOM;
     const int npairs = (nkb + 1) >> 1;
     // this issuer's k-blocks of the item: j = first, first + 2, ...
     const int first = static_cast<int>((kb0 + static_cast<uint32_t>(r)) & 1u);
@@ -129,7 +125,7 @@ __device__ __forceinline__ void run_mma_bs(const KernelParams& p, const Ctx& c, 
     }
     q0 += static_cast<uint32_t>(npairs);
     kb0 += static_cast<uint32_t>(nkb);
-    kt_item += k_count;
+    kt_item += walk.k_count();
   }
   if (stats) {
     p.stats[blockIdx.x * kStatSlots + STAT_MMA_WAIT_FULL] = wait_full;
@@ -161,15 +157,16 @@ constexpr uint32_t kBsBarrier = 1;                // named barrier of the accumu
 
 // Copy the scales of k-blocks kb0 .. kb0 + kBsWindow - 1 of item w into the window at
 // shared address dst; accumulating thread e (0-255) copies slot e of each k-block.
+template <bool GROUPED>
 __device__ __forceinline__ void bs_stage_window(const KernelParams& p, const WorkItem& w, int32_t kb0, uint32_t dst,
                                                 int e) {
   const bool is_a = e < 128;
   const int32_t lim = is_a ? p.M : p.N;
   int32_t idx = is_a ? w.row0 + e : w.col0 + (e - 128);
   idx = idx < lim ? idx : lim - 1;   // rows and columns past the matrix carry zero partials
-  // each group of a grouped GEMM has its own rows of B's scales
-  const int64_t first = is_a ? 0 : static_cast<int64_t>(w.group) * p.bs_group_rows;
-  const float* src = (is_a ? p.bs_a : p.bs_b) + (first + idx / (is_a ? p.bs_rows : p.bs_rows_b)) * p.bs_kblocks;
+  int64_t line = idx / (is_a ? p.bs_rows : p.bs_rows_b);
+  if (GROUPED && !is_a) line += static_cast<int64_t>(w.group) * p.bs_group_rows;   // each group's own rows of B's scales
+  const float* src = (is_a ? p.bs_a : p.bs_b) + line * p.bs_kblocks;
 #pragma unroll
   for (int i = 0; i < kBsWindow; ++i) {
     int32_t kb = kb0 + i;
@@ -202,7 +199,7 @@ __device__ __forceinline__ void bs_fold_columns(float sa, const float* sb, const
 
 // PER_COL: B's scale rows change inside a 32-column chunk (B's tile rows not a multiple of
 // 32), so every column takes its own scale; else one per chunk.
-template <int OUT, bool PER_COL>
+template <int OUT, bool PER_COL, bool GROUPED>
 __device__ __forceinline__ void run_epilogue_bs(const KernelParams& p, const Ctx& c, uint32_t tmem_base,
                                                 uint32_t bar_pfull, uint32_t bar_pempty, uint32_t win_smem,
                                                 const float* win_ptr) {
@@ -234,7 +231,7 @@ __device__ __forceinline__ void run_epilogue_bs(const KernelParams& p, const Ctx
   // at a barrier for a warp that has left.
   bool have = work_next(p.sched, it, w);
   uint32_t g = 0;   // windows begun so far: window g uses buffer g & 1
-  if (have) bs_stage_window(p, w, 0, win_smem, e);
+  if (have) bs_stage_window<GROUPED>(p, w, 0, win_smem, e);
   while (have) {
     const bool have_next = work_next(p.sched, it, wn);
     const int32_t row = w.row0 + row_in_tile;
@@ -248,8 +245,8 @@ __device__ __forceinline__ void run_epilogue_bs(const KernelParams& p, const Ctx
       ptx::cp_async_wait_all();
       ptx::named_bar_sync(kBsBarrier, 256);   // window g is in place; window g - 1 is read
       const uint32_t next_buf = win_smem + ((g + 1) & 1u) * kBsWindowBytes;
-      if (wi + 1 < nwin) bs_stage_window(p, w, (wi + 1) * kBsWindow, next_buf, e);
-      else if (have_next) bs_stage_window(p, wn, 0, next_buf, e);
+      if (wi + 1 < nwin) bs_stage_window<GROUPED>(p, w, (wi + 1) * kBsWindow, next_buf, e);
+      else if (have_next) bs_stage_window<GROUPED>(p, wn, 0, next_buf, e);
       const float* win = win_ptr + (g & 1u) * (kBsWindowBytes / 4);
       const int jend = nkb < (wi + 1) * kBsWindow ? nkb : (wi + 1) * kBsWindow;
       // a pair of k-blocks per step (one slot: two partial buffers, the other slot filling
@@ -320,7 +317,7 @@ __device__ __forceinline__ void run_epilogue_bs(const KernelParams& p, const Ctx
   }
 }
 
-template <int DT, int OUT, bool PER_COL>
+template <int DT, int OUT, bool PER_COL, bool GROUPED>
 __global__ void __launch_bounds__(kBsThreads, 1) gemm_bs_kernel(const __grid_constant__ KernelParams p) {
   using Cfg = TileCfg<128, 1, 1>;
   static_assert(Cfg::NACC == kBsBuffers, "the partial buffers use the accumulator barriers' slots");
@@ -382,16 +379,15 @@ __global__ void __launch_bounds__(kBsThreads, 1) gemm_bs_kernel(const __grid_con
   } else if (warp == 1 || warp == 10) {
     if (lane == 0) {
       const int r = warp == 1 ? 0 : 1;
-      const PlainWalk walk(p.sched, c.unit);
       if (p.bs_k == 32)
-        run_mma_bs<1>(p, c, walk, r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
+        run_mma_bs<1>(p, c, PlainWalk(p.sched, c.unit), r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
       else if (p.bs_k == 64)
-        run_mma_bs<2>(p, c, walk, r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
+        run_mma_bs<2>(p, c, PlainWalk(p.sched, c.unit), r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
       else
-        run_mma_bs<4>(p, c, walk, r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
+        run_mma_bs<4>(p, c, PlainWalk(p.sched, c.unit), r, tmem_base, smem_a, smem_b, bar_full, bar_empty, bar_pfull, bar_pempty, bar_drain);
     }
   } else {
-    run_epilogue_bs<OUT, PER_COL>(p, c, tmem_base, bar_pfull, bar_pempty, ptx::smem_addr(win),
+    run_epilogue_bs<OUT, PER_COL, GROUPED>(p, c, tmem_base, bar_pfull, bar_pempty, ptx::smem_addr(win),
                                   reinterpret_cast<const float*>(win));
   }
 

@@ -85,10 +85,8 @@ __device__ __forceinline__ void bs_producer(const KernelParams& p, const Ctx& c,
 struct WalkK {
   Walk walk;
   int32_t kt;
-  __device__ __forceinline__ bool next(int32_t& k_count) {
-    k_count = kt;
-    return walk.skip();
-  }
+  __device__ __forceinline__ bool next() { return walk.skip(); }
+  __device__ __forceinline__ int32_t k_count() const { return kt; }
 };
 
 // wait_phase for a converged warp, which follows one verdict

@@ -287,7 +287,7 @@ const void* tst_reduce_kernel(int out_type);
 // scale of B per column (block rows not a multiple of 32).  The ring's last stage holds the
 // scale windows, so a plan runs at most (the tile's stages - 1) stages.
 constexpr int kBsThreads = 352;
-const void* tst_bs_kernel(int out_type, bool per_col);
+const void* tst_bs_kernel(int out_type, bool per_col, bool grouped);
 
 // The form for one scale of B per tile and k-block (gemm_bst.cu): k-blocks of 128, B's scale
 // tiles a multiple of 128 rows high; tile and ring as above, a warpgroup of single-thread roles
