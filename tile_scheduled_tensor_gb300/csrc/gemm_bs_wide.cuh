@@ -11,8 +11,9 @@
 //               group table
 //   warps 4-11  accumulate: two per TMEM quadrant, 128 columns each, 16 at a time with the next 16's
 //               load in flight (32 and 32 spill: 640 cycles per 64 columns against 170)
-// 16384 rows over 16 experts of 4096 x 4096 (550 GFLOP): 255 us, 0.56 of twice the measured BF16 rate;
-// 330 with 128 x 128 tiles.  What bounds it now is the accumulating warps' chain per k-block (750
+// 16384 rows over 16 experts of 4096 x 4096 (550 GFLOP): 255 us with one set of inputs over and over, 0.56
+// of twice the measured BF16 rate, and 270 to 279 with inputs in turn, at the clocks that the power cap
+// then leaves; 330 with 128 x 128 tiles.  What bounds it now is the accumulating warps' chain per k-block (750
 // cycles: 340 adding, the rest waiting, handing over and storing) before the 768 of its loads.
 #pragma once
 #include "gemm_bs_tile.cuh"

@@ -38,8 +38,10 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 bool float_type(int32_t t) { return t == TST_OUT_F32 || t == TST_OUT_BF16; }
 int64_t type_bytes(int32_t t) { return t == TST_OUT_F32 ? 4 : t == TST_OUT_BF16 ? 2 : 1; }
 
-// Tokens per block of the routing kernel: the fewest multiple of 32 that keeps to four blocks per SM,
-// which are resident at once, up to 256 (whose bitmap is 8 words per expert).
+// Tokens per block of the routing kernel: the fewest multiple of 32 that keeps to four blocks for each of
+// the GPU's 152 SMs, up to 256 (whose bitmap is 8 words per expert).  Up to 256 experts these blocks are
+// resident at once; registers leave room for two per SM up to 512 experts and one beyond, where they
+// follow one another.
 constexpr int64_t kResidentChunks = 4 * 152;
 int32_t route_chunk(int64_t tokens) {
   const int64_t c = ceil_div(ceil_div(tokens, 32), kResidentChunks) * 32;

@@ -337,10 +337,11 @@ struct alignas(8) Candidate {
 // maximum over the lanes' own maxima leave a bound that at least k logits reach; those that do,
 // seldom more than a few over k, go to a list in shared memory with their experts,
 // and each finds its rank by comparing itself with the others.  Rounds over all logits remain for rows with
-// more than 32 on the list, NaN, infinities or a top of 2^20 or more in magnitude.  What bounds it is a row's chain of
-// steps and the issue slots (some 400 instructions for a row of 256 logits), not the 1 KB that the row
-// reads: 131071 rows of 256, k = 8, in 83 us with the two launches after it, 235 by rounds alone;
-// their bytes take 22 us.  Threads that hold whole or half rows of a tile in shared memory need 230
+// more than 32 on the list, NaN, infinities or a top of 2^20 or more in magnitude.  What bounds it
+// is issue slots, not the 1 KB that a row reads: 464 instructions for a row of 256 logits, 0.76 of the
+// slots taken while a block runs, 0.68 over the launch, whose 586 blocks end unevenly.  131071 rows of
+// 256, k = 8, in 83 us a call with the two launches after it, 235 by rounds alone, 156 where every top
+// is at 2^20 or beyond; their bytes take 22 us.  Threads that hold whole or half rows of a tile in shared memory need 230
 // to 300 instructions a row, but leave 5 to 10 warps on an SM and measured 128 and 99 us.
 // WARPS: 8, or 32 for chunks of 32 tokens that do not fill the SMs: a row's chain of steps, about a
 // microsecond, then passes once.
@@ -710,8 +711,8 @@ __device__ __forceinline__ float grad_scale(const RouteGradParams& p) {
 
 // A warp per row; the chosen experts' parts pass through a row of shared memory to the lanes that
 // hold those experts.  Bound by memory, the logits in and the gradient out, with a row's chain of loads,
-// exponentials and sums over the lanes hidden behind the other warps': 65536 x 256 float32 in 27.8 us,
-// 0.73 of the copy rate.  The sums over the lanes go together, one latency for all of them.
+// exponentials and sums over the lanes hidden behind the other warps': 65536 x 256 float32 in 27.5 us in
+// a graph, 0.74 of the copy rate, and 29 to 30 a call.  The sums over the lanes go together, one latency for all of them.
 template <typename T, int VPL, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) route_grad_kernel(const RouteGradParams p) {
   using Map = RowMap<T, VPL>;
