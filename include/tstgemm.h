@@ -567,6 +567,63 @@ enum {
 tst_status gemm_plan_set_debug(tst_plan *plan, int32_t flags, void *trace_buf, int64_t cap,
                                int64_t timeout_ns);
 
+/* ---------------------------------------------------------------- 8-bit integers
+ *
+ * GEMM of int8 operands with one scale per row of A (a token) and per row of B (a channel):
+ *
+ *   D[i][j] = cast( relu?( (float(sum_k a_ik * b_jk) * row_scale[i]) * col_scale[j] + bias[j] ) )
+ *
+ * A: M x K and B: N x K, int8, K contiguous; D: M x N row-major, FP32 or BF16.  The sum is
+ * exact (in 32-bit integers) for every int8 value, -128 among them; it is rounded to FP32,
+ * multiplied by the row's scale, and by the channel's with the bias added in one fused step.
+ * With groups > 0: `groups` GEMMs sharing N and K, as gemm_grouped_plan_create: A and D hold
+ * the groups' rows one after another (at most M in all), B, col_scale and bias one part per
+ * group (groups * N rows or elements), and the groups' row counts are read from device memory
+ * at run time.  Rows of D behind the last group's stay as they were.
+ *
+ * Conventions as for the other calls; a plan is not re-entrant and belongs to the GPU that
+ * was current when it was made (a run with another current GPU is INVALID_ARG). */
+typedef struct tst_int8_plan tst_int8_plan;
+
+typedef struct {
+    int32_t groups;      /* 0: one GEMM */
+    int32_t out_dtype;   /* TST_OUT_F32 or TST_OUT_BF16 */
+    int32_t has_bias;    /* 1: bias is FP32[N], grouped FP32[groups * N] */
+    int32_t relu;        /* 1: max(z, 0), a NaN stays */
+    int32_t host_only;   /* 1: no GPU (the runs then fail with TST_ERR_NO_DEVICE); num_sms must be set */
+    int32_t num_sms;     /* SMs to use: 0 = all */
+    int64_t timeout_ns;  /* limit of every device-side wait: 0 = 10 s */
+} tst_int8_options;
+
+typedef struct {
+    int64_t M, N, K;
+    int32_t groups;
+    int32_t tile_rows, tile_cols;   /* rows of A (tokens) and columns of D per tile */
+    int32_t grid;                   /* CTAs launched */
+    int32_t smem_bytes;             /* dynamic shared memory per CTA */
+} tst_int8_plan_info;
+
+/* Errors: INVALID_ARG (null plan or opts, sizes < 1 or beyond int32, groups < 0, an out_dtype
+ * other than the two, host_only without num_sms), ALIGNMENT (K not a multiple of 16),
+ * UNSUPPORTED (M or groups * N beyond 2^31 - 256, K beyond 131056 (the 32-bit sums), more than
+ * 512 groups, or a GPU other than sm_103), OOM, CUDA, NO_DEVICE. */
+tst_status gemm_int8_plan_create(tst_int8_plan **plan, int64_t M, int64_t N, int64_t K, const tst_int8_options *opts);
+tst_status gemm_int8_plan_get_info(const tst_int8_plan *plan, tst_int8_plan_info *info);
+/* NULL is accepted. */
+tst_status gemm_int8_plan_destroy(tst_int8_plan *plan);
+
+/* group_rows: DEVICE int32[groups] of a grouped plan (negative counts are taken as 0), else
+ * NULL.  bias is ignored without has_bias.  Errors: INVALID_ARG (a NULL operand, group_rows for
+ * a plan without groups or none for one with them), ALIGNMENT (A or B not 16-byte aligned, the
+ * others not aligned to their elements), NO_DEVICE, CUDA. */
+tst_status gemm_int8_run(tst_int8_plan *plan, const int32_t *group_rows, const int8_t *A, const int8_t *B, void *D,
+                         const float *row_scale, const float *col_scale, const float *bias, void *stream);
+
+/* What the runs since the last query recorded on the device: TST_OK, TST_ERR_TIMEOUT (a bounded
+ * wait ran out) or TST_ERR_DEVICE_CHECK (the groups' rows add up to more than M: rows past M are
+ * not computed).  Synchronises the last run's stream. */
+tst_status gemm_int8_status_query(tst_int8_plan *plan);
+
 /* ---------------------------------------------------------------- mixture of experts
  *
  * The calls around a grouped GEMM whose groups are the experts of a mixture:

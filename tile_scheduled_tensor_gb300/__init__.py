@@ -375,6 +375,78 @@ def gemm_streamk_noalloc(M: int, N: int, K: int, A, B, C, dtype="bf16", mapping=
                                     _stream(stream)), "gemm_streamk_noalloc")
 
 
+# ---------------------------------------------------------------- 8-bit integers
+class Int8Plan:
+    """Owns a tst_int8_plan*; destroyed with the object (or explicitly via destroy())."""
+
+    def __init__(self, handle: int, info, out_dtype: int, has_bias: bool):
+        self.handle = handle
+        self.info = info
+        self.M, self.N, self.K, self.groups = info.M, info.N, info.K, info.groups
+        self.out_dtype, self.has_bias = out_dtype, has_bias
+
+    def destroy(self):
+        if self.handle:
+            _check(lib.gemm_int8_plan_destroy(ctypes.c_void_p(self.handle)), "gemm_int8_plan_destroy")
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+    @property
+    def _h(self):
+        if not self.handle:
+            raise ValueError("plan was destroyed")
+        return self.handle
+
+
+def gemm_int8_plan_create(M: int, N: int, K: int, groups: int = 0, out_dtype="bf16", has_bias: bool = False,
+                          relu: bool = False, host_only: bool = False, num_sms: int = 0,
+                          timeout_ns: int = 0) -> Int8Plan:
+    """Plan D = relu?(row_scale * col_scale * (A x B) + bias) of int8 A (M x K) and B (N x K), the integer
+    sum exact.  groups > 0: that many GEMMs sharing N and K, A and D holding the groups' rows one after
+    another (at most M), B, col_scale and bias one part per group."""
+    out = _enum(_OUT, out_dtype, "out_dtype")
+    opts = _capi.tst_int8_options(int(groups), out, int(bool(has_bias)), int(bool(relu)), int(bool(host_only)),
+                                  int(num_sms), int(timeout_ns))
+    h = ctypes.c_void_p()
+    _check(lib.gemm_int8_plan_create(ctypes.byref(h), int(M), int(N), int(K), ctypes.byref(opts)),
+           "gemm_int8_plan_create")
+    info = _capi.tst_int8_plan_info()
+    _check(lib.gemm_int8_plan_get_info(h, ctypes.byref(info)), "gemm_int8_plan_get_info")
+    return Int8Plan(h.value, info, out, bool(has_bias))
+
+
+def gemm_int8_run(plan: Int8Plan, A, B, D, row_scale, col_scale, bias=None, group_rows=None, stream=None):
+    """Enqueue the int8 GEMM: A M x K, B N x K (grouped: groups * N rows, or groups x N x K), D M x N of the
+    plan's type, row_scale FP32[M], col_scale and bias FP32[N] (grouped: [groups * N]), group_rows int32[groups]."""
+    parts = max(plan.groups, 1) * plan.N
+    if (plan.groups > 0) != (group_rows is not None):
+        raise ValueError("a grouped plan needs group_rows, and no other plan takes them")
+    if plan.has_bias and bias is None:
+        raise ValueError("the plan needs a bias")
+    _check(lib.gemm_int8_run(plan._h, None if group_rows is None else _array(group_rows, "group_rows", "int32", plan.groups),
+                             _array(A, "A", "int8", plan.M * plan.K), _array(B, "B", "int8", parts * plan.K),
+                             _array(D, "D", "float32" if plan.out_dtype == TST_OUT_F32 else "bfloat16", plan.M * plan.N),
+                             _array(row_scale, "row_scale", "float32", plan.M),
+                             _array(col_scale, "col_scale", "float32", parts),
+                             _array(bias, "bias", "float32", parts) if plan.has_bias else None, _stream(stream)),
+           "gemm_int8_run")
+
+
+def gemm_int8_status_query(plan: Int8Plan) -> int:
+    """Status recorded by the runs since the last query (TST_ERR_DEVICE_CHECK: the groups' rows add up to more
+    than M); synchronises the last run's stream."""
+    return lib.gemm_int8_status_query(plan._h)
+
+
+def gemm_int8_plan_destroy(plan: Int8Plan):
+    plan.destroy()
+
+
 # ---------------------------------------------------------------- mixture of experts
 class MoePlan:
     """Owns a tst_moe_plan*; destroyed with the object (or explicitly via destroy())."""

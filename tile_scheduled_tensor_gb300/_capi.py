@@ -98,6 +98,18 @@ class tst_moe_plan_info(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I32, _I64 = ctypes.c_int32, ctypes.c_int64
+
+
+class tst_int8_options(ctypes.Structure):
+    _fields_ = [("groups", _I32), ("out_dtype", _I32), ("has_bias", _I32), ("relu", _I32), ("host_only", _I32),
+                ("num_sms", _I32), ("timeout_ns", _I64)]
+
+
+class tst_int8_plan_info(ctypes.Structure):
+    _fields_ = [("M", _I64), ("N", _I64), ("K", _I64), ("groups", _I32), ("tile_rows", _I32), ("tile_cols", _I32),
+                ("grid", _I32), ("smem_bytes", _I32)]
+
+
 _SIGNATURES = {
     "gemm_plan_create": (ctypes.c_int, [ctypes.POINTER(_P), ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                         ctypes.c_int, ctypes.c_int, tst_mapping, ctypes.c_int,
@@ -137,6 +149,11 @@ _SIGNATURES = {
     "gemm_streamk_noalloc": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                             tst_mapping, ctypes.c_int, ctypes.POINTER(tst_epilogue),
                                             ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P]),
+    "gemm_int8_plan_create": (ctypes.c_int, [ctypes.POINTER(_P), _I64, _I64, _I64, ctypes.POINTER(tst_int8_options)]),
+    "gemm_int8_plan_get_info": (ctypes.c_int, [_P, ctypes.POINTER(tst_int8_plan_info)]),
+    "gemm_int8_plan_destroy": (ctypes.c_int, [_P]),
+    "gemm_int8_run": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "gemm_int8_status_query": (ctypes.c_int, [_P]),
     "moe_plan_create": (ctypes.c_int, [ctypes.POINTER(_P), _I64, _I32, _I32, ctypes.POINTER(tst_moe_options)]),
     "moe_plan_get_info": (ctypes.c_int, [_P, ctypes.POINTER(tst_moe_plan_info)]),
     "moe_plan_destroy": (ctypes.c_int, [_P]),

@@ -247,6 +247,10 @@ int64_t hybrid_split_tiles(int64_t T, int64_t P) {
 
 }  // namespace
 
+bool tst_encode_bytes(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, int box_rows) {
+  return encode_operand(map, ptr, TST_E4M3, rows, K, 128, box_rows);
+}
+
 extern "C" {
 
 const char* gemm_status_string(tst_status s) {

@@ -1,0 +1,366 @@
+// GEMM of 8-bit integers with a scale per token (row of A) and per channel (row of B):
+//
+//   D[i][j] = cast( relu?( float(sum_k a_ik b_jk) ra_i cb_j + bias_j ) ),   the sum exact,
+//
+// dense, or grouped with one N x K matrix, one row of scales and one of biases per group.
+//
+// sm_103a's tcgen05 has no integer kind.  Every int8 value is an FP16 value, a product of two is an
+// integer of at most 2^14, and a sum of 1024 of them is at most 2^24: the FP32 accumulator of
+// kind::f16 holds it exactly, in any order.  So the operands travel as bytes (HBM, L2, TMA, the
+// shared-memory ring), become FP16 on their way to the tensor core, and every 1024 of K the
+// accumulator is added to 32-bit integer sums in registers.
+//
+// The operands are exchanged as in gemm_bs_narrow.cuh: the 128 rows of the MMA (TMEM lanes) are
+// channels, rows of B, and its N are NT tokens, rows of A.  Few tokens then waste no tensor-core
+// rows, and the bulk of the bytes to convert, the weights, goes from registers straight into Tensor
+// Memory, which holds the MMA's first operand: no second pass through shared memory.
+//
+// A byte x becomes FP16 as 0x6400 | (x ^ 0x80), which is 1024 + (x + 128), less 1152: for four bytes
+// one exclusive or, two byte permutes, two packed subtractions.
+//
+// Roles, 384 threads, persistent over NT x 128 tiles of D, k-blocks of 128:
+//   warp 0      TMA producer: 128 x 128 bytes of B and NT x 128 of A per stage of the byte ring
+//   warp 1      MMA issuer: eight K = 16 MMAs per k-block and, every eighth k-block, a new accumulator
+//   warps 2-3   tokens: bytes of the ring -> FP16 in shared memory (the 128-byte swizzle that the
+//               MMA reads)
+//   warps 4-7   weights: a thread per channel, 128 bytes -> 64 columns of Tensor Memory
+//   warps 8-11  a thread per channel: accumulator -> integer sums; scales, bias, ReLU, cast, store
+// Every wait is bounded as in the other kernels.
+#pragma once
+#include "gemm_bs_tile.cuh"
+
+namespace tst {
+
+constexpr int kInt8Threads = 384;
+constexpr int kInt8Fold = 8;   // k-blocks of 128 per accumulator: 1024 products of at most 2^14
+
+template <int NT_>
+struct Int8Cfg {
+  static constexpr int NT = NT_;
+  static constexpr int PER_SM = NT <= 32 ? 2 : 1;          // CTAs per SM
+  static constexpr int W_BYTES = 128 * 128;
+  static constexpr int X_BYTES = NT * 128;
+  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+  static constexpr int CV = 3;                             // converted k-blocks: TMEM columns and shared memory
+  static constexpr int XCV_BYTES = 2 * X_BYTES;            // FP16 tokens of a k-block: two 64-element atoms
+  static constexpr int BUFS = 2;                           // accumulators
+  static constexpr int A_COL = BUFS * NT;                  // first TMEM column of the weights
+  static constexpr int USED_COLS = A_COL + CV * 64;
+  static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
+  static constexpr int LIMIT = PER_SM == 2 ? (228 * 1024 - 2 * 1024) / 2 : kSmemLimit;
+  static constexpr int FIXED = 1024 + CV * XCV_BYTES + kWalkBytes + 512;
+  static constexpr int RAW_STAGES = (LIMIT - FIXED) / STAGE_BYTES;
+  static constexpr int STAGES = RAW_STAGES > 8 ? 8 : RAW_STAGES;
+  static constexpr int XCV_OFFSET = STAGES * STAGE_BYTES;
+  static constexpr int WALK_OFFSET = XCV_OFFSET + CV * XCV_BYTES;
+  static constexpr int BAR_OFFSET = (WALK_OFFSET + kWalkBytes + 7) / 8 * 8;
+  static constexpr int BARS = 2 * STAGES + 2 * CV + 2 * BUFS + 1;
+  static constexpr int MISC_OFFSET = BAR_OFFSET + BARS * 8;
+  static constexpr int SMEM_BYTES = 1024 + MISC_OFFSET + 16;
+  static_assert(STAGE_BYTES % 1024 == 0 && XCV_BYTES % 1024 == 0, "swizzled tiles start on 1024 bytes");
+  static_assert(SMEM_BYTES <= LIMIT && STAGES >= 2 && PER_SM * TMEM_COLS <= 512 && USED_COLS <= TMEM_COLS, "fits an SM");
+};
+
+// 16 int8 values -> 8 pairs of FP16, in their order
+__device__ __forceinline__ void int8_to_half(const uint4& v, uint32_t* h) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = w[i] ^ 0x80808080u;
+    const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(h[2 * i]) : "r"(lo), "r"(0x64806480u));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(h[2 * i + 1]) : "r"(hi), "r"(0x64806480u));
+  }
+}
+
+// The shared addresses of the barriers: byte ring, converted k-blocks, accumulators, drain.
+template <class Cfg>
+struct Int8Bars {
+  uint32_t full, empty, cv_full, cv_empty, acc_full, acc_empty, drain;
+  __device__ __forceinline__ explicit Int8Bars(uint32_t base)
+      : full(base), empty(full + 8 * Cfg::STAGES), cv_full(empty + 8 * Cfg::STAGES), cv_empty(cv_full + 8 * Cfg::CV),
+        acc_full(cv_empty + 8 * Cfg::CV), acc_empty(acc_full + 8 * Cfg::BUFS), drain(acc_empty + 8 * Cfg::BUFS) {}
+};
+
+// position in a ring of N
+template <int N>
+struct RingAt {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) { at = 0; phase ^= 1u; }
+  }
+};
+
+template <class Cfg>
+__device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& c, Walk walk, uint32_t smem, const Int8Bars<Cfg>& bar) {
+  RingAt<Cfg::STAGES> r;
+  uint32_t issued = 0, issued_parity = 0;
+  bool ok = true;
+  Tile w;
+  while (ok && walk.next(w)) {
+    if (w.clamped) record_status(p, ST_DEVICE_CHECK, ROLE_PRODUCER);
+    const int32_t b_row0 = w.group * p.sched.group_b_rows + w.n * 128;
+    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
+      if (!wait_phase<1>(p, c, bar.empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
+      const uint32_t full = bar.full + 8 * r.at, dst = smem + r.at * Cfg::STAGE_BYTES;
+      ptx::mbar_arrive_expect_tx(full, Cfg::STAGE_BYTES);
+      ptx::tma_load_2d(dst, &p.tmap_b, full, kb * 128, b_row0);
+      ptx::tma_load_2d(dst + Cfg::W_BYTES, &p.tmap_a, full, kb * 128, w.row0);
+      issued |= 1u << r.at;
+      issued_parity = (issued_parity & ~(1u << r.at)) | (r.phase << r.at);
+      r.next();
+    }
+  }
+  if (!ok) {   // aborting: wait (bounded) until the loads already issued have landed
+    const uint64_t t0 = ptx::globaltimer();
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      if (!(issued & (1u << s))) continue;
+      while (!ptx::mbar_try_wait(bar.full + 8 * s, (issued_parity >> s) & 1u))
+        if (ptx::globaltimer() - t0 > p.timeout_ns) break;
+    }
+  }
+}
+
+template <class Cfg>
+__device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, uint32_t xcv,
+                                         const Int8Bars<Cfg>& bar) {
+  const uint32_t idesc = ptx::make_idesc(0u, 128, Cfg::NT);   // FP16 operands
+  const uint64_t x_desc0 = ptx::sw128_kmajor_desc(xcv);
+  RingAt<Cfg::CV> r;
+  RingAt<Cfg::BUFS> acc;
+  bool ok = true;
+  while (ok && walk.skip()) {
+    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
+      const int32_t in_fold = kb % kInt8Fold;
+      if (in_fold == 0 && !wait_phase<1>(p, c, bar.acc_empty + 8 * acc.at, acc.phase ^ 1u, ROLE_MMA)) { ok = false; break; }
+      if (!wait_phase<1>(p, c, bar.cv_full + 8 * r.at, r.phase, ROLE_MMA)) { ok = false; break; }
+      ptx::tc_fence_after();
+      const uint32_t d = tmem_base + static_cast<uint32_t>(acc.at * Cfg::NT);
+      const uint32_t a = tmem_base + static_cast<uint32_t>(Cfg::A_COL + r.at * 64);
+      const uint64_t x = x_desc0 + static_cast<uint64_t>(r.at * (Cfg::XCV_BYTES >> 4));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)   // 16 of K: 8 TMEM columns, 32 bytes of an atom
+        ptx::mma_f16_ts(d, a + 8 * i, x + (i >> 2) * (Cfg::X_BYTES >> 4) + (i & 3) * 2, idesc, in_fold != 0 || i != 0);
+      ptx::mma_commit(bar.cv_empty + 8 * r.at);
+      r.next();
+      if (in_fold == kInt8Fold - 1 || kb == p.sched.kt - 1) {
+        ptx::mma_commit(bar.acc_full + 8 * acc.at);
+        acc.next();
+      }
+    }
+  }
+  // every MMA issued completes before TMEM is released
+  ptx::mma_commit(bar.drain);
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait(bar.drain, 0)) {
+    if (ptx::globaltimer() - t0 > p.timeout_ns) {
+      raise_error<1>(p, c, ST_TIMEOUT, ROLE_MMA);
+      break;
+    }
+  }
+}
+
+// Warps 2-3: eight lanes take the same 16-byte piece of eight rows, which the swizzle puts in
+// eight different banks' worth of shared memory, reading and writing.
+template <class Cfg>
+__device__ __forceinline__ void int8_tokens(const KernelParams& p, const Ctx& c, Walk walk, uint8_t* smem, uint8_t* xcv,
+                                            const Int8Bars<Cfg>& bar) {
+  const int lane = threadIdx.x & 31;
+  const int j = (static_cast<int>(threadIdx.x >> 5) - 2) * 4 + (lane >> 3), sub = lane & 7;
+  RingAt<Cfg::STAGES> r;
+  RingAt<Cfg::CV> t;
+  const uint8_t* const src0 = smem + Cfg::W_BYTES + sub * 128 + ((j ^ sub) << 4);
+  uint8_t* const dst0 = xcv + (j >> 2) * Cfg::X_BYTES + sub * 128;
+  const int c0 = (((2 * j) & 7) ^ sub) << 4, c1 = (((2 * j + 1) & 7) ^ sub) << 4;
+  while (walk.skip()) {
+    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
+      if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE) ||
+          !wait_phase_warp(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE))
+        return;
+      const uint8_t* const src = src0 + r.at * Cfg::STAGE_BYTES;
+      uint8_t* const dst = dst0 + t.at * Cfg::XCV_BYTES;
+#pragma unroll
+      for (int i = 0; i < Cfg::NT / 8; i += 2) {
+        const uint4 v0 = *reinterpret_cast<const uint4*>(src + i * 1024), v1 = *reinterpret_cast<const uint4*>(src + i * 1024 + 1024);
+        uint32_t h[16];
+        int8_to_half(v0, h);
+        int8_to_half(v1, h + 8);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          *reinterpret_cast<uint4*>(dst + (i + q) * 1024 + c0) = make_uint4(h[8 * q], h[8 * q + 1], h[8 * q + 2], h[8 * q + 3]);
+          *reinterpret_cast<uint4*>(dst + (i + q) * 1024 + c1) = make_uint4(h[8 * q + 4], h[8 * q + 5], h[8 * q + 6], h[8 * q + 7]);
+        }
+      }
+      ptx::fence_proxy_async_smem();   // the MMA reads these writes through the async proxy
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(bar.empty + 8 * r.at);
+        ptx::mbar_arrive(bar.cv_full + 8 * t.at);
+      }
+      r.next();
+      t.next();
+    }
+  }
+}
+
+template <class Cfg>
+__device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, const uint8_t* smem,
+                                             const Int8Bars<Cfg>& bar) {
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+  const uint8_t* const src0 = smem + (quad * 32 + lane) * 128;
+  const int sub = lane & 7;
+  const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + Cfg::A_COL;
+  RingAt<Cfg::STAGES> r;
+  RingAt<Cfg::CV> t;
+  while (walk.skip()) {
+    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
+      if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return;
+      const uint8_t* const src = src0 + r.at * Cfg::STAGE_BYTES;
+      uint4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + ((q ^ sub) << 4));
+      if (!wait_phase_warp(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE)) return;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {   // 64 of K: 32 columns
+        uint32_t h[32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) int8_to_half(v[q], h + 8 * q);
+        if (half == 0) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + (((4 + q) ^ sub) << 4));
+        }
+        ptx::tmem_store_32cols(taddr0 + static_cast<uint32_t>(t.at * 64 + half * 32), h);
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar.empty + 8 * r.at);   // the bytes are in registers
+      ptx::tmem_wait_stores();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar.cv_full + 8 * t.at);
+      r.next();
+      t.next();
+    }
+  }
+}
+
+template <class Cfg, int OUT>
+__device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, const Int8Bars<Cfg>& bar) {
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+  const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+  RingAt<Cfg::BUFS> acc;
+  Tile w;
+  while (walk.next_warp(w)) {
+    int32_t sum[Cfg::NT];
+    for (int32_t kb = 0; kb < p.sched.kt; kb += kInt8Fold) {
+      if (!wait_phase_warp(p, c, bar.acc_full + 8 * acc.at, acc.phase, ROLE_EPILOGUE)) return;
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < Cfg::NT; q += 16) {
+        float v[16];
+        ptx::tmem_load_16cols(taddr0 + static_cast<uint32_t>(acc.at * Cfg::NT + q), v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int32_t x = __float2int_rn(v[i]);   // a whole number already
+          sum[q + i] = kb == 0 ? x : sum[q + i] + x;
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar.acc_empty + 8 * acc.at);
+      acc.next();
+    }
+    const int32_t col = w.n * 128 + quad * 32 + lane;
+    if (col < p.N) {
+      const int64_t channel = static_cast<int64_t>(w.group) * p.N + col;
+      const float cb = __ldg(p.ext.col_scale + channel);
+      const float b = p.has_bias ? __ldg(p.bias + channel) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < Cfg::NT; ++i) {
+        const int32_t row = w.row0 + i;
+        if (row >= w.row_end) break;
+        float z = fmaf(__int2float_rn(sum[i]) * __ldg(p.ext.row_scale + row), cb, b);
+        if (p.relu) z = z < 0.0f ? 0.0f : z;   // a NaN stays
+        const int64_t at = static_cast<int64_t>(row) * p.N + col;
+        if (OUT == OUT_BF16) reinterpret_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(z);
+        else reinterpret_cast<float*>(p.C)[at] = z;
+      }
+    }
+  }
+}
+
+template <class Cfg, int OUT>
+__global__ void __launch_bounds__(kInt8Threads, Cfg::PER_SM) gemm_int8_kernel(const __grid_constant__ KernelParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = ptx::smem_addr(smem);
+  const Int8Bars<Cfg> bar(base + Cfg::BAR_OFFSET);
+  SharedCtl* ctl = reinterpret_cast<SharedCtl*>(smem + Cfg::MISC_OFFSET);
+  const int warp = threadIdx.x >> 5;
+
+  Ctx c;
+  c.abort = &ctl->abort;
+  c.abort_addr = ptx::smem_addr(&ctl->abort);
+  c.rank = 0;
+  c.rank_m = 0;
+  c.rank_n = 0;
+  c.csize = 1;
+  c.unit = static_cast<int32_t>(blockIdx.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      ptx::mbar_init(bar.full + 8 * s, 1);
+      ptx::mbar_init(bar.empty + 8 * s, 6);      // the converting warps
+    }
+    for (int s = 0; s < Cfg::CV; ++s) {
+      ptx::mbar_init(bar.cv_full + 8 * s, 6);
+      ptx::mbar_init(bar.cv_empty + 8 * s, 1);
+    }
+    for (int b = 0; b < Cfg::BUFS; ++b) {
+      ptx::mbar_init(bar.acc_full + 8 * b, 1);
+      ptx::mbar_init(bar.acc_empty + 8 * b, 4);
+    }
+    ptx::mbar_init(bar.drain, 1);
+    ctl->abort = 0;
+    ctl->ep_ok = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&p.tmap_a);
+    ptx::prefetch_tmap(&p.tmap_b);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), Cfg::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  const GroupTable table(smem + Cfg::WALK_OFFSET);
+  if (warp == 2) fill_group_table(p.sched, table);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+  const Walk walk(p.sched, table, c.unit);
+
+  if (warp == 0) {
+    if (ptx::elect_one()) int8_producer<Cfg>(p, c, walk, base, bar);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (ptx::elect_one()) int8_mma<Cfg>(p, c, walk, tmem_base, base + Cfg::XCV_OFFSET, bar);
+    __syncwarp();
+  } else if (warp < 4) {
+    int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, bar);
+  } else if (warp < 8) {
+    int8_weights<Cfg>(p, c, walk, tmem_base, smem, bar);
+  } else {
+    int8_epilogue<Cfg, OUT>(p, c, walk, tmem_base, bar);
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+  }
+}
+
+}  // namespace tst

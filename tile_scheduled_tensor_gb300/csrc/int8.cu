@@ -1,0 +1,207 @@
+// Host side of the int8 GEMM calls declared in include/tstgemm.h: argument checks, the plan's tile
+// and schedule, tensor maps and the launch of the kernel in gemm_int8.cuh.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <new>
+
+#include "kernel_params.h"
+#include "tstgemm.h"
+
+struct tst_int8_plan {
+  int64_t M = 0, N = 0, K = 0;
+  tst_int8_options opts{};
+  int32_t tokens = 0;          // rows of A per tile
+  int32_t num_sms = 0, device = -1;
+  TstInt8Kernel kernel{};
+  tst::Sched sched{};
+  unsigned long long* d_status = nullptr;
+  cudaStream_t last_stream = nullptr;
+  bool ran = false;
+};
+
+namespace {
+
+// The status word keeps what any run records until the query that reports it: every launch has the same tag.
+constexpr uint32_t kStatusTag = 1;
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 256;   // the last tile's rows and columns are 32-bit, past the matrix too
+constexpr int64_t kMaxK = 131056;                        // 131071 products of up to 2^14 fit 32 bits; K is a multiple of 16
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Zero device memory before returning, on a stream of its own (cudaMemset is ordered with the default stream alone).
+bool zero_now(void* p, size_t bytes) {
+  cudaStream_t s;
+  if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess) return false;
+  const bool ok = cudaMemsetAsync(p, 0, bytes, s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+  return cudaStreamDestroy(s) == cudaSuccess && ok;
+}
+
+// Rows of A per tile, by the rows of a group on average.
+int32_t tile_tokens(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+}  // namespace
+
+extern "C" {
+
+tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int64_t K, const tst_int8_options* opts) {
+  if (out == nullptr) return TST_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (opts == nullptr || M < 1 || N < 1 || K < 1) return TST_ERR_INVALID_ARG;
+  if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return TST_ERR_INVALID_ARG;
+  if (opts->groups < 0 || opts->num_sms < 0 || opts->timeout_ns < 0) return TST_ERR_INVALID_ARG;
+  if (opts->out_dtype != TST_OUT_F32 && opts->out_dtype != TST_OUT_BF16) return TST_ERR_INVALID_ARG;
+  if (opts->host_only && opts->num_sms == 0) return TST_ERR_INVALID_ARG;
+  if (K % 16 != 0) return TST_ERR_ALIGNMENT;   // a row of K bytes is a row of the tensor map
+  const int64_t groups = opts->groups;
+  if (M > kMaxRows || N > kMaxRows || std::max<int64_t>(groups, 1) * N > kMaxRows || K > kMaxK || groups > kBsWalkGroups)
+    return TST_ERR_UNSUPPORTED;
+  const int32_t tokens = tile_tokens(ceil_div(M, std::max<int64_t>(groups, 1)));
+  const int64_t mt = ceil_div(M, tokens), nt = ceil_div(N, 128);
+  const int64_t tiles = (mt + groups) * nt;   // grouped: at most, whatever the split
+  if (tiles >= (int64_t(1) << 30)) return TST_ERR_UNSUPPORTED;
+  tst_int8_plan* p = new (std::nothrow) tst_int8_plan();
+  if (p == nullptr) return TST_ERR_OOM;
+  p->M = M;
+  p->N = N;
+  p->K = K;
+  p->opts = *opts;
+  p->tokens = tokens;
+  p->kernel = tst_int8_kernel(tokens, opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32);
+  p->num_sms = opts->num_sms;
+  if (!opts->host_only) {
+    int dev = 0, count = 0, major = 0, minor = 0, sms = 0;
+    if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
+      cudaGetLastError();
+      delete p;
+      return TST_ERR_NO_DEVICE;
+    }
+    if (cudaGetDevice(&dev) != cudaSuccess) { delete p; return TST_ERR_CUDA; }
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (major != 10 || minor != 3) { delete p; return TST_ERR_UNSUPPORTED; }  // built for sm_103a only
+    p->device = dev;
+    p->num_sms = opts->num_sms > 0 ? std::min(opts->num_sms, sms) : sms;
+    if (cudaFuncSetAttribute(p->kernel.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p->kernel.smem_bytes) != cudaSuccess) {
+      cudaGetLastError();
+      delete p;
+      return TST_ERR_CUDA;
+    }
+    if (cudaMalloc(&p->d_status, 256) != cudaSuccess) {
+      cudaGetLastError();
+      delete p;
+      return TST_ERR_OOM;
+    }
+    if (!zero_now(p->d_status, 256)) {
+      cudaGetLastError();
+      cudaFree(p->d_status);
+      delete p;
+      return TST_ERR_CUDA;
+    }
+  }
+  tst::Sched& s = p->sched;
+  s.mt = static_cast<int32_t>(mt);
+  s.nt = static_cast<int32_t>(nt);
+  s.kt = static_cast<int32_t>(ceil_div(K, 128));
+  s.map_kind = tst::MAP_GROUPED_M;
+  s.group = 8;
+  s.dp_tiles = static_cast<int32_t>(mt * nt);
+  s.grid = static_cast<int32_t>(std::min<int64_t>(int64_t(p->num_sms) * p->kernel.per_sm, tiles));
+  s.sk_groups = 1;
+  s.rows = static_cast<int32_t>(M);
+  s.bm = tokens;
+  s.bn = 128;
+  s.groups = static_cast<int32_t>(groups);
+  s.group_b_rows = static_cast<int32_t>(N);
+  s.cols = static_cast<int32_t>(N);
+  s.bk = 128;
+  *out = p;
+  return TST_OK;
+}
+
+tst_status gemm_int8_plan_destroy(tst_int8_plan* p) {
+  if (p == nullptr) return TST_OK;
+  const tst_status st = p->d_status && cudaFree(p->d_status) != cudaSuccess ? TST_ERR_CUDA : TST_OK;
+  delete p;
+  return st;
+}
+
+tst_status gemm_int8_plan_get_info(const tst_int8_plan* p, tst_int8_plan_info* info) {
+  if (p == nullptr || info == nullptr) return TST_ERR_INVALID_ARG;
+  info->M = p->M;
+  info->N = p->N;
+  info->K = p->K;
+  info->groups = p->sched.groups;
+  info->tile_rows = p->tokens;
+  info->tile_cols = 128;
+  info->grid = p->sched.grid;
+  info->smem_bytes = p->kernel.smem_bytes;
+  return TST_OK;
+}
+
+tst_status gemm_int8_status_query(tst_int8_plan* p) {
+  if (p == nullptr) return TST_ERR_INVALID_ARG;
+  if (p->opts.host_only) return TST_ERR_NO_DEVICE;
+  if (!p->ran) return TST_OK;
+  unsigned long long word = 0;
+  if (cudaStreamSynchronize(p->last_stream) != cudaSuccess ||
+      cudaMemcpy(&word, p->d_status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
+    return TST_ERR_CUDA;
+  if (word == 0) return TST_OK;
+  if (!zero_now(p->d_status, sizeof(word))) return TST_ERR_CUDA;   // before any later run
+  return (word & 0xFFu) == tst::ST_TIMEOUT ? TST_ERR_TIMEOUT : TST_ERR_DEVICE_CHECK;
+}
+
+tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8_t* A, const int8_t* B, void* D,
+                         const float* row_scale, const float* col_scale, const float* bias, void* stream) {
+  if (p == nullptr || A == nullptr || B == nullptr || D == nullptr || row_scale == nullptr || col_scale == nullptr)
+    return TST_ERR_INVALID_ARG;
+  if ((p->sched.groups > 0) != (group_rows != nullptr) || (p->opts.has_bias && bias == nullptr)) return TST_ERR_INVALID_ARG;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, p->opts.out_dtype == TST_OUT_F32 ? 4 : 2) || !aligned(group_rows, 4) ||
+      !aligned(row_scale, 4) || !aligned(col_scale, 4) || (p->opts.has_bias && !aligned(bias, 4)))
+    return TST_ERR_ALIGNMENT;
+  if (p->opts.host_only) return TST_ERR_NO_DEVICE;
+  int now = -1;
+  if (cudaGetDevice(&now) != cudaSuccess) {
+    cudaGetLastError();
+    return TST_ERR_CUDA;
+  }
+  if (now != p->device) return TST_ERR_INVALID_ARG;
+  tst::KernelParams kp = {};
+  if (!tst_encode_bytes(&kp.tmap_a, A, p->M, p->K, p->tokens) ||
+      !tst_encode_bytes(&kp.tmap_b, B, std::max<int64_t>(p->sched.groups, 1) * p->N, p->K, 128))
+    return TST_ERR_CUDA;
+  kp.C = D;
+  kp.bias = p->opts.has_bias ? bias : nullptr;
+  kp.has_bias = p->opts.has_bias ? 1 : 0;
+  kp.relu = p->opts.relu ? 1 : 0;
+  kp.ext.row_scale = row_scale;
+  kp.ext.col_scale = col_scale;
+  kp.status = p->d_status;
+  kp.run_id = kp.status_floor = kStatusTag;
+  kp.M = static_cast<int32_t>(p->M);
+  kp.N = static_cast<int32_t>(p->N);
+  kp.K = static_cast<int32_t>(p->K);
+  kp.sched = p->sched;
+  kp.sched.group_rows = group_rows;
+  kp.timeout_ns = p->opts.timeout_ns > 0 ? static_cast<uint64_t>(p->opts.timeout_ns) : 10ull * 1000 * 1000 * 1000;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p->sched.grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(p->kernel.threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p->kernel.smem_bytes);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  void* args[] = {&kp};
+  if (cudaLaunchKernelExC(&cfg, p->kernel.kernel, args) != cudaSuccess) {
+    cudaGetLastError();
+    return TST_ERR_CUDA;
+  }
+  p->last_stream = static_cast<cudaStream_t>(stream);
+  p->ran = true;
+  return TST_OK;
+}
+
+}  // extern "C"

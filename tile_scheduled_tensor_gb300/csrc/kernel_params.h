@@ -308,6 +308,16 @@ struct TstBsKernel {
 TstBsKernel tst_bs_wide(int out_type);
 TstBsKernel tst_bs_narrow(int rows, int out_type, bool shared);
 
+// GEMM of 8-bit integers (gemm_int8.cu): `tokens` = 16, 32, 64 or 128 rows of A per tile
+struct TstInt8Kernel {
+  const void* kernel;
+  int smem_bytes, threads, per_sm;
+};
+TstInt8Kernel tst_int8_kernel(int tokens, int out_type);
+
+// A tensor map of rows x K bytes, K contiguous, in boxes of box_rows x 128 with the 128-byte swizzle
+bool tst_encode_bytes(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, int box_rows);
+
 inline int tst_kernel_threads(int bn, int ka, bool ext = false) {
   return ((bn == 128 && ka == 2) ? tst::kThreadsDual : tst::kThreads) + (ext ? 128 : 0);
 }
