@@ -75,7 +75,8 @@ typedef enum {
 
 /* output element type.  TST_OUT_E4M3 rounds to nearest even and saturates to
  * +-448 (the clamping mode of "H100 . WGMMA Part 2", section 10). */
-typedef enum { TST_OUT_F32 = 0, TST_OUT_BF16 = 1, TST_OUT_E4M3 = 2 } tst_out_dtype;
+typedef enum { TST_OUT_F32 = 0, TST_OUT_BF16 = 1, TST_OUT_E4M3 = 2,
+               TST_OUT_INT8 = 3   /* rows of moe_dispatch only */ } tst_out_dtype;
 
 /* A M x K (K contiguous), B N x K (K contiguous), C M x N row-major ("TN").
  * e4m3 tensor-core operands must be K-major, which this layout is. */
@@ -666,6 +667,26 @@ typedef struct {
  * other than sm_103), OOM, CUDA, NO_DEVICE. */
 tst_status moe_plan_create(tst_moe_plan **plan, int64_t max_tokens, int32_t experts, int32_t top_k,
                            const tst_moe_options *opts);
+
+/* A plan for routing by scores (moe_route_scored): the same, and its other calls as for any plan. */
+typedef enum { TST_SCORE_SOFTMAX = 0, TST_SCORE_SIGMOID = 1 } tst_moe_score;
+typedef struct {
+    int32_t score;        /* tst_moe_score */
+    int32_t groups;       /* the experts in groups of experts / groups adjacent ones; 1: no groups */
+    int32_t top_groups;   /* groups that a token's experts come from, 1 .. groups */
+    int32_t group_best;   /* 1 or 2: a group's value is the sum of that many of its largest values */
+    int32_t normalize;    /* as in tst_moe_options */
+    float weight_scale;   /* factor of the weights */
+    float balance_coef;
+    int32_t host_only;
+} tst_moe_score_options;
+/* Errors as moe_plan_create, and INVALID_ARG (groups that do not divide the experts, top_groups or
+ * group_best out of range, group_best beyond a group's size, top_k beyond the experts of top_groups
+ * groups, a weight_scale that is no number or infinite), UNSUPPORTED (more than 32 groups, or groups
+ * of more than 32 * L experts where L is 32 / groups rounded down to a power of two). */
+tst_status moe_plan_create_scored(tst_moe_plan **plan, int64_t max_tokens, int32_t experts, int32_t top_k,
+                                  const tst_moe_score_options *opts);
+
 tst_status moe_plan_get_info(const tst_moe_plan *plan, tst_moe_plan_info *info);
 /* NULL is accepted. */
 tst_status moe_plan_destroy(tst_moe_plan *plan);
@@ -697,6 +718,25 @@ tst_status moe_route(tst_moe_plan *plan, int64_t tokens, const void *logits, int
                      const uint8_t *mask, int32_t *expert, float *weight, int32_t *row, int32_t *counts,
                      int32_t *totals, float *loss, void *stream);
 
+/* The same by scores, for a plan of moe_plan_create_scored.  With s = 1 / (1 + e^-l), or the softmax of the
+ * open logits, and c = s + bias[e] (bias: FP32[experts], NULL: 0), computed as FP64 values, a NaN counting
+ * as +inf:
+ *
+ *   group value   the sum of the group_best largest c of the group's open experts (of fewer where
+ *                 fewer are open); the top_groups groups of the largest values stay (ties: the
+ *                 lower group)
+ *   expert[t][j]  the token's top_k experts of those groups by falling c (ties: the lower expert
+ *                 first); one whose c is -inf is never chosen; -1 where fewer are left
+ *   weight[t][j]  weight_scale * s of that expert, divided by the sum of s over j when the plan
+ *                 normalizes; 0 where expert is -1.  The bias is in no weight.
+ *   loss          as above with p = s / (the sum of s over the open experts)
+ *
+ * row, counts and totals as above.  For every finite logit the weights, shares and gradients are finite
+ * (ratios of scores that underflow are taken from the logits). */
+tst_status moe_route_scored(tst_moe_plan *plan, int64_t tokens, const void *logits, int32_t dtype, int64_t ld,
+                            const uint8_t *mask, const float *bias, int32_t *expert, float *weight, int32_t *row,
+                            int32_t *counts, int32_t *totals, float *loss, void *stream);
+
 /* The logits' gradient, given moe_route's inputs and its expert, counts and totals, the
  * gradient d_weight of the weights (NULL: none) and that of the loss (d_loss, FP32[1], NULL:
  * none).  The counts are constants of the loss.  Closed tokens and experts get 0.  d_logits
@@ -706,16 +746,26 @@ tst_status moe_route_backward(tst_moe_plan *plan, int64_t tokens, const void *lo
                               const int32_t *totals, const float *d_weight, const float *d_loss, void *d_logits,
                               int64_t d_ld, void *stream);
 
+/* The same for moe_route_scored; the choice and the counts are constants. */
+tst_status moe_route_scored_backward(tst_moe_plan *plan, int64_t tokens, const void *logits, int32_t dtype, int64_t ld,
+                                     const uint8_t *mask, const int32_t *expert, const int32_t *counts,
+                                     const int32_t *totals, const float *d_weight, const float *d_loss, void *d_logits,
+                                     int64_t d_ld, void *stream);
+
 /* rows[row[t][j]] = x[t] for every token and choice with row >= 0.  x: tokens x hidden of
  * x_dtype (FP32 or BF16), rows x_ld elements apart; rows: n_rows x hidden, contiguous, of
  * x_dtype (copied) or TST_OUT_E4M3: then each 1 x 128 tile (the last may be narrower) of a
  * row has the FP32 scale s = max |x| / 448 (max |x| taken as at least 2^-96), written to
  * scales[n_rows][ceil(hidden / 128)], and holds x * (448 / max |x|) rounded to nearest even,
  * saturated to +-448: A and a_block_scales of a GEMM with ab_block (1, 128).  A NaN gives
- * its tile a NaN scale, an infinity an infinite one.  row = NULL: row t is token t (up to max_tokens
+ * its tile a NaN scale, an infinity an infinite one.  rows_dtype TST_OUT_INT8: each row has the
+ * FP32 scale s = max |x| / 127 (max |x| taken as at least 2^-96), written to scales[n_rows], and
+ * holds x * (127 / max |x|), rounded to FP32 and then to the nearest whole number, ties to even: A
+ * and row_scale of gemm_int8_run.  A NaN gives its row a NaN scale, an infinity an infinite one
+ * (the row's values are then not specified).  row = NULL: row t is token t (up to max_tokens
  * * top_k tokens), to quantize rows that are in order already.  Rows that no token names
  * stay as they were.  Errors: INVALID_ARG, UNSUPPORTED (a copy into another type),
- * ALIGNMENT (as moe_route; e4m3: hidden not a multiple of 16 or rows not 16-byte aligned),
+ * ALIGNMENT (as moe_route; e4m3 and int8: hidden not a multiple of 16 or rows not 16-byte aligned),
  * NO_DEVICE, CUDA. */
 tst_status moe_dispatch(tst_moe_plan *plan, int64_t tokens, int64_t hidden, const void *x, int32_t x_dtype,
                         int64_t x_ld, const int32_t *row, void *rows, int32_t rows_dtype, int64_t n_rows,

@@ -154,3 +154,129 @@ def combine_backward(rows, row, weight, d_out):
         d_weight[has, j] = np.sum(d_out[has] * rows[r], axis=1)
         size[has, j] = np.sum(np.abs(d_out[has] * rows[r]), axis=1)
     return d_rows, d_weight, size
+
+
+# ------------------------------------------------------------------ routing by scores
+def scores(l, sigmoid):
+    """Sigmoid or softmax scores of one token's FP64 logits (-inf: closed, 0)."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        if sigmoid:
+            return 1.0 / (1.0 + np.exp(-l))
+        x = np.exp(l - (np.nan if np.isnan(l).any() else l.max()))
+        return x / x.sum()
+
+
+def shares(l, sigmoid):
+    """Scores over their sum, from the logits where the scores themselves would vanish."""
+    if sigmoid and l.max() < -30.0:   # 1 / (1 + e^-l) = e^l (1 + O(e^-30)) / ...: exact to 1e-13
+        x = np.exp(l - l.max())
+        return x / x.sum()
+    s = scores(l, sigmoid)
+    return s / s.sum()
+
+
+def route_scored(logits, top_k, sigmoid, bias=None, groups=1, top_groups=1, best=1, normalize=True, scale=1.0, coef=0.0,
+                 mask=None):
+    """expert, weight, row, counts, totals, loss of FP64 logits (T x E) by the definition of moe_route_scored."""
+    l = np.array(logits, dtype=np.float64)
+    T, E = l.shape
+    if mask is not None:
+        l[np.asarray(mask) == 0] = -np.inf
+    b = np.zeros(E) if bias is None else np.asarray(bias, dtype=np.float64)
+    size = E // groups
+    expert = np.full((T, top_k), -1, dtype=np.int32)
+    weight, prob, live = np.zeros((T, top_k)), np.zeros(E), 0
+    for t in range(T):
+        open_ = l[t] != -np.inf
+        if not open_.any():
+            continue
+        live += 1
+        s = scores(l[t], sigmoid)
+        with np.errstate(invalid="ignore"):
+            c = s + b
+        c = np.where(np.isnan(c), np.inf, c)
+        c[~open_] = -np.inf
+        prob += np.where(open_, shares(l[t], sigmoid), 0.0)
+        value = []
+        for g in range(groups):
+            top = np.sort(c[g * size:(g + 1) * size])[::-1][:best]
+            value.append(top[top > -np.inf].sum() if top[0] > -np.inf else -np.inf)
+        keep = sorted(range(groups), key=lambda g: (-value[g], g))[:top_groups]
+        pool = [e for g in keep for e in range(g * size, (g + 1) * size) if c[e] > -np.inf]
+        chosen = sorted(pool, key=lambda e: (-c[e], e))[:top_k]
+        if chosen:
+            w = shares(l[t, chosen], sigmoid) if normalize else s[chosen]
+            expert[t, :len(chosen)] = chosen
+            weight[t, :len(chosen)] = w * scale
+    counts = np.bincount(expert[expert >= 0], minlength=E).astype(np.int32)
+    first = np.concatenate([[0], np.cumsum(counts)[:-1]])
+    row = np.full((T, top_k), -1, dtype=np.int32)
+    for e in range(E):
+        at = np.argwhere(expert == e)
+        row[at[:, 0], at[:, 1]] = first[e] + np.arange(len(at))
+    R = int(counts.sum())
+    loss = coef * E * float(np.sum(counts / max(R, 1) * (prob / max(live, 1)))) if R else 0.0
+    return dict(expert=expert, weight=weight, row=row, counts=counts, totals=np.array([R, live], dtype=np.int32), loss=loss)
+
+
+def route_scored_loss(logits, weights_dot, d_loss, r, sigmoid, normalize, scale, coef, mask=None):
+    """sum(weights_dot * weight) + d_loss * loss as a function of the logits, the choice r and its counts fixed: what
+    moe_route_scored_backward differentiates."""
+    l = np.array(logits, dtype=np.float64)
+    E = l.shape[1]
+    if mask is not None:
+        l[np.asarray(mask) == 0] = -np.inf
+    R, n = (max(int(v), 1) for v in r["totals"])
+    total = 0.0
+    for t in range(l.shape[0]):
+        if not (l[t] > -np.inf).any():
+            continue
+        total += d_loss * coef * E * float(np.sum(r["counts"] / R * shares(l[t], sigmoid))) / n
+        s = r["expert"][t][r["expert"][t] >= 0]
+        if len(s):
+            w = shares(l[t, s], sigmoid) if normalize else scores(l[t], sigmoid)[s]
+            total += scale * float(np.sum(weights_dot[t][:len(s)] * w))
+    return total
+
+
+def route_scored_backward(logits, d_weight, d_loss, r, sigmoid, normalize, scale, coef, mask=None):
+    """The gradient of route_scored_loss, and per element the sum of the magnitudes it adds up."""
+    l = np.array(logits, dtype=np.float64)
+    T, E = l.shape
+    if mask is not None:
+        l[np.asarray(mask) == 0] = -np.inf
+    R, n = (max(int(v), 1) for v in r["totals"])
+    g = d_loss * coef * E * r["counts"].astype(np.float64) / (R * n)
+    out, size = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        open_ = l[t] > -np.inf
+        if not open_.any():
+            continue
+        p = np.where(open_, shares(l[t], sigmoid), 0.0)
+        u, m = p * (g - np.sum(p * g)), p * (np.abs(g) + np.sum(p * np.abs(g)))
+        s = r["expert"][t][r["expert"][t] >= 0]
+        if len(s):
+            dw = scale * d_weight[t][:len(s)]
+            if normalize:
+                q = shares(l[t, s], sigmoid)
+                u[s] += q * (dw - np.sum(q * dw))
+                m[s] += q * (np.abs(dw) + np.sum(q * np.abs(dw)))
+            else:
+                sc = scores(l[t], sigmoid)[s]
+                u[s] += sc * dw
+                m[s] += sc * np.abs(dw)
+        with np.errstate(over="ignore"):
+            rest = 1.0 / (1.0 + np.exp(l[t]))   # 1 - s
+        out[t] = u * rest if sigmoid else u - p * u.sum()
+        size[t] = m * rest if sigmoid else m + p * m.sum()
+        out[t][~open_], size[t][~open_] = 0.0, 0.0
+    return out, size
+
+
+def quantize_int8(x):
+    """int8 values and FP32 scales of the rows of FP32 x, with the FP32 steps of the definition."""
+    x = np.asarray(x, dtype=np.float32)
+    amax = np.maximum(np.abs(x).max(axis=1), np.float32(2.0 ** -96))
+    with np.errstate(invalid="ignore"):
+        v = x * (np.float32(127.0) / amax)[:, None]
+        return np.rint(v), amax / np.float32(127.0)

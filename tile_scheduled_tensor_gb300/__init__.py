@@ -12,7 +12,8 @@ import ctypes
 
 from . import _capi
 from ._capi import (TST_BF16, TST_E4M3, TST_E5M2, TST_E4M3_E5M2, TST_E5M2_E4M3,  # noqa: F401
-                    TST_OUT_F32, TST_OUT_BF16, TST_OUT_E4M3, TST_LAYOUT_A_ROW_B_NK,
+                    TST_OUT_F32, TST_OUT_BF16, TST_OUT_E4M3, TST_OUT_INT8, TST_LAYOUT_A_ROW_B_NK,
+                    TST_SCORE_SOFTMAX, TST_SCORE_SIGMOID,
                     TST_ACT_NONE, TST_ACT_RELU, TST_ACT_GELU, TST_ACT_SILU, TST_BIAS_NONE, TST_BIAS_COL,
                     TST_BIAS_ROW,
                     TST_MAP_LINEAR_NFAST, TST_MAP_LINEAR_MFAST, TST_MAP_GROUPED_M, TST_MAP_GROUPED_N,
@@ -451,9 +452,10 @@ def gemm_int8_plan_destroy(plan: Int8Plan):
 class MoePlan:
     """Owns a tst_moe_plan*; destroyed with the object (or explicitly via destroy())."""
 
-    def __init__(self, handle: int, max_tokens: int, experts: int, top_k: int):
+    def __init__(self, handle: int, max_tokens: int, experts: int, top_k: int, scored: bool = False):
         self.handle = handle
         self.max_tokens, self.experts, self.top_k = max_tokens, experts, top_k
+        self.scored = scored   # routes by scores (moe_plan_create's score)
 
     def destroy(self):
         if self.handle:
@@ -473,16 +475,35 @@ class MoePlan:
         return self.handle
 
 
+_SCORE = {"softmax": TST_SCORE_SOFTMAX, "sigmoid": TST_SCORE_SIGMOID}
+
+
 def moe_plan_create(max_tokens: int, experts: int, top_k: int, normalize: bool = True, balance_coef: float = 0.01,
-                    host_only: bool = False) -> MoePlan:
+                    host_only: bool = False, score=None, groups: int = 1, top_groups=None, group_best: int = 1,
+                    weight_scale: float = 1.0) -> MoePlan:
     """Plan the calls around a grouped GEMM whose groups are experts: up to max_tokens tokens per
     call, each sent to top_k of `experts` experts.  normalize: a token's weights are divided by
-    their sum; balance_coef: factor of the balance loss."""
-    opts = _capi.tst_moe_options(int(bool(normalize)), float(balance_coef), int(bool(host_only)))
+    their sum; balance_coef: factor of the balance loss.
+
+    score ('softmax' or 'sigmoid'): moe_route chooses by scores and takes a bias per expert.  Of `groups`
+    groups of adjacent experts each token uses the top_groups (None: all) whose group_best (1 or 2)
+    largest values have the largest sum; the weights, scores without the bias, are multiplied by
+    weight_scale."""
     h = ctypes.c_void_p()
-    _check(lib.moe_plan_create(ctypes.byref(h), int(max_tokens), int(experts), int(top_k), ctypes.byref(opts)),
-           "moe_plan_create")
-    return MoePlan(h.value, int(max_tokens), int(experts), int(top_k))
+    if score is None:
+        if groups != 1 or top_groups not in (None, 1) or group_best != 1 or weight_scale != 1.0:
+            raise ValueError("groups, top_groups, group_best and weight_scale need a score, 'softmax' or 'sigmoid'")
+        opts = _capi.tst_moe_options(int(bool(normalize)), float(balance_coef), int(bool(host_only)))
+        _check(lib.moe_plan_create(ctypes.byref(h), int(max_tokens), int(experts), int(top_k), ctypes.byref(opts)),
+               "moe_plan_create")
+    else:
+        opts = _capi.tst_moe_score_options(_enum(_SCORE, score, "score"), int(groups),
+                                           int(groups if top_groups is None else top_groups), int(group_best),
+                                           int(bool(normalize)), float(weight_scale), float(balance_coef),
+                                           int(bool(host_only)))
+        _check(lib.moe_plan_create_scored(ctypes.byref(h), int(max_tokens), int(experts), int(top_k),
+                                          ctypes.byref(opts)), "moe_plan_create_scored")
+    return MoePlan(h.value, int(max_tokens), int(experts), int(top_k), score is not None)
 
 
 def moe_plan_get_info(plan: MoePlan):
@@ -502,7 +523,7 @@ def moe_status_query(plan: MoePlan) -> int:
 
 
 _OUT_OF = {"torch.float32": TST_OUT_F32, "torch.bfloat16": TST_OUT_BF16, "torch.float8_e4m3fn": TST_OUT_E4M3,
-           "torch.uint8": TST_OUT_E4M3}
+           "torch.uint8": TST_OUT_E4M3, "torch.int8": TST_OUT_INT8}
 _out_cache = {}   # torch dtype -> tst_out_dtype, so that a call does not print a dtype's name each time
 
 
@@ -553,18 +574,25 @@ def _token_mask(mask, tokens: int):
     return mask.data_ptr()
 
 
-def moe_route(plan: MoePlan, logits, expert, weight, row, counts, totals, loss, mask=None, stream=None):
+def moe_route(plan: MoePlan, logits, expert, weight, row, counts, totals, loss, mask=None, stream=None, bias=None):
     """Route each row of logits (tokens x experts, FP32 or BF16) to its top_k experts.  Written:
     expert, row (int32) and weight (FP32), tokens x top_k; counts (int32, per expert: the grouped
     GEMM's group_rows); totals (int32 {rows in all, tokens routed}); loss (FP32, one element).  mask:
-    one byte per token, 0 for a token that is not routed."""
+    one byte per token, 0 for a token that is not routed.  bias (plans with a score): FP32 per expert,
+    added to the scores for the choice alone."""
     ptr, t, _, ld = _matrix(logits, "logits", cols=plan.experts)
     n = t * plan.top_k
-    _check(lib.moe_route(plan._h, t, ptr, _out_of(logits, "logits"), ld, _token_mask(mask, t),
-                         _array(expert, "expert", "int32", n), _array(weight, "weight", "float32", n),
-                         _array(row, "row", "int32", n), _array(counts, "counts", "int32", plan.experts),
-                         _array(totals, "totals", "int32", 2), _array(loss, "loss", "float32", 1),
-                         _stream(stream)), "moe_route")
+    args = (_array(expert, "expert", "int32", n), _array(weight, "weight", "float32", n), _array(row, "row", "int32", n),
+            _array(counts, "counts", "int32", plan.experts), _array(totals, "totals", "int32", 2),
+            _array(loss, "loss", "float32", 1), _stream(stream))
+    if plan.scored:
+        b = None if bias is None else _array(bias, "bias", "float32", plan.experts)
+        _check(lib.moe_route_scored(plan._h, t, ptr, _out_of(logits, "logits"), ld, _token_mask(mask, t), b, *args),
+               "moe_route_scored")
+        return
+    if bias is not None:
+        raise ValueError("a bias needs a plan with a score")
+    _check(lib.moe_route(plan._h, t, ptr, _out_of(logits, "logits"), ld, _token_mask(mask, t), *args), "moe_route")
 
 
 def moe_route_backward(plan: MoePlan, logits, expert, counts, totals, d_logits, d_weight=None, d_loss=None, mask=None,
@@ -577,12 +605,13 @@ def moe_route_backward(plan: MoePlan, logits, expert, counts, totals, d_logits, 
     if d_logits.dtype != logits.dtype:
         raise ValueError(f"d_logits must have the logits' type, {logits.dtype}")
     n = t * plan.top_k
-    _check(lib.moe_route_backward(plan._h, t, ptr, _out_of(logits, "logits"), ld, _token_mask(mask, t),
-                                  _array(expert, "expert", "int32", n), _array(counts, "counts", "int32", plan.experts),
-                                  _array(totals, "totals", "int32", 2),
-                                  None if d_weight is None else _array(d_weight, "d_weight", "float32", n),
-                                  None if d_loss is None else _array(d_loss, "d_loss", "float32", 1),
-                                  dptr, d_ld, _stream(stream)), "moe_route_backward")
+    call, name = (lib.moe_route_scored_backward, "moe_route_scored_backward") if plan.scored else \
+        (lib.moe_route_backward, "moe_route_backward")
+    _check(call(plan._h, t, ptr, _out_of(logits, "logits"), ld, _token_mask(mask, t),
+                _array(expert, "expert", "int32", n), _array(counts, "counts", "int32", plan.experts),
+                _array(totals, "totals", "int32", 2),
+                None if d_weight is None else _array(d_weight, "d_weight", "float32", n),
+                None if d_loss is None else _array(d_loss, "d_loss", "float32", 1), dptr, d_ld, _stream(stream)), name)
 
 
 def _whole_rows(x, what: str, cols=None):
@@ -598,15 +627,15 @@ def _whole_rows(x, what: str, cols=None):
 
 def moe_dispatch(plan: MoePlan, x, row, rows, scales=None, stream=None):
     """rows[row[t][j]] = x[t].  rows of x's type: copied; rows of float8_e4m3fn (or uint8): quantized
-    with one FP32 scale per 128 elements, written to scales (rows x ceil(hidden / 128)).  row None:
-    row t is token t."""
+    with one FP32 scale per 128 elements, written to scales (rows x ceil(hidden / 128)); rows of int8: with
+    one per row, written to scales (one per row).  row None: row t is token t."""
     ptr, t, h, ld = _matrix(x, "x")
     out, n, _ = _whole_rows(rows, "rows", h)
     code = _out_of(rows, "rows")
-    if code == TST_OUT_E4M3:
+    if code in (TST_OUT_E4M3, TST_OUT_INT8):
         if scales is None:
-            raise ValueError("e4m3 rows need scales")
-        sptr = _array(scales, "scales", "float32", n * -(-h // 128))
+            raise ValueError("e4m3 and int8 rows need scales")
+        sptr = _array(scales, "scales", "float32", n * (1 if code == TST_OUT_INT8 else -(-h // 128)))
     else:
         sptr = None
     _check(lib.moe_dispatch(plan._h, t, h, ptr, _out_of(x, "x"), ld,

@@ -19,7 +19,8 @@ TST_ERR_DEVICE_CHECK = 7
 TST_ERR_NO_DEVICE = 8
 
 TST_BF16, TST_E4M3, TST_E5M2, TST_E4M3_E5M2, TST_E5M2_E4M3 = 0, 1, 2, 3, 4
-TST_OUT_F32, TST_OUT_BF16, TST_OUT_E4M3 = 0, 1, 2
+TST_OUT_F32, TST_OUT_BF16, TST_OUT_E4M3, TST_OUT_INT8 = 0, 1, 2, 3
+TST_SCORE_SOFTMAX, TST_SCORE_SIGMOID = 0, 1
 TST_ACT_NONE, TST_ACT_RELU, TST_ACT_GELU, TST_ACT_SILU = 0, 1, 2, 3
 TST_BIAS_NONE, TST_BIAS_COL, TST_BIAS_ROW = 0, 1, 2
 TST_LAYOUT_A_ROW_B_NK = 0
@@ -100,6 +101,11 @@ _P = ctypes.c_void_p
 _I32, _I64 = ctypes.c_int32, ctypes.c_int64
 
 
+class tst_moe_score_options(ctypes.Structure):
+    _fields_ = [("score", _I32), ("groups", _I32), ("top_groups", _I32), ("group_best", _I32), ("normalize", _I32),
+                ("weight_scale", ctypes.c_float), ("balance_coef", ctypes.c_float), ("host_only", _I32)]
+
+
 class tst_int8_options(ctypes.Structure):
     _fields_ = [("groups", _I32), ("out_dtype", _I32), ("has_bias", _I32), ("relu", _I32), ("host_only", _I32),
                 ("num_sms", _I32), ("timeout_ns", _I64)]
@@ -160,6 +166,10 @@ _SIGNATURES = {
     "moe_status_query": (ctypes.c_int, [_P]),
     "moe_route": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_route_backward": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "moe_plan_create_scored": (ctypes.c_int, [ctypes.POINTER(_P), _I64, _I32, _I32,
+                                              ctypes.POINTER(tst_moe_score_options)]),
+    "moe_route_scored": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_route_scored_backward": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
     "moe_dispatch": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _I64, _P, _P, _I32, _I64, _P, _P]),
     "moe_combine": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _I64, _P, _P, _P, _I32, _I64, _P]),
     "moe_combine_backward": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _I64, _P, _P, _P, _I32, _I64, _P, _P, _P]),

@@ -3,17 +3,25 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <new>
 
-#include "moe_route.cuh"
+#include "moe_finish.cuh"
+#include "moe_plan.h"
 #include "moe_rows.cuh"
+#include "moe_score.cuh"
 #include "tstgemm.h"
 
 struct tst_moe_plan {
   int64_t max_tokens = 0;
   int32_t experts = 0, top_k = 0, normalize = 0;
   float coef = 0.0f;
+  bool scored = false;         // moe_plan_create_scored
+  int32_t sigmoid = 0, groups = 1, top_groups = 1, best = 1;
+  int32_t lanes = 32, vpl = 1; // of a warp per group; logits per lane
+  float weight_scale = 1.0f;
+  TstScoreKernels score{};
   bool host_only = false;
   int device = -1;
   int32_t num_sms = 0;
@@ -59,6 +67,14 @@ int32_t route_warps(int32_t experts, int32_t chunk, int64_t chunks) {
 size_t route_smem(int32_t experts, int32_t top_k, int32_t chunk, int32_t warps) {
   const size_t staged = experts <= tst::kRouteThreadRow ? 2 * static_cast<size_t>(chunk) * (top_k | 1) : 0;
   return (static_cast<size_t>(experts) * (chunk / 32 + warps + 1) + 1 + staged) * 4;
+}
+
+// the same of a scored plan: a warp per row, `vpl` logits a lane
+int32_t score_warps(int32_t vpl, int32_t chunk, int64_t chunks) {
+  return chunk == 32 && chunks <= 152 && vpl <= 8 ? 32 : tst::kRouteWarps;
+}
+size_t score_smem(int32_t experts, int32_t chunk, int32_t warps) {
+  return (static_cast<size_t>(experts) * (chunk / 32 + warps + 2) + 1) * 4;
 }
 
 // Zero device memory before returning, on a stream of its own: cudaMemset is ordered with the default
@@ -193,20 +209,202 @@ bool slice(RowsParams& p, int64_t units, int64_t per_warp) {
   return ceil_div(p.tokens * p.slices, tst::kRowsThreads / 32) < (int64_t(1) << 31);
 }
 
+// int8 rows: a warp per token up to 2048 elements, else 128 threads
+template <typename T, bool VEC>
+tst_status launch_int8_of(const RowsParams& a, cudaStream_t s) {
+  const int64_t per_block = a.hidden <= 2048 ? 4 : 1, grid = ceil_div(a.tokens, per_block);
+  if (grid >= (int64_t(1) << 31)) return TST_ERR_UNSUPPORTED;
+  const unsigned g = static_cast<unsigned>(grid);
+  if (a.hidden <= 512) tst::dispatch_int8_kernel<T, VEC, 32, 1><<<g, 128, 0, s>>>(a);
+  else if (a.hidden <= 1024) tst::dispatch_int8_kernel<T, VEC, 32, 2><<<g, 128, 0, s>>>(a);
+  else if (a.hidden <= 2048) tst::dispatch_int8_kernel<T, VEC, 32, 4><<<g, 128, 0, s>>>(a);
+  else if (a.hidden <= 4096) tst::dispatch_int8_kernel<T, VEC, 128, 2><<<g, 128, 0, s>>>(a);
+  else tst::dispatch_int8_kernel<T, VEC, 128, 4><<<g, 128, 0, s>>>(a);
+  return TST_OK;
+}
+template <typename T>
+tst_status launch_int8(const RowsParams& a, bool vec, cudaStream_t s) {
+  return vec ? launch_int8_of<T, true>(a, s) : launch_int8_of<T, false>(a, s);
+}
+
+// The launches that finish a routing call once its chunks' kernel is on the stream.
+bool finish_route(const RouteParams& a0, cudaStream_t s) {
+  RouteParams a = a0;
+  if (a.chunks == 1) return true;   // it has finished by itself
+  if (a.chunks > 1 && a.chunks <= tst::kFewChunks)
+    return launch(reinterpret_cast<const void*>(&tst::route_sum_place_kernel), a.chunks, tst::kRouteThreads,
+                  (3 * static_cast<size_t>(a.experts) + 1) * 4, s, a, true);
+  return launch(reinterpret_cast<const void*>(&tst::route_scan_kernel), ceil_div(a.experts + 1, tst::kRouteWarps),
+                tst::kRouteThreads, 0, s, a, true) &&
+         launch(reinterpret_cast<const void*>(&tst::route_place_kernel), std::max(a.chunks, 1), tst::kRouteThreads,
+                static_cast<size_t>(a.experts) * 4, s, a, true);
+}
+
+// whether rows of `ld` elements at `p` can be read in the packs of moe_score.cuh's ScoreMap
+bool whole_groups(const tst_moe_plan* p, const void* x, int64_t ld, int64_t elt) {
+  const int64_t w = std::min<int64_t>(p->vpl, 16 / elt);
+  return aligned(x, w * elt) && ld % w == 0 && (p->experts / p->groups) % w == 0;
+}
+
+// moe_route and moe_route_scored
+tst_status route(tst_moe_plan* p, bool scored, int64_t tokens, const void* logits, int32_t dtype, int64_t ld, const uint8_t* mask,
+                 const float* bias, int32_t* expert, float* weight, int32_t* row, int32_t* counts, int32_t* totals, float* loss,
+                 void* stream) {
+  const tst_status st = check_run(p, tokens, p ? p->max_tokens : 0);
+  if (st != TST_OK) return st;
+  if (p->scored != scored || !float_type(dtype) || ld < p->experts || counts == nullptr || totals == nullptr || loss == nullptr)
+    return TST_ERR_INVALID_ARG;
+  if (tokens > 0 && (logits == nullptr || expert == nullptr || weight == nullptr || row == nullptr))
+    return TST_ERR_INVALID_ARG;
+  if (!aligned(logits, type_bytes(dtype)) || !aligned(bias, 4) || !aligned(expert, 4) || !aligned(weight, 4) || !aligned(row, 4) ||
+      !aligned(counts, 4) || !aligned(totals, 4) || !aligned(loss, 4))
+    return TST_ERR_ALIGNMENT;
+  if (p->host_only) return TST_ERR_NO_DEVICE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  RouteParams a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.mask = mask;
+  a.expert = expert;
+  a.weight = weight;
+  a.row = row;
+  a.counts = counts;
+  a.totals = totals;
+  a.loss = loss;
+  a.part_count = p->d_part_count;
+  a.part_prob = p->d_part_prob;
+  a.prob = p->d_prob;
+  a.tokens = static_cast<int32_t>(tokens);
+  a.experts = p->experts;
+  a.top_k = p->top_k;
+  a.chunk = route_chunk(tokens);
+  a.chunks = static_cast<int32_t>(ceil_div(tokens, a.chunk));
+  a.normalize = p->normalize;
+  a.coef = p->coef;
+  bool ok = true;
+  if (tokens > 0 && scored) {
+    tst::ScoreParams b{};
+    b.r = a;
+    b.bias = bias;
+    b.groups = p->groups;
+    b.size = p->experts / p->groups;
+    b.lanes = p->lanes;
+    b.top_groups = p->top_groups;
+    b.best = p->best;
+    b.sigmoid = p->sigmoid;
+    b.weight_scale = p->weight_scale;
+    const int32_t warps = score_warps(p->vpl, a.chunk, a.chunks);
+    const void* f = p->score.rows(dtype == TST_OUT_BF16, p->vpl, whole_groups(p, logits, ld, type_bytes(dtype)), warps);
+    ok = launch(f, a.chunks, 32 * warps, score_smem(a.experts, a.chunk, warps), s, b);
+  } else if (tokens > 0) {
+    const int32_t warps = route_warps(a.experts, a.chunk, a.chunks);
+    const void* f = dtype == TST_OUT_F32 ? route_kernel<float>(a, warps) : route_kernel<__nv_bfloat16>(a, warps);
+    ok = launch(f, a.chunks, 32 * warps, route_smem(a.experts, a.top_k, a.chunk, warps), s, a);
+  }
+  if (!ok || !finish_route(a, s)) {
+    cudaGetLastError();
+    return TST_ERR_CUDA;
+  }
+  return finish(p, s);
+}
+
+// moe_route_backward and moe_route_scored_backward
+tst_status route_backward(tst_moe_plan* p, bool scored, int64_t tokens, const void* logits, int32_t dtype, int64_t ld,
+                          const uint8_t* mask, const int32_t* expert, const int32_t* counts, const int32_t* totals,
+                          const float* d_weight, const float* d_loss, void* d_logits, int64_t d_ld, void* stream) {
+  const tst_status st = check_run(p, tokens, p ? p->max_tokens : 0);
+  if (st != TST_OK) return st;
+  if (p->scored != scored || !float_type(dtype) || ld < p->experts || d_ld < p->experts || counts == nullptr || totals == nullptr)
+    return TST_ERR_INVALID_ARG;
+  if (tokens > 0 && (logits == nullptr || expert == nullptr || d_logits == nullptr)) return TST_ERR_INVALID_ARG;
+  if (!aligned(logits, type_bytes(dtype)) || !aligned(d_logits, type_bytes(dtype)) || !aligned(expert, 4) ||
+      !aligned(counts, 4) || !aligned(totals, 4) || !aligned(d_weight, 4) || !aligned(d_loss, 4))
+    return TST_ERR_ALIGNMENT;
+  if (p->host_only) return TST_ERR_NO_DEVICE;
+  if (tokens == 0) return TST_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  RouteGradParams a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.mask = mask;
+  a.expert = expert;
+  a.counts = counts;
+  a.totals = totals;
+  a.d_weight = d_weight;
+  a.d_loss = d_loss;
+  a.d_logits = d_logits;
+  a.d_ld = d_ld;
+  a.tokens = static_cast<int32_t>(tokens);
+  a.experts = p->experts;
+  a.top_k = p->top_k;
+  a.normalize = p->normalize;
+  a.coef = p->coef;
+  if (scored) {
+    tst::ScoreGradParams b{};
+    b.r = a;
+    b.size = p->experts / p->groups;
+    b.lanes = p->lanes;
+    b.groups = p->groups;
+    b.sigmoid = p->sigmoid;
+    b.weight_scale = p->weight_scale;
+    const int64_t elt = type_bytes(dtype);
+    const void* f = p->score.grad(dtype == TST_OUT_BF16, p->vpl, whole_groups(p, logits, ld, elt) && whole_groups(p, d_logits, d_ld, elt));
+    if (!launch(f, std::min<int64_t>(ceil_div(tokens, tst::kRouteWarps), 4 * p->num_sms), tst::kRouteThreads, 0, s, b)) {
+      cudaGetLastError();
+      return TST_ERR_CUDA;
+    }
+    return finish(p, s);
+  }
+  const void* f = dtype == TST_OUT_F32 ? grad_kernel<float>(a) : grad_kernel<__nv_bfloat16>(a);
+  const bool small = a.experts <= tst::kRouteThreadRow;
+  // a thread per row, in blocks small enough to spread few rows; or warps, four blocks per SM's worth
+  const int32_t threads = small ? (tokens <= 64 * p->num_sms ? 64 : tst::kRouteThreads) : tst::kRouteThreads;
+  const int64_t grid = small ? ceil_div(tokens, threads)
+                             : std::min<int64_t>(ceil_div(tokens, tst::kRouteWarps), 4 * p->num_sms);
+  if (!launch(f, grid, threads, 0, s, a)) {
+    cudaGetLastError();
+    return TST_ERR_CUDA;
+  }
+  return finish(p, s);
+}
+
 }  // namespace
 
-extern "C" {
-
-tst_status moe_plan_create(tst_moe_plan** out, int64_t max_tokens, int32_t experts, int32_t top_k,
-                           const tst_moe_options* opts) {
+tst_status tst_moe_create(tst_moe_plan** out, int64_t max_tokens, int32_t experts, int32_t top_k, const tst_moe_options* opts,
+                          const tst_moe_score_options* score, const TstScoreKernels* kernels) {
   if (out == nullptr) return TST_ERR_INVALID_ARG;
   *out = nullptr;
   if (opts == nullptr || max_tokens < 1 || experts < 1 || top_k < 1 || top_k > experts) return TST_ERR_INVALID_ARG;
   if (max_tokens * top_k >= (int64_t(1) << 31) || max_tokens >= (int64_t(1) << 31)) return TST_ERR_INVALID_ARG;
   if (!(opts->balance_coef == opts->balance_coef)) return TST_ERR_INVALID_ARG;
   if (experts > tst::kMoeMaxExperts || top_k > tst::kMoeMaxTopK) return TST_ERR_UNSUPPORTED;
+  int32_t lanes = 32, vpl = 1;
+  if (score != nullptr) {
+    if ((score->score != TST_SCORE_SOFTMAX && score->score != TST_SCORE_SIGMOID) || score->groups < 1 || experts % score->groups != 0 ||
+        score->top_groups < 1 || score->top_groups > score->groups)
+      return TST_ERR_INVALID_ARG;
+    const int32_t size = experts / score->groups;
+    if (score->group_best < 1 || score->group_best > 2 || score->group_best > size || top_k > score->top_groups * size)
+      return TST_ERR_INVALID_ARG;
+    if (!std::isfinite(score->weight_scale)) return TST_ERR_INVALID_ARG;
+    if (score->groups > 32) return TST_ERR_UNSUPPORTED;
+    while (lanes * score->groups > 32) lanes /= 2;   // 32 / groups, rounded down to a power of two
+    while (vpl * lanes < size) vpl *= 2;
+    if (vpl > 32) return TST_ERR_UNSUPPORTED;
+  }
   tst_moe_plan* p = new (std::nothrow) tst_moe_plan();
   if (p == nullptr) return TST_ERR_OOM;
+  if (score != nullptr) {
+    p->scored = true;
+    p->sigmoid = score->score == TST_SCORE_SIGMOID;
+    p->groups = score->groups;
+    p->top_groups = score->top_groups;
+    p->best = score->group_best;
+    p->lanes = lanes;
+    p->vpl = vpl;
+    p->weight_scale = score->weight_scale;
+    p->score = *kernels;
+  }
   p->max_tokens = max_tokens;
   p->experts = experts;
   p->top_k = top_k;
@@ -233,24 +431,32 @@ tst_status moe_plan_create(tst_moe_plan** out, int64_t max_tokens, int32_t exper
     p->device = dev;
     p->num_sms = sms;
     // each instance that a call of this plan may take, with and without whole packs
+    auto allow = [&](const void* f, size_t smem) {
+      cudaFuncAttributes have;
+      return cudaFuncGetAttributes(&have, f) == cudaSuccess &&
+             (have.maxDynamicSharedSizeBytes >= static_cast<int>(smem) ||
+              cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess);
+    };
+    bool ok = true;
     RouteParams a{};
     a.experts = experts;
     for (int64_t ld : {int64_t(1024), int64_t(1025)})
       for (int32_t chunk : {32, 256}) {
         a.ld = ld;
-        const int32_t warps = route_warps(experts, chunk, 1);
-        const int smem = static_cast<int>(route_smem(experts, top_k, chunk, warps));
-        for (const void* f : {route_kernel<float>(a, warps), route_kernel<__nv_bfloat16>(a, warps)}) {
-          cudaFuncAttributes have;
-          if (cudaFuncGetAttributes(&have, f) != cudaSuccess ||
-              (have.maxDynamicSharedSizeBytes < smem &&
-               cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)) {
-            cudaGetLastError();
-            delete p;
-            return TST_ERR_CUDA;
-          }
+        const int32_t warps = p->scored ? score_warps(vpl, chunk, 1) : route_warps(experts, chunk, 1);
+        if (p->scored) {
+          const size_t smem = score_smem(experts, chunk, warps);
+          for (bool bf16 : {false, true}) ok = ok && allow(p->score.rows(bf16, vpl, ld == 1024, warps), smem);
+        } else {
+          const size_t smem = route_smem(experts, top_k, chunk, warps);
+          ok = ok && allow(route_kernel<float>(a, warps), smem) && allow(route_kernel<__nv_bfloat16>(a, warps), smem);
         }
       }
+    if (!ok) {
+      cudaGetLastError();
+      delete p;
+      return TST_ERR_CUDA;
+    }
     if (cudaMalloc(&p->dev_block, p->dev_bytes) != cudaSuccess) {
       cudaGetLastError();
       delete p;
@@ -270,6 +476,13 @@ tst_status moe_plan_create(tst_moe_plan** out, int64_t max_tokens, int32_t exper
   }
   *out = p;
   return TST_OK;
+}
+
+extern "C" {
+
+tst_status moe_plan_create(tst_moe_plan** out, int64_t max_tokens, int32_t experts, int32_t top_k,
+                           const tst_moe_options* opts) {
+  return tst_moe_create(out, max_tokens, experts, top_k, opts, nullptr, nullptr);
 }
 
 tst_status moe_plan_destroy(tst_moe_plan* p) {
@@ -306,104 +519,27 @@ tst_status moe_status_query(tst_moe_plan* p) {
 tst_status moe_route(tst_moe_plan* p, int64_t tokens, const void* logits, int32_t dtype, int64_t ld,
                      const uint8_t* mask, int32_t* expert, float* weight, int32_t* row, int32_t* counts,
                      int32_t* totals, float* loss, void* stream) {
-  const tst_status st = check_run(p, tokens, p ? p->max_tokens : 0);
-  if (st != TST_OK) return st;
-  if (!float_type(dtype) || ld < p->experts || counts == nullptr || totals == nullptr || loss == nullptr)
-    return TST_ERR_INVALID_ARG;
-  if (tokens > 0 && (logits == nullptr || expert == nullptr || weight == nullptr || row == nullptr))
-    return TST_ERR_INVALID_ARG;
-  if (!aligned(logits, type_bytes(dtype)) || !aligned(expert, 4) || !aligned(weight, 4) || !aligned(row, 4) ||
-      !aligned(counts, 4) || !aligned(totals, 4) || !aligned(loss, 4))
-    return TST_ERR_ALIGNMENT;
-  if (p->host_only) return TST_ERR_NO_DEVICE;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  RouteParams a{};
-  a.logits = logits;
-  a.ld = ld;
-  a.mask = mask;
-  a.expert = expert;
-  a.weight = weight;
-  a.row = row;
-  a.counts = counts;
-  a.totals = totals;
-  a.loss = loss;
-  a.part_count = p->d_part_count;
-  a.part_prob = p->d_part_prob;
-  a.prob = p->d_prob;
-  a.tokens = static_cast<int32_t>(tokens);
-  a.experts = p->experts;
-  a.top_k = p->top_k;
-  a.chunk = route_chunk(tokens);
-  a.chunks = static_cast<int32_t>(ceil_div(tokens, a.chunk));
-  a.normalize = p->normalize;
-  a.coef = p->coef;
-  bool ok = true;
-  if (tokens > 0) {
-    const int32_t warps = route_warps(a.experts, a.chunk, a.chunks);
-    const void* f = dtype == TST_OUT_F32 ? route_kernel<float>(a, warps) : route_kernel<__nv_bfloat16>(a, warps);
-    ok = launch(f, a.chunks, 32 * warps, route_smem(a.experts, a.top_k, a.chunk, warps), s, a);
-  }
-  if (a.chunks == 1) {
-    // it has finished by itself
-  } else if (a.chunks > 1 && a.chunks <= tst::kFewChunks) {
-    ok = ok && launch(reinterpret_cast<const void*>(&tst::route_sum_place_kernel), a.chunks, tst::kRouteThreads,
-                      (3 * static_cast<size_t>(a.experts) + 1) * 4, s, a, true);
-  } else {
-    ok = ok &&
-         launch(reinterpret_cast<const void*>(&tst::route_scan_kernel), ceil_div(a.experts + 1, tst::kRouteWarps),
-                tst::kRouteThreads, 0, s, a, true) &&
-         launch(reinterpret_cast<const void*>(&tst::route_place_kernel), std::max(a.chunks, 1), tst::kRouteThreads,
-                static_cast<size_t>(a.experts) * 4, s, a, true);
-  }
-  if (!ok) {
-    cudaGetLastError();
-    return TST_ERR_CUDA;
-  }
-  return finish(p, s);
+  return route(p, false, tokens, logits, dtype, ld, mask, nullptr, expert, weight, row, counts, totals, loss, stream);
+}
+
+tst_status moe_route_scored(tst_moe_plan* p, int64_t tokens, const void* logits, int32_t dtype, int64_t ld,
+                            const uint8_t* mask, const float* bias, int32_t* expert, float* weight, int32_t* row,
+                            int32_t* counts, int32_t* totals, float* loss, void* stream) {
+  return route(p, true, tokens, logits, dtype, ld, mask, bias, expert, weight, row, counts, totals, loss, stream);
 }
 
 tst_status moe_route_backward(tst_moe_plan* p, int64_t tokens, const void* logits, int32_t dtype, int64_t ld,
                               const uint8_t* mask, const int32_t* expert, const int32_t* counts,
                               const int32_t* totals, const float* d_weight, const float* d_loss, void* d_logits,
                               int64_t d_ld, void* stream) {
-  const tst_status st = check_run(p, tokens, p ? p->max_tokens : 0);
-  if (st != TST_OK) return st;
-  if (!float_type(dtype) || ld < p->experts || d_ld < p->experts || counts == nullptr || totals == nullptr)
-    return TST_ERR_INVALID_ARG;
-  if (tokens > 0 && (logits == nullptr || expert == nullptr || d_logits == nullptr)) return TST_ERR_INVALID_ARG;
-  if (!aligned(logits, type_bytes(dtype)) || !aligned(d_logits, type_bytes(dtype)) || !aligned(expert, 4) ||
-      !aligned(counts, 4) || !aligned(totals, 4) || !aligned(d_weight, 4) || !aligned(d_loss, 4))
-    return TST_ERR_ALIGNMENT;
-  if (p->host_only) return TST_ERR_NO_DEVICE;
-  if (tokens == 0) return TST_OK;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  RouteGradParams a{};
-  a.logits = logits;
-  a.ld = ld;
-  a.mask = mask;
-  a.expert = expert;
-  a.counts = counts;
-  a.totals = totals;
-  a.d_weight = d_weight;
-  a.d_loss = d_loss;
-  a.d_logits = d_logits;
-  a.d_ld = d_ld;
-  a.tokens = static_cast<int32_t>(tokens);
-  a.experts = p->experts;
-  a.top_k = p->top_k;
-  a.normalize = p->normalize;
-  a.coef = p->coef;
-  const void* f = dtype == TST_OUT_F32 ? grad_kernel<float>(a) : grad_kernel<__nv_bfloat16>(a);
-  const bool small = a.experts <= tst::kRouteThreadRow;
-  // a thread per row, in blocks small enough to spread few rows; or warps, four blocks per SM's worth
-  const int32_t threads = small ? (tokens <= 64 * p->num_sms ? 64 : tst::kRouteThreads) : tst::kRouteThreads;
-  const int64_t grid = small ? ceil_div(tokens, threads)
-                             : std::min<int64_t>(ceil_div(tokens, tst::kRouteWarps), 4 * p->num_sms);
-  if (!launch(f, grid, threads, 0, s, a)) {
-    cudaGetLastError();
-    return TST_ERR_CUDA;
-  }
-  return finish(p, s);
+  return route_backward(p, false, tokens, logits, dtype, ld, mask, expert, counts, totals, d_weight, d_loss, d_logits, d_ld, stream);
+}
+
+tst_status moe_route_scored_backward(tst_moe_plan* p, int64_t tokens, const void* logits, int32_t dtype, int64_t ld,
+                                     const uint8_t* mask, const int32_t* expert, const int32_t* counts,
+                                     const int32_t* totals, const float* d_weight, const float* d_loss, void* d_logits,
+                                     int64_t d_ld, void* stream) {
+  return route_backward(p, true, tokens, logits, dtype, ld, mask, expert, counts, totals, d_weight, d_loss, d_logits, d_ld, stream);
 }
 
 tst_status moe_dispatch(tst_moe_plan* p, int64_t tokens, int64_t hidden, const void* x, int32_t x_dtype, int64_t x_ld,
@@ -411,7 +547,7 @@ tst_status moe_dispatch(tst_moe_plan* p, int64_t tokens, int64_t hidden, const v
                         void* stream) {
   const tst_status st = check_run(p, tokens, p ? (row ? p->max_tokens : p->max_tokens * p->top_k) : 0);
   if (st != TST_OK) return st;
-  const bool quantize = rows_dtype == TST_OUT_E4M3;
+  const bool quantize = rows_dtype == TST_OUT_E4M3 || rows_dtype == TST_OUT_INT8;
   if (hidden < 1 || hidden >= (int64_t(1) << 30) || n_rows < 0 || n_rows >= (int64_t(1) << 31) || x_ld < hidden ||
       !float_type(x_dtype))
     return TST_ERR_INVALID_ARG;
@@ -437,10 +573,15 @@ tst_status moe_dispatch(tst_moe_plan* p, int64_t tokens, int64_t hidden, const v
   a.n_rows = n_rows;
   a.hidden = static_cast<int32_t>(hidden);
   a.top_k = p->top_k;
+  const bool vec16 = aligned(x, 16) && (x_ld * elt) % 16 == 0;
+  if (rows_dtype == TST_OUT_INT8) {
+    const tst_status l = x_dtype == TST_OUT_F32 ? launch_int8<float>(a, vec16, s) : launch_int8<__nv_bfloat16>(a, vec16, s);
+    return l != TST_OK ? l : finish(p, s);
+  }
   if (quantize) {
     if (!slice(a, hidden, 512)) return TST_ERR_UNSUPPORTED;
     const int32_t grid = row_grid(tokens * a.slices);
-    const bool vec = aligned(x, 16) && (x_ld * elt) % 16 == 0;
+    const bool vec = vec16;
     if (x_dtype == TST_OUT_F32) {
       if (vec) tst::dispatch_e4m3_kernel<float, true><<<grid, tst::kRowsThreads, 0, s>>>(a);
       else tst::dispatch_e4m3_kernel<float, false><<<grid, tst::kRowsThreads, 0, s>>>(a);

@@ -113,6 +113,83 @@ __global__ void __launch_bounds__(kRowsThreads) dispatch_e4m3_kernel(const RowsP
   }
 }
 
+// int8 rows with one FP32 scale each: scale = amax / 127, value = x (127 / amax), rounded to FP32 and then to
+// the nearest whole number, ties to even.  amax as above (a NaN or an infinity leaves its mark in the scale).
+// TPT threads hold a token, U pieces of 16 elements each, TPT pieces apart; what a token has beyond them is
+// read again for the values.  Adding 1.5 * 2^23 rounds a value of up to 127 and leaves its two's complement in
+// the low byte.
+constexpr float kInt8Max = 127.0f;
+template <typename T, bool VEC, int TPT, int U>
+__global__ void __launch_bounds__(TPT < 128 ? 128 : TPT) dispatch_int8_kernel(const RowsParams p) {
+  constexpr int BLOCK = TPT < 128 ? 128 : TPT, WARPS = BLOCK / 32;
+  __shared__ uint32_t part[WARPS];
+  const int lane = threadIdx.x & 31, at = threadIdx.x % TPT;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (BLOCK / TPT) + threadIdx.x / TPT;
+  const bool on = t < p.tokens;
+  const T* const src = static_cast<const T*>(p.x) + (on ? t : 0) * p.x_ld;
+  const int pieces = on ? p.hidden / 16 : 0;   // hidden is a multiple of 16
+  float v[U][16];
+  uint32_t bits = __float_as_uint(kScaleFloor);
+  auto widen = [&](const float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t a = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+      bits = a > bits ? a : bits;
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (at + u * TPT < pieces) load_f32<T, 16, VEC>(src + static_cast<int64_t>(at + u * TPT) * 16, v[u]);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (at + u * TPT < pieces) widen(v[u]);
+  for (int q = at + U * TPT; q < pieces; q += TPT) {
+    float x[16];
+    load_f32<T, 16, VEC>(src + static_cast<int64_t>(q) * 16, x);
+    widen(x);
+  }
+  bits = __reduce_max_sync(0xFFFFFFFFu, bits);
+  if constexpr (TPT > 32) {
+    if (lane == 0) part[threadIdx.x >> 5] = bits;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) bits = part[i] > bits ? part[i] : bits;
+  }
+  const float amax = __uint_as_float(bits);
+  const float scale = amax / kInt8Max, inv = kInt8Max / amax;
+  auto narrow = [&](const float (&x)[16]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__fadd_rn(__fmul_rn(x[4 * q + i], inv), 12582912.0f));
+      w[q] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  };
+  uint4 q[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (at + u * TPT < pieces) q[u] = narrow(v[u]);
+  if (!on) return;
+  const int k = p.row ? p.top_k : 1;
+  for (int j = 0; j < k; ++j) {
+    const int64_t r = p.row ? p.row[t * k + j] : t;
+    if (!row_ok(p, r)) continue;
+    uint4* const out = reinterpret_cast<uint4*>(static_cast<int8_t*>(p.out) + r * p.hidden);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at + u * TPT < pieces) out[at + u * TPT] = q[u];
+    for (int i = at + U * TPT; i < pieces; i += TPT) {
+      float x[16];
+      load_f32<T, 16, VEC>(src + static_cast<int64_t>(i) * 16, x);
+      out[i] = narrow(x);
+    }
+    if (at == 0) p.scales[r] = scale;
+  }
+}
+
 // Rows copied unchanged, in units U of 16 bytes where the addresses allow, else of one element.
 template <typename U>
 __global__ void __launch_bounds__(kRowsThreads) dispatch_copy_kernel(const RowsParams p) {
