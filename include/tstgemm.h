@@ -602,6 +602,7 @@ typedef struct {
     int32_t tile_rows, tile_cols;   /* rows of A (tokens) and columns of D per tile */
     int32_t grid;                   /* CTAs launched */
     int32_t smem_bytes;             /* dynamic shared memory per CTA */
+    int64_t workspace_bytes;        /* device bytes owned by the plan: with many tokens A in FP16, 2 M K */
 } tst_int8_plan_info;
 
 /* Errors: INVALID_ARG (null plan or opts, sizes < 1 or beyond int32, groups < 0, an out_dtype

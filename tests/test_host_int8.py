@@ -25,6 +25,7 @@ def test_plan_rules_and_info():
             _plan(**kw)
         assert e.value.status == status, kw
     _plan(K=131056), _plan(groups=512)
+    assert _plan(M=16384, N=4096).info.workspace_bytes >= 2 * 16384 * 512 > _plan(M=8).info.workspace_bytes   # FP16 tokens
     assert tst.lib.gemm_int8_plan_create(None, 1, 1, 16, None) == invalid
     h = ctypes.c_void_p(1)
     assert tst.lib.gemm_int8_plan_create(ctypes.byref(h), 1, 1, 16, None) == invalid and not h.value

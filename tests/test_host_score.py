@@ -16,7 +16,7 @@ def test_plan_rules():
     info = tst.moe_plan_get_info(_plan(normalize=False, balance_coef=0.5))
     assert (info.max_tokens, info.experts, info.top_k, info.normalize, info.balance_coef) == (100, 64, 8, 0, 0.5)
     for kw, status in ((dict(T=0), invalid), (dict(E=60), invalid), (dict(groups=0), invalid), (dict(top_groups=0), invalid), (dict(top_groups=9), invalid),
-                       (dict(group_best=0), invalid), (dict(group_best=3), invalid), (dict(k=33), invalid), (dict(top_groups=1, k=9), invalid),
+                       (dict(group_best=0), invalid), (dict(group_best=3), invalid), (dict(k=33), unsupported), (dict(top_groups=1, k=9), invalid),
                        (dict(groups=64, top_groups=32, group_best=2), invalid), (dict(score=2), invalid), (dict(weight_scale=float("nan")), invalid),
                        (dict(weight_scale=float("inf")), invalid), (dict(balance_coef=float("nan")), invalid),
                        (dict(groups=64, top_groups=32, group_best=1), unsupported), (dict(E=1028, groups=4), unsupported),
@@ -64,7 +64,8 @@ def test_route_refusals():
 
 
 def test_int8_row_refusals():
-    disp = dict(plan=_plan()._h, tokens=10, hidden=64, x=A16, x_dtype=BF16, x_ld=64, row=A4, rows=A16, rows_dtype=INT8, n_rows=80,
+    p = _plan()
+    disp = dict(plan=p._h, tokens=10, hidden=64, x=A16, x_dtype=BF16, x_ld=64, row=A4, rows=A16, rows_dtype=INT8, n_rows=80,
                 scales=A4, stream=None)
     d = lambda **kw: tst.lib.moe_dispatch(*dict(disp, **kw).values())  # noqa: E731
     assert d() == tst.TST_ERR_NO_DEVICE and d(row=None) == tst.TST_ERR_NO_DEVICE and d(x=A2) == tst.TST_ERR_NO_DEVICE

@@ -48,10 +48,12 @@ SHAPES = [(1, 1, 16), (1, 128, 128), (2, 3, 48), (16, 130, 1024), (17, 129, 1040
           (64, 128, 4096), (65, 127, 1008), (128, 256, 1152), (129, 300, 4112), (256, 384, 512), (257, 1000, 8208), (700, 513, 3088)]
 
 
+# num_sms 2: each CTA (or pair) takes many tiles, and the wide form is chosen wherever it can be
 @pytest.mark.parametrize("M,N,K", SHAPES)
-def test_sums_are_exact(M, N, K):
+@pytest.mark.parametrize("num_sms", [0, 2])
+def test_sums_are_exact(M, N, K, num_sms):
     A, B, _, _, _ = _operands(M + N + K, M, N, K, low=-128)
-    plan = tst.gemm_int8_plan_create(M, N, K, out_dtype="f32")
+    plan = tst.gemm_int8_plan_create(M, N, K, out_dtype="f32", num_sms=num_sms)
     D = _run(plan, A, B, np.ones(M, np.float32), np.ones(N, np.float32))
     assert tst.gemm_int8_status_query(plan) == tst.TST_OK
     assert np.array_equal(D.cpu().numpy(), int8.sums(A, B).astype(np.float32))
@@ -59,11 +61,12 @@ def test_sums_are_exact(M, N, K):
 
 @pytest.mark.parametrize("M,N,K", [(3, 5, 1024), (20, 140, 8192), (130, 260, 1040), (2, 3, 131056), (300, 260, 16384)])
 @pytest.mark.parametrize("a,b", [(-128, -128), (-128, 127), (127, 127)])
-def test_largest_magnitudes(M, N, K, a, b):
+@pytest.mark.parametrize("num_sms", [0, 2])
+def test_largest_magnitudes(M, N, K, a, b, num_sms):
     # every partial sum as large as it can be: 2^24 per accumulator, close to 2^31 over the longest K
     A, B = np.full((M, K), a, np.int8), np.full((N, K), b, np.int8)
     A[0, ::7], B[0, 1::5] = 1, -1   # and sums that are no multiple of a power of two
-    plan = tst.gemm_int8_plan_create(M, N, K, out_dtype="f32")
+    plan = tst.gemm_int8_plan_create(M, N, K, out_dtype="f32", num_sms=num_sms)
     D = _run(plan, A, B, np.ones(M, np.float32), np.ones(N, np.float32))
     assert np.array_equal(D.cpu().numpy(), int8.sums(A, B).astype(np.float32))
 
@@ -72,23 +75,24 @@ def test_largest_magnitudes(M, N, K, a, b):
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_scales_bias_relu(M, N, K, out):
     A, B, ra, cb, bias = _operands(7 * M + N, M, N, K)
-    for use_bias, relu in ((False, False), (True, True), (True, False)):
-        plan = tst.gemm_int8_plan_create(M, N, K, out_dtype=out, has_bias=use_bias, relu=relu)
+    for use_bias, relu, num_sms in ((False, False, 0), (True, True, 0), (True, False, 2)):
+        plan = tst.gemm_int8_plan_create(M, N, K, out_dtype=out, has_bias=use_bias, relu=relu, num_sms=num_sms)
         D = _run(plan, A, B, ra, cb, bias if use_bias else None)
         _check(D, *int8.gemm(A, B, ra, cb, bias if use_bias else None, relu))
 
 
 GROUPS = [("one", 1, 5, 130, 272, [5]), ("empty first and last", 5, 40, 200, 1040, [0, 17, 0, 23, 0]),
           ("one row each", 60, 60, 96, 144, [1] * 60), ("uneven", 7, 333, 257, 2064, [1, 200, 0, 33, 64, 32, 3]),
-          ("many", 300, 700, 130, 128, [(i * 7) % 5 for i in range(300)]), ("large", 3, 1500, 384, 1536, [129, 1000, 371]),
+          ("many", 300, 700, 130, 128, [(i * 7) % 5 for i in range(300)]), ("large", 3, 1500, 384, 1536, [129, 1000, 371]), ("large with rows to spare", 4, 1700, 300, 1040, [0, 600, 1, 500]),
           ("none", 4, 9, 64, 64, [0, 0, 0, 0])]
 
 
 @pytest.mark.parametrize("name,G,M,N,K,rows", GROUPS, ids=[g[0] for g in GROUPS])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-def test_grouped(name, G, M, N, K, rows, out):
+@pytest.mark.parametrize("num_sms", [0, 2])
+def test_grouped(name, G, M, N, K, rows, out, num_sms):
     A, B, ra, cb, bias = _operands(G + M, M, N, K, parts=G)
-    plan = tst.gemm_int8_plan_create(M, N, K, groups=G, out_dtype=out, has_bias=True)
+    plan = tst.gemm_int8_plan_create(M, N, K, groups=G, out_dtype=out, has_bias=True, num_sms=num_sms)
     D = _run(plan, A, B, ra, cb, bias, rows, fill=-77.0)
     assert tst.gemm_int8_status_query(plan) == tst.TST_OK
     used = sum(rows)
@@ -97,13 +101,15 @@ def test_grouped(name, G, M, N, K, rows, out):
     _check(D[:used], want, size)
 
 
-def test_rows_past_the_matrix_are_reported():
-    A, B, ra, cb, _ = _operands(3, 100, 64, 128, parts=3)
-    plan = tst.gemm_int8_plan_create(100, 64, 128, groups=3, out_dtype="f32")
-    D = _run(plan, A, B, ra, cb, None, [60, -4, 70])
+@pytest.mark.parametrize("scale,num_sms", [(1, 0), (10, 2)])
+def test_rows_past_the_matrix_are_reported(scale, num_sms):
+    M = 100 * scale
+    A, B, ra, cb, _ = _operands(3, M, 64, 128, parts=3)
+    plan = tst.gemm_int8_plan_create(M, 64, 128, groups=3, out_dtype="f32", num_sms=num_sms)
+    D = _run(plan, A, B, ra, cb, None, [60 * scale, -4, 70 * scale])
     assert tst.gemm_int8_status_query(plan) == tst.TST_ERR_DEVICE_CHECK
     assert tst.gemm_int8_status_query(plan) == tst.TST_OK   # reported once
-    want, size = int8.gemm(A, B, ra, cb, None, False, [60, 0, 40])
+    want, size = int8.gemm(A, B, ra, cb, None, False, [60 * scale, 0, 40 * scale])
     _check(D, want, size)
 
 
@@ -114,36 +120,38 @@ def test_scales_that_are_not_numbers_stay_visible():
     assert np.isnan(D[1]).all() and np.isnan(D[:, 3]).all() and np.isfinite(D[0, 4:]).all()
 
 
-def test_streams_and_graphs():
+@pytest.mark.parametrize("scale,num_sms", [(1, 0), (10, 2)])
+def test_streams_and_graphs(scale, num_sms):
     # a plan on another stream, and captured: the replay reads what its inputs hold then
-    G, M, N, K = 4, 90, 192, 1168
+    G, M, N, K = 4, 90 * scale, 192, 1168
     A, B, ra, cb, bias = _operands(9, M, N, K, parts=G)
     A2 = _operands(10, M, N, K)[0]
-    plan = tst.gemm_int8_plan_create(M, N, K, groups=G, out_dtype="f32", has_bias=True)
+    plan = tst.gemm_int8_plan_create(M, N, K, groups=G, out_dtype="f32", has_bias=True, num_sms=num_sms)
+    first, second = ([n * scale for n in rows] for rows in ([10, 0, 50, 30], [40, 41, 0, 9]))
     a, b, r, c, bs = (_dev(x) for x in (A, B, ra, cb, bias))
-    rows = torch.tensor([10, 0, 50, 30], dtype=torch.int32, device="cuda")
+    rows = torch.tensor(first, dtype=torch.int32, device="cuda")
     D = torch.empty(M, N, device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     tst.gemm_int8_run(plan, a, b, D, r, c, bias=bs, group_rows=rows, stream=s)
     s.synchronize()
-    _check(D, *int8.gemm(A, B, ra, cb, bias, False, [10, 0, 50, 30]))
+    _check(D, *int8.gemm(A, B, ra, cb, bias, False, first))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         tst.gemm_int8_run(plan, a, b, D, r, c, bias=bs, group_rows=rows)
     a.copy_(_dev(A2))
-    rows.copy_(torch.tensor([40, 41, 0, 9], dtype=torch.int32))
+    rows.copy_(torch.tensor(second, dtype=torch.int32))
     D.fill_(float("nan"))
     graph.replay()
     torch.cuda.synchronize()
-    _check(D, *int8.gemm(A2, B, ra, cb, bias, False, [40, 41, 0, 9]))
+    _check(D, *int8.gemm(A2, B, ra, cb, bias, False, second))
     assert tst.gemm_int8_status_query(plan) == tst.TST_OK
 
 
 def test_two_plans_at_once():
     # plans share nothing: two on two streams, many times
     jobs = []
-    for i, (M, N, K) in enumerate([(12, 1024, 2048), (200, 640, 1040)]):
+    for i, (M, N, K) in enumerate([(12, 1024, 2048), (200, 640, 1040), (4000, 1300, 528)]):
         A, B, ra, cb, _ = _operands(20 + i, M, N, K)
         jobs.append((tst.gemm_int8_plan_create(M, N, K, out_dtype="f32"), [_dev(x) for x in (A, B)], torch.empty(M, N, device="cuda"),
                      [_dev(x) for x in (ra, cb)], torch.cuda.Stream(), int8.gemm(A, B, ra, cb)))

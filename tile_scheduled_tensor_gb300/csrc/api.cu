@@ -250,6 +250,9 @@ int64_t hybrid_split_tiles(int64_t T, int64_t P) {
 bool tst_encode_bytes(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, int box_rows) {
   return encode_operand(map, ptr, TST_E4M3, rows, K, 128, box_rows);
 }
+bool tst_encode_halves(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, int box_rows) {
+  return encode_operand(map, ptr, TST_BF16, rows, K, 64, box_rows);
+}
 
 extern "C" {
 

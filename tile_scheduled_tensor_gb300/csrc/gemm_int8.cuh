@@ -245,6 +245,26 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
   }
 }
 
+// A thread's column of a tile: rows row0 .. row0 + N - 1 of D from their integer sums.  A warp stores 32
+// adjacent columns of a row at once.
+template <int N, int OUT>
+__device__ __forceinline__ void int8_store(const KernelParams& p, const Tile& w, int32_t row0, int32_t col, const int32_t (&sum)[N]) {
+  if (col >= p.N) return;
+  const int64_t channel = static_cast<int64_t>(w.group) * p.N + col;
+  const float cb = __ldg(p.ext.col_scale + channel);
+  const float b = p.has_bias ? __ldg(p.bias + channel) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int32_t row = row0 + i;
+    if (row >= w.row_end) break;
+    float z = fmaf(__int2float_rn(sum[i]) * __ldg(p.ext.row_scale + row), cb, b);
+    if (p.relu) z = z < 0.0f ? 0.0f : z;   // a NaN stays
+    const int64_t at = static_cast<int64_t>(row) * p.N + col;
+    if (OUT == OUT_BF16) reinterpret_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(z);
+    else reinterpret_cast<float*>(p.C)[at] = z;
+  }
+}
+
 template <class Cfg, int OUT>
 __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, const Int8Bars<Cfg>& bar) {
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
@@ -271,22 +291,7 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
       if (lane == 0) ptx::mbar_arrive(bar.acc_empty + 8 * acc.at);
       acc.next();
     }
-    const int32_t col = w.n * 128 + quad * 32 + lane;
-    if (col < p.N) {
-      const int64_t channel = static_cast<int64_t>(w.group) * p.N + col;
-      const float cb = __ldg(p.ext.col_scale + channel);
-      const float b = p.has_bias ? __ldg(p.bias + channel) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < Cfg::NT; ++i) {
-        const int32_t row = w.row0 + i;
-        if (row >= w.row_end) break;
-        float z = fmaf(__int2float_rn(sum[i]) * __ldg(p.ext.row_scale + row), cb, b);
-        if (p.relu) z = z < 0.0f ? 0.0f : z;   // a NaN stays
-        const int64_t at = static_cast<int64_t>(row) * p.N + col;
-        if (OUT == OUT_BF16) reinterpret_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(z);
-        else reinterpret_cast<float*>(p.C)[at] = z;
-      }
-    }
+    int8_store<Cfg::NT, OUT>(p, w, w.row0, w.n * 128 + quad * 32 + lane, sum);
   }
 }
 

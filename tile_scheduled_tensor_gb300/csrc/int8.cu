@@ -17,7 +17,8 @@ struct tst_int8_plan {
   int32_t num_sms = 0, device = -1;
   TstInt8Kernel kernel{};
   tst::Sched sched{};
-  unsigned long long* d_status = nullptr;
+  unsigned long long* d_status = nullptr;   // 256 bytes, then the FP16 tokens of the wide form
+  size_t dev_bytes = 0;
   cudaStream_t last_stream = nullptr;
   bool ran = false;
 };
@@ -40,8 +41,12 @@ bool zero_now(void* p, size_t bytes) {
   return cudaStreamDestroy(s) == cudaSuccess && ok;
 }
 
-// Rows of A per tile, by the rows of a group on average.
-int32_t tile_tokens(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Rows of A per tile, by the rows of a group on average and the tiles that leaves for the SMs.
+int32_t tile_tokens(int64_t rows, int64_t M, int64_t N, int32_t num_sms) {
+  const int64_t wide = ceil_div(M, kInt8WideTokens) * ceil_div(N, 256);
+  if (rows > 96 && 2 * wide >= num_sms) return kInt8WideTokens;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
 
 }  // namespace
 
@@ -59,18 +64,12 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   const int64_t groups = opts->groups;
   if (M > kMaxRows || N > kMaxRows || std::max<int64_t>(groups, 1) * N > kMaxRows || K > kMaxK || groups > kBsWalkGroups)
     return TST_ERR_UNSUPPORTED;
-  const int32_t tokens = tile_tokens(ceil_div(M, std::max<int64_t>(groups, 1)));
-  const int64_t mt = ceil_div(M, tokens), nt = ceil_div(N, 128);
-  const int64_t tiles = (mt + groups) * nt;   // grouped: at most, whatever the split
-  if (tiles >= (int64_t(1) << 30)) return TST_ERR_UNSUPPORTED;
   tst_int8_plan* p = new (std::nothrow) tst_int8_plan();
   if (p == nullptr) return TST_ERR_OOM;
   p->M = M;
   p->N = N;
   p->K = K;
   p->opts = *opts;
-  p->tokens = tokens;
-  p->kernel = tst_int8_kernel(tokens, opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32);
   p->num_sms = opts->num_sms;
   if (!opts->host_only) {
     int dev = 0, count = 0, major = 0, minor = 0, sms = 0;
@@ -86,12 +85,23 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
     if (major != 10 || minor != 3) { delete p; return TST_ERR_UNSUPPORTED; }  // built for sm_103a only
     p->device = dev;
     p->num_sms = opts->num_sms > 0 ? std::min(opts->num_sms, sms) : sms;
+  }
+  const int32_t tokens = tile_tokens(ceil_div(M, std::max<int64_t>(groups, 1)), M, N, p->num_sms);
+  p->tokens = tokens;
+  p->kernel = tst_int8_kernel(tokens, opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32);
+  const bool pairs = p->kernel.ctas == 2;
+  const int32_t cols = pairs ? 256 : 128;
+  const int64_t mt = ceil_div(M, tokens), nt = ceil_div(N, cols);
+  const int64_t tiles = (mt + groups) * nt;   // grouped: at most, whatever the split
+  if (tiles >= (int64_t(1) << 30)) { delete p; return TST_ERR_UNSUPPORTED; }
+  p->dev_bytes = 256 + (pairs ? 2 * static_cast<size_t>(M) * K : 0);
+  if (!opts->host_only) {
     if (cudaFuncSetAttribute(p->kernel.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p->kernel.smem_bytes) != cudaSuccess) {
       cudaGetLastError();
       delete p;
       return TST_ERR_CUDA;
     }
-    if (cudaMalloc(&p->d_status, 256) != cudaSuccess) {
+    if (cudaMalloc(&p->d_status, p->dev_bytes) != cudaSuccess) {
       cudaGetLastError();
       delete p;
       return TST_ERR_OOM;
@@ -110,11 +120,12 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   s.map_kind = tst::MAP_GROUPED_M;
   s.group = 8;
   s.dp_tiles = static_cast<int32_t>(mt * nt);
-  s.grid = static_cast<int32_t>(std::min<int64_t>(int64_t(p->num_sms) * p->kernel.per_sm, tiles));
+  s.grid = static_cast<int32_t>(std::min<int64_t>(int64_t(p->num_sms) * p->kernel.per_sm / p->kernel.ctas, tiles));
+  if (s.grid < 1) s.grid = 1;
   s.sk_groups = 1;
   s.rows = static_cast<int32_t>(M);
   s.bm = tokens;
-  s.bn = 128;
+  s.bn = cols;
   s.groups = static_cast<int32_t>(groups);
   s.group_b_rows = static_cast<int32_t>(N);
   s.cols = static_cast<int32_t>(N);
@@ -137,9 +148,10 @@ tst_status gemm_int8_plan_get_info(const tst_int8_plan* p, tst_int8_plan_info* i
   info->K = p->K;
   info->groups = p->sched.groups;
   info->tile_rows = p->tokens;
-  info->tile_cols = 128;
-  info->grid = p->sched.grid;
+  info->tile_cols = p->sched.bn;
+  info->grid = p->sched.grid * p->kernel.ctas;
   info->smem_bytes = p->kernel.smem_bytes;
+  info->workspace_bytes = static_cast<int64_t>(p->dev_bytes);
   return TST_OK;
 }
 
@@ -172,7 +184,10 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
   }
   if (now != p->device) return TST_ERR_INVALID_ARG;
   tst::KernelParams kp = {};
-  if (!tst_encode_bytes(&kp.tmap_a, A, p->M, p->K, p->tokens) ||
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool pairs = p->kernel.ctas == 2;
+  void* const half = p->d_status + 32;
+  if (!(pairs ? tst_encode_halves(&kp.tmap_a, half, p->M, p->K, p->tokens / 2) : tst_encode_bytes(&kp.tmap_a, A, p->M, p->K, p->tokens)) ||
       !tst_encode_bytes(&kp.tmap_b, B, std::max<int64_t>(p->sched.groups, 1) * p->N, p->K, 128))
     return TST_ERR_CUDA;
   kp.C = D;
@@ -190,16 +205,29 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
   kp.sched.group_rows = group_rows;
   kp.timeout_ns = p->opts.timeout_ns > 0 ? static_cast<uint64_t>(p->opts.timeout_ns) : 10ull * 1000 * 1000 * 1000;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p->sched.grid), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p->sched.grid * p->kernel.ctas), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(p->kernel.threads), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(p->kernel.smem_bytes);
-  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  if (pairs) {
+    // the pair as a cluster; it may start while the tokens are made FP16, and waits for them itself
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
   void* args[] = {&kp};
+  if (pairs && !tst_int8_widen(A, half, p->M, p->K, group_rows, p->sched.groups, p->num_sms, s)) return TST_ERR_CUDA;
   if (cudaLaunchKernelExC(&cfg, p->kernel.kernel, args) != cudaSuccess) {
     cudaGetLastError();
     return TST_ERR_CUDA;
   }
-  p->last_stream = static_cast<cudaStream_t>(stream);
+  p->last_stream = s;
   p->ran = true;
   return TST_OK;
 }
