@@ -600,6 +600,7 @@ typedef struct {
     int64_t M, N, K;
     int32_t groups;
     int32_t tile_rows, tile_cols;   /* rows of A (tokens) and columns of D per tile */
+    int32_t split;                  /* CTAs that share a tile along K, 1, 2, 4 or 8 */
     int32_t grid;                   /* CTAs launched */
     int32_t smem_bytes;             /* dynamic shared memory per CTA */
     int64_t workspace_bytes;        /* device bytes owned by the plan: with many tokens A in FP16, 2 M K */

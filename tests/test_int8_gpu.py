@@ -48,7 +48,7 @@ SHAPES = [(1, 1, 16), (1, 128, 128), (2, 3, 48), (16, 130, 1024), (17, 129, 1040
           (64, 128, 4096), (65, 127, 1008), (128, 256, 1152), (129, 300, 4112), (256, 384, 512), (257, 1000, 8208), (700, 513, 3088)]
 
 
-# num_sms 2: each CTA (or pair) takes many tiles, and the wide form is chosen wherever it can be
+# 0: all SMs, so that small ones are split along K.  num_sms 2: each CTA (or pair) takes many tiles, and the wide form is chosen wherever it can be
 @pytest.mark.parametrize("M,N,K", SHAPES)
 @pytest.mark.parametrize("num_sms", [0, 2])
 def test_sums_are_exact(M, N, K, num_sms):
@@ -81,7 +81,7 @@ def test_scales_bias_relu(M, N, K, out):
         _check(D, *int8.gemm(A, B, ra, cb, bias if use_bias else None, relu))
 
 
-GROUPS = [("one", 1, 5, 130, 272, [5]), ("empty first and last", 5, 40, 200, 1040, [0, 17, 0, 23, 0]),
+GROUPS = [("one", 1, 5, 130, 272, [5]), ("split over K", 3, 40, 384, 4112, [7, 0, 33]), ("empty first and last", 5, 40, 200, 1040, [0, 17, 0, 23, 0]),
           ("one row each", 60, 60, 96, 144, [1] * 60), ("uneven", 7, 333, 257, 2064, [1, 200, 0, 33, 64, 32, 3]),
           ("many", 300, 700, 130, 128, [(i * 7) % 5 for i in range(300)]), ("large", 3, 1500, 384, 1536, [129, 1000, 371]), ("large with rows to spare", 4, 1700, 300, 1040, [0, 600, 1, 500]),
           ("none", 4, 9, 64, 64, [0, 0, 0, 0])]

@@ -113,7 +113,7 @@ class tst_int8_options(ctypes.Structure):
 
 class tst_int8_plan_info(ctypes.Structure):
     _fields_ = [("M", _I64), ("N", _I64), ("K", _I64), ("groups", _I32), ("tile_rows", _I32), ("tile_cols", _I32),
-                ("grid", _I32), ("smem_bytes", _I32), ("workspace_bytes", _I64)]
+                ("split", _I32), ("grid", _I32), ("smem_bytes", _I32), ("workspace_bytes", _I64)]
 
 
 _SIGNATURES = {

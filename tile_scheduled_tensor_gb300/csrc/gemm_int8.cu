@@ -4,17 +4,20 @@
 
 #include "gemm_int8_wide.cuh"
 
+TstInt8Kernel tst_int8_split_kernel(int tokens, int out_type);   // gemm_int8_split.cu
+
 namespace {
 template <int NT>
 TstInt8Kernel kernel_of(int out_type) {
-  using Cfg = tst::Int8Cfg<NT>;
+  using Cfg = tst::Int8Cfg<NT, false>;
   const void* f = out_type == tst::OUT_BF16 ? reinterpret_cast<const void*>(&tst::gemm_int8_kernel<Cfg, tst::OUT_BF16>)
                                             : reinterpret_cast<const void*>(&tst::gemm_int8_kernel<Cfg, tst::OUT_F32>);
-  return {f, Cfg::SMEM_BYTES, tst::kInt8Threads, Cfg::PER_SM, 1};
+  return {f, Cfg::SMEM_BYTES, Cfg::THREADS, Cfg::PER_SM};
 }
 }  // namespace
 
-TstInt8Kernel tst_int8_kernel(int tokens, int out_type) {
+TstInt8Kernel tst_int8_kernel(int tokens, int out_type, bool split) {
+  if (split) return tst_int8_split_kernel(tokens, out_type);
   switch (tokens) {
     case 16: return kernel_of<16>(out_type);
     case 32: return kernel_of<32>(out_type);
@@ -25,7 +28,7 @@ TstInt8Kernel tst_int8_kernel(int tokens, int out_type) {
   using Cfg = tst::Int8WideCfg<kInt8WideTokens>;
   const void* f = out_type == tst::OUT_BF16 ? reinterpret_cast<const void*>(&tst::gemm_int8_wide_kernel<Cfg, tst::OUT_BF16>)
                                             : reinterpret_cast<const void*>(&tst::gemm_int8_wide_kernel<Cfg, tst::OUT_F32>);
-  return {f, Cfg::SMEM_BYTES, tst::kInt8WideThreads, 1, 2};
+  return {f, Cfg::SMEM_BYTES, tst::kInt8WideThreads, 1};
 }
 
 bool tst_int8_widen(const void* a, void* half, int64_t rows, int64_t K, const int32_t* group_rows, int32_t groups, int32_t num_sms,

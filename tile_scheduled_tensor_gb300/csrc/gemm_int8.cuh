@@ -18,26 +18,34 @@
 // A byte x becomes FP16 as 0x6400 | (x ^ 0x80), which is 1024 + (x + 128), less 1152: for four bytes
 // one exclusive or, two byte permutes, two packed subtractions.
 //
-// Roles, 384 threads, persistent over NT x 128 tiles of D, k-blocks of 128:
+// Roles, persistent over NT x 128 tiles of D, k-blocks of 128:
 //   warp 0      TMA producer: 128 x 128 bytes of B and NT x 128 of A per stage of the byte ring
 //   warp 1      MMA issuer: eight K = 16 MMAs per k-block and, every eighth k-block, a new accumulator
-//   warps 2-3   tokens: bytes of the ring -> FP16 in shared memory (the 128-byte swizzle that the
-//               MMA reads)
+//   warps 2-3   (up to 32 tokens; from 64 on warps 12-15) tokens: bytes of the ring -> FP16 in shared
+//               memory (the 128-byte swizzle that the MMA reads)
 //   warps 4-7   weights: a thread per channel, 128 bytes -> 64 columns of Tensor Memory
 //   warps 8-11  a thread per channel: accumulator -> integer sums; scales, bias, ReLU, cast, store
+// Where the tiles do not fill the SMs, a cluster of 2, 4 or 8 CTAs shares a tile, each taking a part of K.
+// Each CTA then finishes a slice of the tile's tokens: the others write their integer sums of it into its
+// shared memory.  Sums of integers are the same in any order, so a split changes no bit of D.
 // Every wait is bounded as in the other kernels.
 #pragma once
 #include "gemm_bs_tile.cuh"
 
 namespace tst {
 
-constexpr int kInt8Threads = 384;
 constexpr int kInt8Fold = 8;   // k-blocks of 128 per accumulator: 1024 products of at most 2^14
 
-template <int NT_>
+// SPLITS: a cluster of CTAs shares each tile along K
+template <int NT_, bool SPLITS_>
 struct Int8Cfg {
   static constexpr int NT = NT_;
+  static constexpr bool SPLITS = SPLITS_;
   static constexpr int PER_SM = NT <= 32 ? 2 : 1;          // CTAs per SM
+  static constexpr bool WIDER = NT >= 64;                  // a warpgroup of its own for the tokens
+  static constexpr int XWARPS = WIDER ? 4 : 2;
+  static constexpr int THREADS = WIDER ? 512 : 384;
+  static constexpr int RED_BYTES = SPLITS ? NT * 128 * 4 : 0;   // the cluster's sums of this CTA's slice
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
@@ -48,13 +56,14 @@ struct Int8Cfg {
   static constexpr int USED_COLS = A_COL + CV * 64;
   static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
   static constexpr int LIMIT = PER_SM == 2 ? (228 * 1024 - 2 * 1024) / 2 : kSmemLimit;
-  static constexpr int FIXED = 1024 + CV * XCV_BYTES + kWalkBytes + 512;
+  static constexpr int FIXED = 1024 + CV * XCV_BYTES + RED_BYTES + kWalkBytes + 512;
   static constexpr int RAW_STAGES = (LIMIT - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = RAW_STAGES > 8 ? 8 : RAW_STAGES;
   static constexpr int XCV_OFFSET = STAGES * STAGE_BYTES;
-  static constexpr int WALK_OFFSET = XCV_OFFSET + CV * XCV_BYTES;
+  static constexpr int RED_OFFSET = XCV_OFFSET + CV * XCV_BYTES;
+  static constexpr int WALK_OFFSET = RED_OFFSET + RED_BYTES;
   static constexpr int BAR_OFFSET = (WALK_OFFSET + kWalkBytes + 7) / 8 * 8;
-  static constexpr int BARS = 2 * STAGES + 2 * CV + 2 * BUFS + 1;
+  static constexpr int BARS = 2 * STAGES + 2 * CV + 2 * BUFS + 3;
   static constexpr int MISC_OFFSET = BAR_OFFSET + BARS * 8;
   static constexpr int SMEM_BYTES = 1024 + MISC_OFFSET + 16;
   static_assert(STAGE_BYTES % 1024 == 0 && XCV_BYTES % 1024 == 0, "swizzled tiles start on 1024 bytes");
@@ -73,13 +82,27 @@ __device__ __forceinline__ void int8_to_half(const uint4& v, uint32_t* h) {
   }
 }
 
+template <int OUT>
+struct OutOf { using T = float; };
+template <>
+struct OutOf<OUT_BF16> { using T = __nv_bfloat16; };
+
 // The shared addresses of the barriers: byte ring, converted k-blocks, accumulators, drain.
 template <class Cfg>
 struct Int8Bars {
-  uint32_t full, empty, cv_full, cv_empty, acc_full, acc_empty, drain;
+  uint32_t full, empty, cv_full, cv_empty, acc_full, acc_empty, drain, red_full, red_empty;
   __device__ __forceinline__ explicit Int8Bars(uint32_t base)
       : full(base), empty(full + 8 * Cfg::STAGES), cv_full(empty + 8 * Cfg::STAGES), cv_empty(cv_full + 8 * Cfg::CV),
-        acc_full(cv_empty + 8 * Cfg::CV), acc_empty(acc_full + 8 * Cfg::BUFS), drain(acc_empty + 8 * Cfg::BUFS) {}
+        acc_full(cv_empty + 8 * Cfg::CV), acc_empty(acc_full + 8 * Cfg::BUFS), drain(acc_empty + 8 * Cfg::BUFS),
+        red_full(drain + 8), red_empty(red_full + 8) {}
+};
+
+// this CTA's k-blocks: all, or its part of a split tile's
+struct KRange {
+  int32_t first, end;
+  __device__ __forceinline__ KRange(const KernelParams& p, const Ctx& c)
+      : first(p.sched.kt * static_cast<int32_t>(c.rank) / static_cast<int32_t>(c.csize)),
+        end(p.sched.kt * static_cast<int32_t>(c.rank + 1) / static_cast<int32_t>(c.csize)) {}
 };
 
 // position in a ring of N
@@ -94,14 +117,15 @@ struct RingAt {
 
 template <class Cfg>
 __device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& c, Walk walk, uint32_t smem, const Int8Bars<Cfg>& bar) {
+  const KRange k(p, c);
   RingAt<Cfg::STAGES> r;
   uint32_t issued = 0, issued_parity = 0;
   bool ok = true;
   Tile w;
   while (ok && walk.next(w)) {
-    if (w.clamped) record_status(p, ST_DEVICE_CHECK, ROLE_PRODUCER);
+    if (w.clamped && c.rank == 0) record_status(p, ST_DEVICE_CHECK, ROLE_PRODUCER);
     const int32_t b_row0 = w.group * p.sched.group_b_rows + w.n * 128;
-    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
+    for (int32_t kb = k.first; kb < k.end; ++kb) {
       if (!wait_phase<1>(p, c, bar.empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
       const uint32_t full = bar.full + 8 * r.at, dst = smem + r.at * Cfg::STAGE_BYTES;
       ptx::mbar_arrive_expect_tx(full, Cfg::STAGE_BYTES);
@@ -127,12 +151,13 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
                                          const Int8Bars<Cfg>& bar) {
   const uint32_t idesc = ptx::make_idesc(0u, 128, Cfg::NT);   // FP16 operands
   const uint64_t x_desc0 = ptx::sw128_kmajor_desc(xcv);
+  const KRange k(p, c);
   RingAt<Cfg::CV> r;
   RingAt<Cfg::BUFS> acc;
   bool ok = true;
   while (ok && walk.skip()) {
-    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
-      const int32_t in_fold = kb % kInt8Fold;
+    for (int32_t kb = k.first; kb < k.end; ++kb) {
+      const int32_t in_fold = (kb - k.first) % kInt8Fold;
       if (in_fold == 0 && !wait_phase<1>(p, c, bar.acc_empty + 8 * acc.at, acc.phase ^ 1u, ROLE_MMA)) { ok = false; break; }
       if (!wait_phase<1>(p, c, bar.cv_full + 8 * r.at, r.phase, ROLE_MMA)) { ok = false; break; }
       ptx::tc_fence_after();
@@ -144,7 +169,7 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
         ptx::mma_f16_ts(d, a + 8 * i, x + (i >> 2) * (Cfg::X_BYTES >> 4) + (i & 3) * 2, idesc, in_fold != 0 || i != 0);
       ptx::mma_commit(bar.cv_empty + 8 * r.at);
       r.next();
-      if (in_fold == kInt8Fold - 1 || kb == p.sched.kt - 1) {
+      if (in_fold == kInt8Fold - 1 || kb == k.end - 1) {
         ptx::mma_commit(bar.acc_full + 8 * acc.at);
         acc.next();
       }
@@ -161,35 +186,40 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
   }
 }
 
-// Warps 2-3: eight lanes take the same 16-byte piece of eight rows, which the swizzle puts in
-// eight different banks' worth of shared memory, reading and writing.
+// Eight lanes take the same 16-byte piece of eight rows, which the swizzle puts in eight different
+// banks' worth of shared memory, reading and writing; up to four pieces of a thread are in flight.
 template <class Cfg>
-__device__ __forceinline__ void int8_tokens(const KernelParams& p, const Ctx& c, Walk walk, uint8_t* smem, uint8_t* xcv,
+__device__ __forceinline__ void int8_tokens(const KernelParams& p, const Ctx& c, Walk walk, uint8_t* smem, uint8_t* xcv, int warp,
                                             const Int8Bars<Cfg>& bar) {
+  constexpr int PIECES = Cfg::NT * 8 / (32 * Cfg::XWARPS);   // of 16 bytes, per thread and k-block
+  constexpr int ROWS = Cfg::XWARPS * 4;                      // rows between a thread's pieces: 8 or 16
+  constexpr int FLIGHT = PIECES < 4 ? PIECES : 4;
   const int lane = threadIdx.x & 31;
-  const int j = (static_cast<int>(threadIdx.x >> 5) - 2) * 4 + (lane >> 3), sub = lane & 7;
+  const int at = warp * 4 + (lane >> 3), j = at & 7, sub = lane & 7;   // piece of the row, row of eight
+  const int row0 = (at >> 3) * 8 + sub;
+  const KRange k(p, c);
   RingAt<Cfg::STAGES> r;
   RingAt<Cfg::CV> t;
-  const uint8_t* const src0 = smem + Cfg::W_BYTES + sub * 128 + ((j ^ sub) << 4);
-  uint8_t* const dst0 = xcv + (j >> 2) * Cfg::X_BYTES + sub * 128;
+  const uint8_t* const src0 = smem + Cfg::W_BYTES + row0 * 128 + ((j ^ sub) << 4);
+  uint8_t* const dst0 = xcv + (j >> 2) * Cfg::X_BYTES + row0 * 128;
   const int c0 = (((2 * j) & 7) ^ sub) << 4, c1 = (((2 * j + 1) & 7) ^ sub) << 4;
   while (walk.skip()) {
-    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
-      if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE) ||
-          !wait_phase_warp(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE))
-        return;
+    for (int32_t kb = k.first; kb < k.end; ++kb) {
+      if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return;
       const uint8_t* const src = src0 + r.at * Cfg::STAGE_BYTES;
       uint8_t* const dst = dst0 + t.at * Cfg::XCV_BYTES;
 #pragma unroll
-      for (int i = 0; i < Cfg::NT / 8; i += 2) {
-        const uint4 v0 = *reinterpret_cast<const uint4*>(src + i * 1024), v1 = *reinterpret_cast<const uint4*>(src + i * 1024 + 1024);
-        uint32_t h[16];
-        int8_to_half(v0, h);
-        int8_to_half(v1, h + 8);
+      for (int i = 0; i < PIECES; i += FLIGHT) {
+        uint4 v[FLIGHT];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          *reinterpret_cast<uint4*>(dst + (i + q) * 1024 + c0) = make_uint4(h[8 * q], h[8 * q + 1], h[8 * q + 2], h[8 * q + 3]);
-          *reinterpret_cast<uint4*>(dst + (i + q) * 1024 + c1) = make_uint4(h[8 * q + 4], h[8 * q + 5], h[8 * q + 6], h[8 * q + 7]);
+        for (int q = 0; q < FLIGHT; ++q) v[q] = *reinterpret_cast<const uint4*>(src + (i + q) * ROWS * 128);
+        if (i == 0 && !wait_phase_warp(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE)) return;
+#pragma unroll
+        for (int q = 0; q < FLIGHT; ++q) {
+          uint32_t h[8];
+          int8_to_half(v[q], h);
+          *reinterpret_cast<uint4*>(dst + (i + q) * ROWS * 128 + c0) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + (i + q) * ROWS * 128 + c1) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       }
       ptx::fence_proxy_async_smem();   // the MMA reads these writes through the async proxy
@@ -211,10 +241,11 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
   const uint8_t* const src0 = smem + (quad * 32 + lane) * 128;
   const int sub = lane & 7;
   const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + Cfg::A_COL;
+  const KRange k(p, c);
   RingAt<Cfg::STAGES> r;
   RingAt<Cfg::CV> t;
   while (walk.skip()) {
-    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
+    for (int32_t kb = k.first; kb < k.end; ++kb) {
       if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return;
       const uint8_t* const src = src0 + r.at * Cfg::STAGE_BYTES;
       uint4 v[4];
@@ -245,35 +276,99 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
   }
 }
 
+// The row scales of N rows from row0 on, a row per lane: fetched by a whole warp while a tile is summed
+template <int N>
+struct RowScales {
+  static constexpr int V = (N + 31) / 32;
+  float v[V];
+  __device__ __forceinline__ void load(const KernelParams& p, int32_t row0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int32_t row = row0 + i * 32 + static_cast<int32_t>(threadIdx.x & 31);
+      v[i] = __ldg(p.ext.row_scale + (row < p.M ? row : p.M - 1));   // rows past the end are not stored
+    }
+  }
+  __device__ __forceinline__ float of(int i) const { return __shfl_sync(0xFFFFFFFFu, v[i >> 5], i & 31); }
+};
+
 // A thread's column of a tile: rows row0 .. row0 + N - 1 of D from their integer sums.  A warp stores 32
 // adjacent columns of a row at once.
 template <int N, int OUT>
-__device__ __forceinline__ void int8_store(const KernelParams& p, const Tile& w, int32_t row0, int32_t col, const int32_t (&sum)[N]) {
-  if (col >= p.N) return;
-  const int64_t channel = static_cast<int64_t>(w.group) * p.N + col;
+__device__ __forceinline__ void int8_store(const KernelParams& p, const Tile& w, int32_t row0, int32_t col, const int32_t (&sum)[N],
+                                           const RowScales<N>& scale) {
+  const bool on = col < p.N;
+  const int64_t channel = static_cast<int64_t>(w.group) * p.N + (on ? col : 0);
   const float cb = __ldg(p.ext.col_scale + channel);
   const float b = p.has_bias ? __ldg(p.bias + channel) : 0.0f;
+  using Out = typename OutOf<OUT>::T;
+  Out* dst = static_cast<Out*>(p.C) + static_cast<int64_t>(row0) * p.N + col;
+  const int32_t rows = on ? w.row_end - row0 : 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int32_t row = row0 + i;
-    if (row >= w.row_end) break;
-    float z = fmaf(__int2float_rn(sum[i]) * __ldg(p.ext.row_scale + row), cb, b);
+  for (int i = 0; i < N; ++i, dst += p.N) {
+    float z = fmaf(__int2float_rn(sum[i]) * scale.of(i), cb, b);
     if (p.relu) z = z < 0.0f ? 0.0f : z;   // a NaN stays
-    const int64_t at = static_cast<int64_t>(row) * p.N + col;
-    if (OUT == OUT_BF16) reinterpret_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(z);
-    else reinterpret_cast<float*>(p.C)[at] = z;
+    if (i < rows) *dst = static_cast<Out>(z);
   }
 }
 
+// A split tile: this CTA's sums go to the CTAs that finish their rows, and it finishes its own slice of
+// NT / csize rows from what the cluster has written here.  red: csize x slice x 128 sums.
 template <class Cfg, int OUT>
-__device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, const Int8Bars<Cfg>& bar) {
+__device__ __forceinline__ bool int8_exchange(const KernelParams& p, const Ctx& c, const Tile& w, int quad, int32_t (&sum)[Cfg::NT],
+                                              const RowScales<Cfg::NT>& scale, const Int8Bars<Cfg>& bar, uint32_t red, uint32_t phase) {
+  const int lane = threadIdx.x & 31, channel = quad * 32 + lane;
+  const int32_t size = static_cast<int32_t>(c.csize), rank = static_cast<int32_t>(c.rank);
+  const int32_t slice = Cfg::NT / size, rows = w.row_end - w.row0 < Cfg::NT ? w.row_end - w.row0 : Cfg::NT;
+  if (!wait_phase_warp(p, c, bar.red_empty, phase ^ 1u, ROLE_EPILOGUE)) return false;
+#pragma unroll
+  for (int i = 0; i < Cfg::NT; ++i)
+    if (i < rows) {
+      const int32_t to = i / slice;
+      ptx::st_cluster_u32(ptx::mapa(red + static_cast<uint32_t>(((rank * slice + i - to * slice) * 128 + channel) * 4), to),
+                          static_cast<uint32_t>(sum[i]));
+    }
+  __syncwarp();
+  if (lane < size) ptx::mbar_arrive_cluster(ptx::mapa(bar.red_full, lane));
+  if (!wait_phase_warp(p, c, bar.red_full, phase, ROLE_EPILOGUE)) return false;
+  ptx::mbar_try_wait_cluster(bar.red_full, phase);   // complete: the other CTAs' writes are visible
+  const int32_t col = w.n * 128 + channel;
+  const bool on = col < p.N;
+  const int64_t at = static_cast<int64_t>(w.group) * p.N + (on ? col : 0);
+  const float cb = __ldg(p.ext.col_scale + at);
+  const float b = p.has_bias ? __ldg(p.bias + at) : 0.0f;
+  using Out = typename OutOf<OUT>::T;
+  for (int32_t i = 0; i < slice; ++i) {
+    const int32_t row = rank * slice + i;
+    if (row >= rows) break;
+    int32_t s = 0;
+    for (int32_t q = 0; q < size; ++q) s += static_cast<int32_t>(ptx::ld_shared_u32(red + static_cast<uint32_t>(((q * slice + i) * 128 + channel) * 4)));
+    float ra = scale.v[0];
+#pragma unroll
+    for (int v = 1; v < RowScales<Cfg::NT>::V; ++v) ra = (row >> 5) == v ? scale.v[v] : ra;
+    ra = __shfl_sync(0xFFFFFFFFu, ra, row & 31);
+    float z = fmaf(__int2float_rn(s) * ra, cb, b);
+    if (p.relu) z = z < 0.0f ? 0.0f : z;   // a NaN stays
+    if (on) static_cast<Out*>(p.C)[static_cast<int64_t>(w.row0 + row) * p.N + col] = static_cast<Out>(z);
+  }
+  __syncwarp();
+  if (lane < size) ptx::mbar_arrive_cluster(ptx::mapa(bar.red_empty, lane));   // read: the next tile's may come
+  return true;
+}
+
+template <class Cfg, int OUT>
+__device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, uint32_t red,
+                                              const Int8Bars<Cfg>& bar) {
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+  const KRange k(p, c);
+  uint32_t red_phase = 0;
   RingAt<Cfg::BUFS> acc;
   Tile w;
   while (walk.next_warp(w)) {
+    RowScales<Cfg::NT> scale;
+    scale.load(p, w.row0);
     int32_t sum[Cfg::NT];
-    for (int32_t kb = 0; kb < p.sched.kt; kb += kInt8Fold) {
+    for (int32_t kb = k.first; kb < k.end; kb += kInt8Fold) {
       if (!wait_phase_warp(p, c, bar.acc_full + 8 * acc.at, acc.phase, ROLE_EPILOGUE)) return;
       ptx::tc_fence_after();
 #pragma unroll
@@ -283,7 +378,7 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int32_t x = __float2int_rn(v[i]);   // a whole number already
-          sum[q + i] = kb == 0 ? x : sum[q + i] + x;
+          sum[q + i] = kb == k.first ? x : sum[q + i] + x;
         }
       }
       ptx::tc_fence_before();
@@ -291,13 +386,25 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
       if (lane == 0) ptx::mbar_arrive(bar.acc_empty + 8 * acc.at);
       acc.next();
     }
-    int8_store<Cfg::NT, OUT>(p, w, w.row0, w.n * 128 + quad * 32 + lane, sum);
+    if constexpr (Cfg::SPLITS) {
+      if (c.csize > 1) {
+        if (!int8_exchange<Cfg, OUT>(p, c, w, quad, sum, scale, bar, red, red_phase)) return;
+        red_phase ^= 1u;
+        continue;
+      }
+    }
+    int8_store<Cfg::NT, OUT>(p, w, w.row0, w.n * 128 + quad * 32 + lane, sum, scale);
   }
 }
 
+// Registers per thread where four warpgroups split the block's: roles, weights, sums, tokens
+constexpr int kInt8SplitRegs[4] = {56, 104, 200, 104};
+static_assert(kInt8SplitRegs[0] + kInt8SplitRegs[1] + kInt8SplitRegs[2] + kInt8SplitRegs[3] <= 512, "the split fits the launch of 512 x 128");
+
 template <class Cfg, int OUT>
-__global__ void __launch_bounds__(kInt8Threads, Cfg::PER_SM) gemm_int8_kernel(const __grid_constant__ KernelParams p) {
+__global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_int8_kernel(const __grid_constant__ KernelParams p) {
   extern __shared__ uint8_t smem_raw[];
+  // the same offset in every CTA of a cluster: the window's start is
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = ptx::smem_addr(smem);
   const Int8Bars<Cfg> bar(base + Cfg::BAR_OFFSET);
@@ -307,19 +414,19 @@ __global__ void __launch_bounds__(kInt8Threads, Cfg::PER_SM) gemm_int8_kernel(co
   Ctx c;
   c.abort = &ctl->abort;
   c.abort_addr = ptx::smem_addr(&ctl->abort);
-  c.rank = 0;
+  c.csize = Cfg::SPLITS ? static_cast<uint32_t>(p.sk_slots) : 1u;
+  c.rank = c.csize > 1 ? ptx::cluster_ctarank() : 0u;
   c.rank_m = 0;
   c.rank_n = 0;
-  c.csize = 1;
-  c.unit = static_cast<int32_t>(blockIdx.x);
+  c.unit = static_cast<int32_t>(blockIdx.x / c.csize);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
       ptx::mbar_init(bar.full + 8 * s, 1);
-      ptx::mbar_init(bar.empty + 8 * s, 6);      // the converting warps
+      ptx::mbar_init(bar.empty + 8 * s, 4 + Cfg::XWARPS);   // the converting warps
     }
     for (int s = 0; s < Cfg::CV; ++s) {
-      ptx::mbar_init(bar.cv_full + 8 * s, 6);
+      ptx::mbar_init(bar.cv_full + 8 * s, 4 + Cfg::XWARPS);
       ptx::mbar_init(bar.cv_empty + 8 * s, 1);
     }
     for (int b = 0; b < Cfg::BUFS; ++b) {
@@ -327,6 +434,8 @@ __global__ void __launch_bounds__(kInt8Threads, Cfg::PER_SM) gemm_int8_kernel(co
       ptx::mbar_init(bar.acc_empty + 8 * b, 4);
     }
     ptx::mbar_init(bar.drain, 1);
+    ptx::mbar_init(bar.red_full, 4 * c.csize);    // the summing warps of the cluster
+    ptx::mbar_init(bar.red_empty, 4 * c.csize);
     ctl->abort = 0;
     ctl->ep_ok = 0;
     ptx::fence_mbar_init();
@@ -341,26 +450,36 @@ __global__ void __launch_bounds__(kInt8Threads, Cfg::PER_SM) gemm_int8_kernel(co
   if (warp == 2) fill_group_table(p.sched, table);
   ptx::tc_fence_before();
   __syncthreads();
+  if (c.csize > 1) ptx::cluster_sync();   // the other CTAs' barriers exist before anyone signals them
   ptx::tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
   const Walk walk(p.sched, table, c.unit);
 
-  if (warp == 0) {
-    if (ptx::elect_one()) int8_producer<Cfg>(p, c, walk, base, bar);
-    __syncwarp();
-  } else if (warp == 1) {
-    if (ptx::elect_one()) int8_mma<Cfg>(p, c, walk, tmem_base, base + Cfg::XCV_OFFSET, bar);
-    __syncwarp();
-  } else if (warp < 4) {
-    int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, bar);
+  if (warp < 4) {
+    if constexpr (Cfg::WIDER) ptx::setmaxnreg_dec<kInt8SplitRegs[0]>();
+    if (warp == 0) {
+      if (ptx::elect_one()) int8_producer<Cfg>(p, c, walk, base, bar);
+      __syncwarp();
+    } else if (warp == 1) {
+      if (ptx::elect_one()) int8_mma<Cfg>(p, c, walk, tmem_base, base + Cfg::XCV_OFFSET, bar);
+      __syncwarp();
+    } else if constexpr (!Cfg::WIDER) {
+      int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, warp - 2, bar);
+    }
   } else if (warp < 8) {
+    if constexpr (Cfg::WIDER) ptx::setmaxnreg_dec<kInt8SplitRegs[1]>();
     int8_weights<Cfg>(p, c, walk, tmem_base, smem, bar);
-  } else {
-    int8_epilogue<Cfg, OUT>(p, c, walk, tmem_base, bar);
+  } else if (warp < 12) {
+    if constexpr (Cfg::WIDER) ptx::setmaxnreg_inc<kInt8SplitRegs[2]>();
+    int8_epilogue<Cfg, OUT>(p, c, walk, tmem_base, base + Cfg::RED_OFFSET, bar);
+  } else if constexpr (Cfg::WIDER) {
+    ptx::setmaxnreg_dec<kInt8SplitRegs[3]>();
+    int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, warp - 12, bar);
   }
 
   ptx::tc_fence_before();
   __syncthreads();
+  if (c.csize > 1) ptx::cluster_sync();   // no CTA leaves while another may still write its shared memory
   if (warp == 1) {
     __syncwarp();
     ptx::tc_fence_after();

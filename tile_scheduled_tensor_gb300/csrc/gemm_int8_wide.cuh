@@ -217,6 +217,8 @@ __device__ __forceinline__ void int8_wide_epilogue(const KernelParams& p, const 
   RingAt<Cfg::BUFS> acc;
   Tile w;
   while (walk.next_warp(w)) {
+    RowScales<HALF> scale;
+    scale.load(p, w.row0 + half * HALF);
     int32_t sum[HALF];
     for (int32_t kb = 0; kb < p.sched.kt; kb += kInt8Fold) {
       if (!wait_phase_pair_warp(p, c, bar.acc_full + 8 * acc.at, acc.phase, ROLE_EPILOGUE)) return;
@@ -236,7 +238,8 @@ __device__ __forceinline__ void int8_wide_epilogue(const KernelParams& p, const 
       if (lane == 0) ptx::mbar_arrive_remote(acc_empty + 8 * acc.at);
       acc.next();
     }
-    int8_store<HALF, OUT>(p, w, w.row0 + half * HALF, w.n * 256 + static_cast<int32_t>(c.rank) * 128 + quad * 32 + lane, sum);
+    int8_store<HALF, OUT>(p, w, w.row0 + half * HALF, w.n * 256 + static_cast<int32_t>(c.rank) * 128 + quad * 32 + lane, sum,
+                          scale);
   }
 }
 

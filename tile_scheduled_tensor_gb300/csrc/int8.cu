@@ -16,6 +16,8 @@ struct tst_int8_plan {
   int32_t tokens = 0;          // rows of A per tile
   int32_t num_sms = 0, device = -1;
   TstInt8Kernel kernel{};
+  bool pairs = false;          // the wide form
+  int32_t split = 1;           // CTAs that share a tile along K
   tst::Sched sched{};
   unsigned long long* d_status = nullptr;   // 256 bytes, then the FP16 tokens of the wide form
   size_t dev_bytes = 0;
@@ -88,12 +90,19 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   }
   const int32_t tokens = tile_tokens(ceil_div(M, std::max<int64_t>(groups, 1)), M, N, p->num_sms);
   p->tokens = tokens;
-  p->kernel = tst_int8_kernel(tokens, opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32);
-  const bool pairs = p->kernel.ctas == 2;
+  p->pairs = tokens == kInt8WideTokens;
+  const bool pairs = p->pairs;
   const int32_t cols = pairs ? 256 : 128;
   const int64_t mt = ceil_div(M, tokens), nt = ceil_div(N, cols);
   const int64_t tiles = (mt + groups) * nt;   // grouped: at most, whatever the split
   if (tiles >= (int64_t(1) << 30)) { delete p; return TST_ERR_UNSUPPORTED; }
+  // a tile's K over as many CTAs as are left idle, each with two k-blocks or more
+  const int64_t kt = ceil_div(K, 128);
+  const int out_type = opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32;
+  const int64_t slots = int64_t(p->num_sms) * tst_int8_kernel(tokens, out_type, false).per_sm;
+  while (tokens <= kInt8SplitTokens && p->split < 8 && 2 * p->split * tiles <= slots && kt >= 4 * p->split) p->split *= 2;
+  p->kernel = tst_int8_kernel(tokens, out_type, p->split > 1);
+  const int32_t ctas = pairs ? 2 : p->split;   // of a cluster
   p->dev_bytes = 256 + (pairs ? 2 * static_cast<size_t>(M) * K : 0);
   if (!opts->host_only) {
     if (cudaFuncSetAttribute(p->kernel.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p->kernel.smem_bytes) != cudaSuccess) {
@@ -116,11 +125,11 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   tst::Sched& s = p->sched;
   s.mt = static_cast<int32_t>(mt);
   s.nt = static_cast<int32_t>(nt);
-  s.kt = static_cast<int32_t>(ceil_div(K, 128));
+  s.kt = static_cast<int32_t>(kt);
   s.map_kind = tst::MAP_GROUPED_M;
   s.group = 8;
   s.dp_tiles = static_cast<int32_t>(mt * nt);
-  s.grid = static_cast<int32_t>(std::min<int64_t>(int64_t(p->num_sms) * p->kernel.per_sm / p->kernel.ctas, tiles));
+  s.grid = static_cast<int32_t>(std::min<int64_t>(int64_t(p->num_sms) * p->kernel.per_sm / ctas, tiles));
   if (s.grid < 1) s.grid = 1;
   s.sk_groups = 1;
   s.rows = static_cast<int32_t>(M);
@@ -149,7 +158,8 @@ tst_status gemm_int8_plan_get_info(const tst_int8_plan* p, tst_int8_plan_info* i
   info->groups = p->sched.groups;
   info->tile_rows = p->tokens;
   info->tile_cols = p->sched.bn;
-  info->grid = p->sched.grid * p->kernel.ctas;
+  info->grid = p->sched.grid * (p->pairs ? 2 : p->split);
+  info->split = p->split;
   info->smem_bytes = p->kernel.smem_bytes;
   info->workspace_bytes = static_cast<int64_t>(p->dev_bytes);
   return TST_OK;
@@ -185,7 +195,8 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
   if (now != p->device) return TST_ERR_INVALID_ARG;
   tst::KernelParams kp = {};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool pairs = p->kernel.ctas == 2;
+  const bool pairs = p->pairs;
+  const int32_t ctas = pairs ? 2 : p->split;   // of a cluster
   void* const half = p->d_status + 32;
   if (!(pairs ? tst_encode_halves(&kp.tmap_a, half, p->M, p->K, p->tokens / 2) : tst_encode_bytes(&kp.tmap_a, A, p->M, p->K, p->tokens)) ||
       !tst_encode_bytes(&kp.tmap_b, B, std::max<int64_t>(p->sched.groups, 1) * p->N, p->K, 128))
@@ -203,23 +214,24 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
   kp.K = static_cast<int32_t>(p->K);
   kp.sched = p->sched;
   kp.sched.group_rows = group_rows;
+  kp.sk_slots = p->split;
   kp.timeout_ns = p->opts.timeout_ns > 0 ? static_cast<uint64_t>(p->opts.timeout_ns) : 10ull * 1000 * 1000 * 1000;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p->sched.grid * p->kernel.ctas), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p->sched.grid * ctas), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(p->kernel.threads), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(p->kernel.smem_bytes);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  if (pairs) {
-    // the pair as a cluster; it may start while the tokens are made FP16, and waits for them itself
+  if (ctas > 1) {
+    // a pair may start while the tokens are made FP16, and waits for them itself
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = pairs ? 2 : 1;
   }
   void* args[] = {&kp};
   if (pairs && !tst_int8_widen(A, half, p->M, p->K, group_rows, p->sched.groups, p->num_sms, s)) return TST_ERR_CUDA;
