@@ -21,9 +21,10 @@
 // Roles, persistent over NT x 128 tiles of D, k-blocks of 128:
 //   warp 0      TMA producer: 128 x 128 bytes of B and NT x 128 of A per stage of the byte ring
 //   warp 1      MMA issuer: eight K = 16 MMAs per k-block and, every eighth k-block, a new accumulator
-//   warps 2-3   (up to 32 tokens; from 64 on warps 12-15) tokens: bytes of the ring -> FP16 in shared
-//               memory (the 128-byte swizzle that the MMA reads)
-//   warps 4-7   weights: a thread per channel, 128 bytes -> 64 columns of Tensor Memory
+//   warps 2-3   (of 128 tokens: warps 12-15) tokens: bytes of the ring -> FP16 in shared memory (the
+//               128-byte swizzle that the MMA reads)
+//   warps 4-7   (of 128 tokens: and 16-19, in turn) weights: a thread per channel, 128 bytes -> 64
+//               columns of Tensor Memory
 //   warps 8-11  a thread per channel: accumulator -> integer sums; scales, bias, ReLU, cast, store
 // Where the tiles do not fill the SMs, a cluster of 2, 4 or 8 CTAs shares a tile, each taking a part of K.
 // Each CTA then finishes a slice of the tile's tokens: the others write their integer sums of it into its
@@ -41,15 +42,17 @@ template <int NT_, bool SPLITS_>
 struct Int8Cfg {
   static constexpr int NT = NT_;
   static constexpr bool SPLITS = SPLITS_;
-  static constexpr int PER_SM = NT <= 32 ? 2 : 1;          // CTAs per SM
-  static constexpr bool WIDER = NT >= 64;                  // a warpgroup of its own for the tokens
+  static constexpr int PER_SM = NT <= 32 || (NT == 64 && !SPLITS) ? 2 : 1;   // CTAs per SM
+  static constexpr bool WIDER = NT == 128;                 // warpgroups of their own for the tokens and for every second k-block's weights
   static constexpr int XWARPS = WIDER ? 4 : 2;
-  static constexpr int THREADS = WIDER ? 512 : 384;
+  static constexpr int WSETS = WIDER ? 2 : 1;
+  static constexpr int THREADS = WIDER ? 640 : 384;
+  static constexpr bool REGS = NT >= 64;                   // the warpgroups split the registers unevenly
   static constexpr int RED_BYTES = SPLITS ? NT * 128 * 4 : 0;   // the cluster's sums of this CTA's slice
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-  static constexpr int CV = 3;                             // converted k-blocks: TMEM columns and shared memory
+  static constexpr int CV = NT == 64 ? 2 : 3;              // converted k-blocks: TMEM columns and shared memory
   static constexpr int XCV_BYTES = 2 * X_BYTES;            // FP16 tokens of a k-block: two 64-element atoms
   static constexpr int BUFS = 2;                           // accumulators
   static constexpr int A_COL = BUFS * NT;                  // first TMEM column of the weights
@@ -187,13 +190,13 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
 }
 
 // Eight lanes take the same 16-byte piece of eight rows, which the swizzle puts in eight different
-// banks' worth of shared memory, reading and writing; up to four pieces of a thread are in flight.
+// banks' worth of shared memory, reading and writing; two or four pieces of a thread are in flight.
 template <class Cfg>
 __device__ __forceinline__ void int8_tokens(const KernelParams& p, const Ctx& c, Walk walk, uint8_t* smem, uint8_t* xcv, int warp,
                                             const Int8Bars<Cfg>& bar) {
   constexpr int PIECES = Cfg::NT * 8 / (32 * Cfg::XWARPS);   // of 16 bytes, per thread and k-block
   constexpr int ROWS = Cfg::XWARPS * 4;                      // rows between a thread's pieces: 8 or 16
-  constexpr int FLIGHT = PIECES < 4 ? PIECES : 4;
+  constexpr int FLIGHT = PIECES < 4 ? PIECES : Cfg::WIDER ? 4 : 2;
   const int lane = threadIdx.x & 31;
   const int at = warp * 4 + (lane >> 3), j = at & 7, sub = lane & 7;   // piece of the row, row of eight
   const int row0 = (at >> 3) * 8 + sub;
@@ -234,9 +237,10 @@ __device__ __forceinline__ void int8_tokens(const KernelParams& p, const Ctx& c,
   }
 }
 
+// set: of WSETS that take the k-blocks in turn
 template <class Cfg>
 __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, const uint8_t* smem,
-                                             const Int8Bars<Cfg>& bar) {
+                                             int set, const Int8Bars<Cfg>& bar) {
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const uint8_t* const src0 = smem + (quad * 32 + lane) * 128;
   const int sub = lane & 7;
@@ -244,8 +248,18 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
   const KRange k(p, c);
   RingAt<Cfg::STAGES> r;
   RingAt<Cfg::CV> t;
+  int turn = 0;
   while (walk.skip()) {
     for (int32_t kb = k.first; kb < k.end; ++kb) {
+      if constexpr (Cfg::WSETS > 1) {
+        const bool mine = turn == set;
+        turn ^= 1;
+        if (!mine) {
+          r.next();
+          t.next();
+          continue;
+        }
+      }
       if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return;
       const uint8_t* const src = src0 + r.at * Cfg::STAGE_BYTES;
       uint4 v[4];
@@ -291,8 +305,17 @@ struct RowScales {
   __device__ __forceinline__ float of(int i) const { return __shfl_sync(0xFFFFFFFFu, v[i >> 5], i & 31); }
 };
 
-// A thread's column of a tile: rows row0 .. row0 + N - 1 of D from their integer sums.  A warp stores 32
-// adjacent columns of a row at once.
+__device__ __forceinline__ float relu_nan(float z) {   // a NaN stays
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(z));
+  return r;
+}
+
+// A thread's column of a tile: rows row0 .. row0 + N - 1 of D from their integer sums.  A warp holds 32
+// adjacent columns.  FP32 rows are stored 128 bytes at once.  BF16, where rows and D are whole 4-byte
+// words: neighbouring lanes exchange a value, so that each has two adjacent columns of one of two rows,
+// and a store takes two rows of 64 bytes, half as many of them (8192 x 8192 x 1024, bound by this code:
+// 144 us with a store per row).
 template <int N, int OUT>
 __device__ __forceinline__ void int8_store(const KernelParams& p, const Tile& w, int32_t row0, int32_t col, const int32_t (&sum)[N],
                                            const RowScales<N>& scale) {
@@ -300,14 +323,34 @@ __device__ __forceinline__ void int8_store(const KernelParams& p, const Tile& w,
   const int64_t channel = static_cast<int64_t>(w.group) * p.N + (on ? col : 0);
   const float cb = __ldg(p.ext.col_scale + channel);
   const float b = p.has_bias ? __ldg(p.bias + channel) : 0.0f;
+  const int32_t rows = w.row_end - row0;
+  auto value = [&](int i) {
+    const float z = fmaf(__int2float_rn(sum[i]) * scale.of(i), cb, b);
+    return p.relu ? relu_nan(z) : z;
+  };
+  if constexpr (OUT == OUT_BF16) {
+    if (p.tma_store) {   // whole words
+      const bool odd = (threadIdx.x & 1) != 0;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + static_cast<int64_t>(row0 + (odd ? 1 : 0)) * p.N + (col & ~1);
+      const int64_t step = 2 * static_cast<int64_t>(p.N);
+      const int32_t mine = on ? rows - (odd ? 1 : 0) : 0;
+#pragma unroll
+      for (int i = 0; i < N; i += 2, dst += step) {
+        const float z0 = value(i), z1 = value(i + 1);
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? z0 : z1, 1);
+        const __nv_bfloat162 two = __floats2bfloat162_rn(odd ? other : z0, odd ? z1 : other);
+        if (i < mine) *reinterpret_cast<__nv_bfloat162*>(dst) = two;
+      }
+      return;
+    }
+  }
   using Out = typename OutOf<OUT>::T;
   Out* dst = static_cast<Out*>(p.C) + static_cast<int64_t>(row0) * p.N + col;
-  const int32_t rows = on ? w.row_end - row0 : 0;
+  const int32_t mine = on ? rows : 0;
 #pragma unroll
   for (int i = 0; i < N; ++i, dst += p.N) {
-    float z = fmaf(__int2float_rn(sum[i]) * scale.of(i), cb, b);
-    if (p.relu) z = z < 0.0f ? 0.0f : z;   // a NaN stays
-    if (i < rows) *dst = static_cast<Out>(z);
+    const float z = value(i);
+    if (i < mine) *dst = static_cast<Out>(z);
   }
 }
 
@@ -347,7 +390,7 @@ __device__ __forceinline__ bool int8_exchange(const KernelParams& p, const Ctx& 
     for (int v = 1; v < RowScales<Cfg::NT>::V; ++v) ra = (row >> 5) == v ? scale.v[v] : ra;
     ra = __shfl_sync(0xFFFFFFFFu, ra, row & 31);
     float z = fmaf(__int2float_rn(s) * ra, cb, b);
-    if (p.relu) z = z < 0.0f ? 0.0f : z;   // a NaN stays
+    if (p.relu) z = relu_nan(z);
     if (on) static_cast<Out*>(p.C)[static_cast<int64_t>(w.row0 + row) * p.N + col] = static_cast<Out>(z);
   }
   __syncwarp();
@@ -397,9 +440,14 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
   }
 }
 
-// Registers per thread where four warpgroups split the block's: roles, weights, sums, tokens
-constexpr int kInt8SplitRegs[4] = {56, 104, 200, 104};
-static_assert(kInt8SplitRegs[0] + kInt8SplitRegs[1] + kInt8SplitRegs[2] + kInt8SplitRegs[3] <= 512, "the split fits the launch of 512 x 128");
+// Registers per thread of the warpgroups where they differ: roles, weights, sums, tokens, weights.  64 tokens:
+// two CTAs of 384 x 80 (split tiles: one); 128: one of 640 x 96.
+template <int NT>
+struct Int8Regs {
+  static constexpr int ROLE = 56, WEIGHT = 72, SUM = NT == 64 ? 112 : 184, TOKEN = 72;
+  static_assert(NT != 64 || ROLE + WEIGHT + SUM <= 3 * 80, "the split fits the launch");
+  static_assert(NT != 128 || ROLE + 2 * WEIGHT + SUM + TOKEN <= 5 * 96, "the split fits the launch");
+};
 
 template <class Cfg, int OUT>
 __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_int8_kernel(const __grid_constant__ KernelParams p) {
@@ -455,8 +503,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_int8_kernel(co
   const uint32_t tmem_base = ctl->tmem_base;
   const Walk walk(p.sched, table, c.unit);
 
+  using Regs = Int8Regs<Cfg::NT>;
   if (warp < 4) {
-    if constexpr (Cfg::WIDER) ptx::setmaxnreg_dec<kInt8SplitRegs[0]>();
+    if constexpr (Cfg::REGS) ptx::setmaxnreg_dec<Regs::ROLE>();
     if (warp == 0) {
       if (ptx::elect_one()) int8_producer<Cfg>(p, c, walk, base, bar);
       __syncwarp();
@@ -467,14 +516,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_int8_kernel(co
       int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, warp - 2, bar);
     }
   } else if (warp < 8) {
-    if constexpr (Cfg::WIDER) ptx::setmaxnreg_dec<kInt8SplitRegs[1]>();
-    int8_weights<Cfg>(p, c, walk, tmem_base, smem, bar);
+    if constexpr (Cfg::REGS) ptx::setmaxnreg_dec<Regs::WEIGHT>();
+    int8_weights<Cfg>(p, c, walk, tmem_base, smem, 0, bar);
   } else if (warp < 12) {
-    if constexpr (Cfg::WIDER) ptx::setmaxnreg_inc<kInt8SplitRegs[2]>();
+    if constexpr (Cfg::REGS) ptx::setmaxnreg_inc<Regs::SUM>();
     int8_epilogue<Cfg, OUT>(p, c, walk, tmem_base, base + Cfg::RED_OFFSET, bar);
   } else if constexpr (Cfg::WIDER) {
-    ptx::setmaxnreg_dec<kInt8SplitRegs[3]>();
-    int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, warp - 12, bar);
+    if (warp < 16) {
+      ptx::setmaxnreg_dec<Regs::TOKEN>();
+      int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, warp - 12, bar);
+    } else {
+      ptx::setmaxnreg_dec<Regs::WEIGHT>();
+      int8_weights<Cfg>(p, c, walk, tmem_base, smem, 1, bar);
+    }
   }
 
   ptx::tc_fence_before();

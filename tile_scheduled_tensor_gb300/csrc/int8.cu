@@ -62,6 +62,11 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   if (opts->groups < 0 || opts->num_sms < 0 || opts->timeout_ns < 0) return TST_ERR_INVALID_ARG;
   if (opts->out_dtype != TST_OUT_F32 && opts->out_dtype != TST_OUT_BF16) return TST_ERR_INVALID_ARG;
   if (opts->host_only && opts->num_sms == 0) return TST_ERR_INVALID_ARG;
+  const int32_t tr = opts->tile_rows, sp = opts->split;
+  if (tr < 0 || sp < 0) return TST_ERR_INVALID_ARG;
+  if ((tr != 0 && tr != 16 && tr != 32 && tr != 64 && tr != 128 && tr != kInt8WideTokens) || (sp != 0 && sp != 1 && sp != 2 && sp != 4 && sp != 8) ||
+      (sp > 1 && (tr == 0 || tr > kInt8SplitTokens)) || (tr == kInt8WideTokens && opts->num_sms == 1))
+    return TST_ERR_UNSUPPORTED;
   if (K % 16 != 0) return TST_ERR_ALIGNMENT;   // a row of K bytes is a row of the tensor map
   const int64_t groups = opts->groups;
   if (M > kMaxRows || N > kMaxRows || std::max<int64_t>(groups, 1) * N > kMaxRows || K > kMaxK || groups > kBsWalkGroups)
@@ -88,7 +93,7 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
     p->device = dev;
     p->num_sms = opts->num_sms > 0 ? std::min(opts->num_sms, sms) : sms;
   }
-  const int32_t tokens = tile_tokens(ceil_div(M, std::max<int64_t>(groups, 1)), M, N, p->num_sms);
+  const int32_t tokens = opts->tile_rows > 0 ? opts->tile_rows : tile_tokens(ceil_div(M, std::max<int64_t>(groups, 1)), M, N, p->num_sms);
   p->tokens = tokens;
   p->pairs = tokens == kInt8WideTokens;
   const bool pairs = p->pairs;
@@ -99,8 +104,12 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   // a tile's K over as many CTAs as are left idle, each with two k-blocks or more
   const int64_t kt = ceil_div(K, 128);
   const int out_type = opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32;
-  const int64_t slots = int64_t(p->num_sms) * tst_int8_kernel(tokens, out_type, false).per_sm;
-  while (tokens <= kInt8SplitTokens && p->split < 8 && 2 * p->split * tiles <= slots && kt >= 4 * p->split) p->split *= 2;
+  const int64_t slots = int64_t(p->num_sms) * tst_int8_kernel(tokens, out_type, tokens <= kInt8SplitTokens).per_sm;   // of split tiles, where they can be
+  if (opts->split > 0) {
+    p->split = static_cast<int32_t>(std::min<int64_t>(opts->split, kt));
+    while (p->split & (p->split - 1)) --p->split;
+  }
+  while (opts->split == 0 && tokens <= kInt8SplitTokens && p->split < 8 && 2 * p->split * tiles <= slots && kt >= 4 * p->split) p->split *= 2;
   p->kernel = tst_int8_kernel(tokens, out_type, p->split > 1);
   const int32_t ctas = pairs ? 2 : p->split;   // of a cluster
   p->dev_bytes = 256 + (pairs ? 2 * static_cast<size_t>(M) * K : 0);
@@ -215,6 +224,7 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
   kp.sched = p->sched;
   kp.sched.group_rows = group_rows;
   kp.sk_slots = p->split;
+  kp.tma_store = aligned(D, 4) && p->N % 2 == 0;   // BF16 rows of whole words
   kp.timeout_ns = p->opts.timeout_ns > 0 ? static_cast<uint64_t>(p->opts.timeout_ns) : 10ull * 1000 * 1000 * 1000;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p->sched.grid * ctas), 1, 1);
