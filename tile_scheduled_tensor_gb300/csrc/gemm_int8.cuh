@@ -18,13 +18,15 @@
 // A byte x becomes FP16 as 0x6400 | (x ^ 0x80), which is 1024 + (x + 128), less 1152: for four bytes
 // one exclusive or, two byte permutes, two packed subtractions.
 //
-// Roles, persistent over NT x 128 tiles of D, k-blocks of 128:
-//   warp 0      TMA producer: 128 x 128 bytes of B and NT x 128 of A per stage of the byte ring
+// Roles, 384 threads (of 128 tokens: 512), persistent over NT x 128 tiles of D, k-blocks of 128:
+//   warp 0      TMA producer: 128 x 128 bytes of B per stage of the byte ring, and up to 32 tokens' bytes
 //   warp 1      MMA issuer: eight K = 16 MMAs per k-block and, every eighth k-block, a new accumulator
-//   warps 2-3   (of 128 tokens: warps 12-15) tokens: bytes of the ring -> FP16 in shared memory (the
-//               128-byte swizzle that the MMA reads)
-//   warps 4-7   (of 128 tokens: and 16-19, in turn) weights: a thread per channel, 128 bytes -> 64
-//               columns of Tensor Memory
+//   warps 2-3   tokens.  Up to 32: bytes of the ring -> FP16 in shared memory (the 128-byte swizzle that
+//               the MMA reads).  From 64 on the conversion would cost more than the weights' (two
+//               warps took 1400 cycles per k-block of 64 tokens, its MMAs take 256): a kernel before
+//               makes A FP16, as for the wide form, and warp 2 brings that by TMA
+//   warps 4-7   weights: a thread per channel, 128 bytes -> 64 columns of Tensor Memory (of 128 tokens
+//               also the last four warps, every second k-block)
 //   warps 8-11  a thread per channel: accumulator -> integer sums; scales, bias, ReLU, cast, store
 // Where the tiles do not fill the SMs, a cluster of 2, 4 or 8 CTAs shares a tile, each taking a part of K.
 // Each CTA then finishes a slice of the tile's tokens: the others write their integer sums of it into its
@@ -37,40 +39,43 @@ namespace tst {
 
 constexpr int kInt8Fold = 8;   // k-blocks of 128 per accumulator: 1024 products of at most 2^14
 
-// SPLITS: a cluster of CTAs shares each tile along K
+// SPLITS: a cluster of CTAs shares each tile along K.  HALVES: A has been made FP16 before (int8_widen_kernel).
 template <int NT_, bool SPLITS_>
 struct Int8Cfg {
   static constexpr int NT = NT_;
   static constexpr bool SPLITS = SPLITS_;
+  static constexpr bool HALVES = NT >= 64;
   static constexpr int PER_SM = NT <= 32 || (NT == 64 && !SPLITS) ? 2 : 1;   // CTAs per SM
-  static constexpr bool WIDER = NT == 128;                 // warpgroups of their own for the tokens and for every second k-block's weights
-  static constexpr int XWARPS = WIDER ? 4 : 2;
-  static constexpr int WSETS = WIDER ? 2 : 1;
-  static constexpr int THREADS = WIDER ? 640 : 384;
-  static constexpr bool REGS = NT >= 64;                   // the warpgroups split the registers unevenly
-  static constexpr int RED_BYTES = SPLITS ? NT * 128 * 4 : 0;   // the cluster's sums of this CTA's slice
+  static constexpr int WSETS = NT == 128 ? 2 : 1;          // warpgroups that convert weights, k-blocks in turn
+  static constexpr int THREADS = 256 + 128 * WSETS;
   static constexpr int W_BYTES = 128 * 128;
-  static constexpr int X_BYTES = NT * 128;
-  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-  static constexpr int CV = NT == 64 ? 2 : 3;              // converted k-blocks: TMEM columns and shared memory
+  static constexpr int X_BYTES = NT * 128;                 // a 128-byte column of the tokens' tile
   static constexpr int XCV_BYTES = 2 * X_BYTES;            // FP16 tokens of a k-block: two 64-element atoms
+  static constexpr int STAGE_BYTES = HALVES ? W_BYTES : W_BYTES + X_BYTES;   // of the byte ring
+  static constexpr int CV = NT == 64 ? 2 : 3;              // converted k-blocks of weights: 64 TMEM columns each
+  static constexpr int XS = !HALVES ? CV : NT == 64 && !SPLITS ? 2 : 3;      // FP16 k-blocks of tokens
   static constexpr int BUFS = 2;                           // accumulators
   static constexpr int A_COL = BUFS * NT;                  // first TMEM column of the weights
   static constexpr int USED_COLS = A_COL + CV * 64;
   static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
+  static constexpr int RED_BYTES = SPLITS ? NT * 128 * 4 : 0;   // the cluster's sums of this CTA's slice
   static constexpr int LIMIT = PER_SM == 2 ? (228 * 1024 - 2 * 1024) / 2 : kSmemLimit;
-  static constexpr int FIXED = 1024 + CV * XCV_BYTES + RED_BYTES + kWalkBytes + 512;
+  static constexpr int FIXED = 1024 + XS * XCV_BYTES + RED_BYTES + kWalkBytes + 512;
   static constexpr int RAW_STAGES = (LIMIT - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = RAW_STAGES > 8 ? 8 : RAW_STAGES;
   static constexpr int XCV_OFFSET = STAGES * STAGE_BYTES;
-  static constexpr int RED_OFFSET = XCV_OFFSET + CV * XCV_BYTES;
+  static constexpr int RED_OFFSET = XCV_OFFSET + XS * XCV_BYTES;
   static constexpr int WALK_OFFSET = RED_OFFSET + RED_BYTES;
   static constexpr int BAR_OFFSET = (WALK_OFFSET + kWalkBytes + 7) / 8 * 8;
-  static constexpr int BARS = 2 * STAGES + 2 * CV + 2 * BUFS + 3;
+  static constexpr int BARS = 2 * STAGES + 2 * CV + 2 * XS + 2 * BUFS + 3;
   static constexpr int MISC_OFFSET = BAR_OFFSET + BARS * 8;
   static constexpr int SMEM_BYTES = 1024 + MISC_OFFSET + 16;
   static_assert(STAGE_BYTES % 1024 == 0 && XCV_BYTES % 1024 == 0, "swizzled tiles start on 1024 bytes");
   static_assert(SMEM_BYTES <= LIMIT && STAGES >= 2 && PER_SM * TMEM_COLS <= 512 && USED_COLS <= TMEM_COLS, "fits an SM");
+  // registers per thread of the warpgroups: roles (and 2 warps of tokens), weights, sums
+  static constexpr int ROLE_REGS = NT <= 32 ? 72 : 56, WEIGHT_REGS = 88, SUM_REGS = NT <= 32 ? 80 : NT == 64 ? 96 : 184;
+  static constexpr int LAUNCH_REGS = PER_SM == 2 ? 80 : NT == 128 ? 128 : 80;
+  static_assert(ROLE_REGS + WSETS * WEIGHT_REGS + SUM_REGS <= (2 + WSETS) * LAUNCH_REGS, "the split fits the launch");
 };
 
 // 16 int8 values -> 8 pairs of FP16, in their order
@@ -93,10 +98,10 @@ struct OutOf<OUT_BF16> { using T = __nv_bfloat16; };
 // The shared addresses of the barriers: byte ring, converted k-blocks, accumulators, drain.
 template <class Cfg>
 struct Int8Bars {
-  uint32_t full, empty, cv_full, cv_empty, acc_full, acc_empty, drain, red_full, red_empty;
+  uint32_t full, empty, cv_full, cv_empty, x_full, x_empty, acc_full, acc_empty, drain, red_full, red_empty;
   __device__ __forceinline__ explicit Int8Bars(uint32_t base)
       : full(base), empty(full + 8 * Cfg::STAGES), cv_full(empty + 8 * Cfg::STAGES), cv_empty(cv_full + 8 * Cfg::CV),
-        acc_full(cv_empty + 8 * Cfg::CV), acc_empty(acc_full + 8 * Cfg::BUFS), drain(acc_empty + 8 * Cfg::BUFS),
+        x_full(cv_empty + 8 * Cfg::CV), x_empty(x_full + 8 * Cfg::XS), acc_full(x_empty + 8 * Cfg::XS), acc_empty(acc_full + 8 * Cfg::BUFS), drain(acc_empty + 8 * Cfg::BUFS),
         red_full(drain + 8), red_empty(red_full + 8) {}
 };
 
@@ -118,6 +123,17 @@ struct RingAt {
   }
 };
 
+// bounded wait until the copies of an aborting producer have landed
+template <int N>
+__device__ __forceinline__ void int8_land(const KernelParams& p, uint32_t full, uint32_t issued, uint32_t parity) {
+  const uint64_t t0 = ptx::globaltimer();
+  for (int s = 0; s < N; ++s) {
+    if (!(issued & (1u << s))) continue;
+    while (!ptx::mbar_try_wait(full + 8 * s, (parity >> s) & 1u))
+      if (ptx::globaltimer() - t0 > p.timeout_ns) return;
+  }
+}
+
 template <class Cfg>
 __device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& c, Walk walk, uint32_t smem, const Int8Bars<Cfg>& bar) {
   const KRange k(p, c);
@@ -133,20 +149,37 @@ __device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& 
       const uint32_t full = bar.full + 8 * r.at, dst = smem + r.at * Cfg::STAGE_BYTES;
       ptx::mbar_arrive_expect_tx(full, Cfg::STAGE_BYTES);
       ptx::tma_load_2d(dst, &p.tmap_b, full, kb * 128, b_row0);
-      ptx::tma_load_2d(dst + Cfg::W_BYTES, &p.tmap_a, full, kb * 128, w.row0);
+      if constexpr (!Cfg::HALVES) ptx::tma_load_2d(dst + Cfg::W_BYTES, &p.tmap_a, full, kb * 128, w.row0);
       issued |= 1u << r.at;
       issued_parity = (issued_parity & ~(1u << r.at)) | (r.phase << r.at);
       r.next();
     }
   }
-  if (!ok) {   // aborting: wait (bounded) until the loads already issued have landed
-    const uint64_t t0 = ptx::globaltimer();
-    for (int s = 0; s < Cfg::STAGES; ++s) {
-      if (!(issued & (1u << s))) continue;
-      while (!ptx::mbar_try_wait(bar.full + 8 * s, (issued_parity >> s) & 1u))
-        if (ptx::globaltimer() - t0 > p.timeout_ns) break;
+  if (!ok) int8_land<Cfg::STAGES>(p, bar.full, issued, issued_parity);
+}
+
+// FP16 tokens: NT rows of two 64-element atoms per k-block.
+template <class Cfg>
+__device__ __forceinline__ void int8_token_loads(const KernelParams& p, const Ctx& c, Walk walk, uint32_t xs, const Int8Bars<Cfg>& bar) {
+  const KRange k(p, c);
+  RingAt<Cfg::XS> r;
+  uint32_t issued = 0, issued_parity = 0;
+  bool ok = true;
+  Tile w;
+  ptx::griddep_wait();   // they are the kernel's before
+  while (ok && walk.next(w)) {
+    for (int32_t kb = k.first; kb < k.end; ++kb) {
+      if (!wait_phase<1>(p, c, bar.x_empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
+      const uint32_t full = bar.x_full + 8 * r.at, dst = xs + r.at * Cfg::XCV_BYTES;
+      ptx::mbar_arrive_expect_tx(full, Cfg::XCV_BYTES);
+      ptx::tma_load_2d(dst, &p.tmap_a, full, kb * 128, w.row0);
+      ptx::tma_load_2d(dst + Cfg::X_BYTES, &p.tmap_a, full, kb * 128 + 64, w.row0);
+      issued |= 1u << r.at;
+      issued_parity = (issued_parity & ~(1u << r.at)) | (r.phase << r.at);
+      r.next();
     }
   }
+  if (!ok) int8_land<Cfg::XS>(p, bar.x_full, issued, issued_parity);
 }
 
 template <class Cfg>
@@ -156,22 +189,27 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
   const uint64_t x_desc0 = ptx::sw128_kmajor_desc(xcv);
   const KRange k(p, c);
   RingAt<Cfg::CV> r;
+  RingAt<Cfg::XS> xr;   // of tokens: by TMA, or beside the weights of the same k-block
   RingAt<Cfg::BUFS> acc;
   bool ok = true;
   while (ok && walk.skip()) {
     for (int32_t kb = k.first; kb < k.end; ++kb) {
       const int32_t in_fold = (kb - k.first) % kInt8Fold;
       if (in_fold == 0 && !wait_phase<1>(p, c, bar.acc_empty + 8 * acc.at, acc.phase ^ 1u, ROLE_MMA)) { ok = false; break; }
+      if constexpr (Cfg::HALVES)
+        if (!wait_phase<1>(p, c, bar.x_full + 8 * xr.at, xr.phase, ROLE_MMA)) { ok = false; break; }
       if (!wait_phase<1>(p, c, bar.cv_full + 8 * r.at, r.phase, ROLE_MMA)) { ok = false; break; }
       ptx::tc_fence_after();
       const uint32_t d = tmem_base + static_cast<uint32_t>(acc.at * Cfg::NT);
       const uint32_t a = tmem_base + static_cast<uint32_t>(Cfg::A_COL + r.at * 64);
-      const uint64_t x = x_desc0 + static_cast<uint64_t>(r.at * (Cfg::XCV_BYTES >> 4));
+      const uint64_t x = x_desc0 + static_cast<uint64_t>(xr.at * (Cfg::XCV_BYTES >> 4));
 #pragma unroll
       for (int i = 0; i < 8; ++i)   // 16 of K: 8 TMEM columns, 32 bytes of an atom
         ptx::mma_f16_ts(d, a + 8 * i, x + (i >> 2) * (Cfg::X_BYTES >> 4) + (i & 3) * 2, idesc, in_fold != 0 || i != 0);
       ptx::mma_commit(bar.cv_empty + 8 * r.at);
+      if constexpr (Cfg::HALVES) ptx::mma_commit(bar.x_empty + 8 * xr.at);
       r.next();
+      xr.next();
       if (in_fold == kInt8Fold - 1 || kb == k.end - 1) {
         ptx::mma_commit(bar.acc_full + 8 * acc.at);
         acc.next();
@@ -190,21 +228,20 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
 }
 
 // Eight lanes take the same 16-byte piece of eight rows, which the swizzle puts in eight different
-// banks' worth of shared memory, reading and writing; two or four pieces of a thread are in flight.
+// banks' worth of shared memory, reading and writing.
 template <class Cfg>
 __device__ __forceinline__ void int8_tokens(const KernelParams& p, const Ctx& c, Walk walk, uint8_t* smem, uint8_t* xcv, int warp,
                                             const Int8Bars<Cfg>& bar) {
-  constexpr int PIECES = Cfg::NT * 8 / (32 * Cfg::XWARPS);   // of 16 bytes, per thread and k-block
-  constexpr int ROWS = Cfg::XWARPS * 4;                      // rows between a thread's pieces: 8 or 16
-  constexpr int FLIGHT = PIECES < 4 ? PIECES : Cfg::WIDER ? 4 : 2;
+  constexpr int PIECES = Cfg::NT / 8;   // of 16 bytes, per thread of two warps and k-block: 2 or 4
+  constexpr int ROWS = 8;               // rows between a thread's pieces
+  constexpr int FLIGHT = PIECES;
   const int lane = threadIdx.x & 31;
-  const int at = warp * 4 + (lane >> 3), j = at & 7, sub = lane & 7;   // piece of the row, row of eight
-  const int row0 = (at >> 3) * 8 + sub;
+  const int j = warp * 4 + (lane >> 3), sub = lane & 7;   // piece of the row, row of eight
   const KRange k(p, c);
   RingAt<Cfg::STAGES> r;
   RingAt<Cfg::CV> t;
-  const uint8_t* const src0 = smem + Cfg::W_BYTES + row0 * 128 + ((j ^ sub) << 4);
-  uint8_t* const dst0 = xcv + (j >> 2) * Cfg::X_BYTES + row0 * 128;
+  const uint8_t* const src0 = smem + Cfg::W_BYTES + sub * 128 + ((j ^ sub) << 4);
+  uint8_t* const dst0 = xcv + (j >> 2) * Cfg::X_BYTES + sub * 128;
   const int c0 = (((2 * j) & 7) ^ sub) << 4, c1 = (((2 * j + 1) & 7) ^ sub) << 4;
   while (walk.skip()) {
     for (int32_t kb = k.first; kb < k.end; ++kb) {
@@ -237,7 +274,8 @@ __device__ __forceinline__ void int8_tokens(const KernelParams& p, const Ctx& c,
   }
 }
 
-// set: of WSETS that take the k-blocks in turn
+// set: of WSETS that take the k-blocks in turn.  The next k-block's bytes are read while this one's stores
+// into Tensor Memory complete.
 template <class Cfg>
 __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, const uint8_t* smem,
                                              int set, const Int8Bars<Cfg>& bar) {
@@ -246,47 +284,41 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
   const int sub = lane & 7;
   const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + Cfg::A_COL;
   const KRange k(p, c);
+  int64_t blocks = 0;   // k-blocks of this CTA
+  while (walk.skip()) blocks += k.end - k.first;
   RingAt<Cfg::STAGES> r;
   RingAt<Cfg::CV> t;
-  int turn = 0;
-  while (walk.skip()) {
-    for (int32_t kb = k.first; kb < k.end; ++kb) {
-      if constexpr (Cfg::WSETS > 1) {
-        const bool mine = turn == set;
-        turn ^= 1;
-        if (!mine) {
-          r.next();
-          t.next();
-          continue;
-        }
-      }
-      if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return;
-      const uint8_t* const src = src0 + r.at * Cfg::STAGE_BYTES;
-      uint4 v[4];
+  uint4 v[8];
+  auto read = [&] {   // a k-block's bytes, which frees its stage
+    if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return false;
+    const uint8_t* const src = src0 + r.at * Cfg::STAGE_BYTES;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + ((q ^ sub) << 4));
-      if (!wait_phase_warp(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE)) return;
-      ptx::tc_fence_after();
+    for (int q = 0; q < 8; ++q) v[q] = *reinterpret_cast<const uint4*>(src + ((q ^ sub) << 4));
+    return true;
+  };
+  for (int i = 0; i < set; ++i) { r.next(); t.next(); }
+  if (set < blocks && !read()) return;
+  for (int64_t i = set; i < blocks; i += Cfg::WSETS) {
+    if (!wait_phase_warp(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE)) return;
+    ptx::tc_fence_after();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {   // 64 of K: 32 columns
-        uint32_t h[32];
+    for (int half = 0; half < 2; ++half) {   // 64 of K: 32 columns
+      uint32_t h[32];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) int8_to_half(v[q], h + 8 * q);
-        if (half == 0) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(src + (((4 + q) ^ sub) << 4));
-        }
-        ptx::tmem_store_32cols(taddr0 + static_cast<uint32_t>(t.at * 64 + half * 32), h);
-      }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar.empty + 8 * r.at);   // the bytes are in registers
-      ptx::tmem_wait_stores();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar.cv_full + 8 * t.at);
-      r.next();
-      t.next();
+      for (int q = 0; q < 4; ++q) int8_to_half(v[4 * half + q], h + 8 * q);
+      ptx::tmem_store_32cols(taddr0 + static_cast<uint32_t>(t.at * 64 + half * 32), h);
     }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar.empty + 8 * r.at);   // every lane has its bytes
+#pragma unroll
+    for (int s = 0; s < Cfg::WSETS; ++s) r.next();
+    if (i + Cfg::WSETS < blocks && !read()) return;
+    ptx::tmem_wait_stores();
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar.cv_full + 8 * t.at);
+#pragma unroll
+    for (int s = 0; s < Cfg::WSETS; ++s) t.next();
   }
 }
 
@@ -440,17 +472,8 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
   }
 }
 
-// Registers per thread of the warpgroups where they differ: roles, weights, sums, tokens, weights.  64 tokens:
-// two CTAs of 384 x 80 (split tiles: one); 128: one of 640 x 96.
-template <int NT>
-struct Int8Regs {
-  static constexpr int ROLE = 56, WEIGHT = 72, SUM = NT == 64 ? 112 : 184, TOKEN = 72;
-  static_assert(NT != 64 || ROLE + WEIGHT + SUM <= 3 * 80, "the split fits the launch");
-  static_assert(NT != 128 || ROLE + 2 * WEIGHT + SUM + TOKEN <= 5 * 96, "the split fits the launch");
-};
-
 template <class Cfg, int OUT>
-__global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_int8_kernel(const __grid_constant__ KernelParams p) {
+__global__ void __launch_bounds__(Cfg::THREADS, Cfg::NT == 128 ? 1 : 2) gemm_int8_kernel(const __grid_constant__ KernelParams p) {
   extern __shared__ uint8_t smem_raw[];
   // the same offset in every CTA of a cluster: the window's start is
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -471,11 +494,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_int8_kernel(co
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
       ptx::mbar_init(bar.full + 8 * s, 1);
-      ptx::mbar_init(bar.empty + 8 * s, 4 + Cfg::XWARPS);   // the converting warps
+      ptx::mbar_init(bar.empty + 8 * s, Cfg::HALVES ? 4 : 6);   // the converting warps
     }
     for (int s = 0; s < Cfg::CV; ++s) {
-      ptx::mbar_init(bar.cv_full + 8 * s, 4 + Cfg::XWARPS);
+      ptx::mbar_init(bar.cv_full + 8 * s, Cfg::HALVES ? 4 : 6);
       ptx::mbar_init(bar.cv_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < Cfg::XS; ++s) {
+      ptx::mbar_init(bar.x_full + 8 * s, 1);
+      ptx::mbar_init(bar.x_empty + 8 * s, 1);
     }
     for (int b = 0; b < Cfg::BUFS; ++b) {
       ptx::mbar_init(bar.acc_full + 8 * b, 1);
@@ -503,32 +530,27 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_int8_kernel(co
   const uint32_t tmem_base = ctl->tmem_base;
   const Walk walk(p.sched, table, c.unit);
 
-  using Regs = Int8Regs<Cfg::NT>;
   if (warp < 4) {
-    if constexpr (Cfg::REGS) ptx::setmaxnreg_dec<Regs::ROLE>();
+    ptx::setmaxnreg_dec<Cfg::ROLE_REGS>();
     if (warp == 0) {
       if (ptx::elect_one()) int8_producer<Cfg>(p, c, walk, base, bar);
       __syncwarp();
     } else if (warp == 1) {
       if (ptx::elect_one()) int8_mma<Cfg>(p, c, walk, tmem_base, base + Cfg::XCV_OFFSET, bar);
       __syncwarp();
-    } else if constexpr (!Cfg::WIDER) {
+    } else if constexpr (!Cfg::HALVES) {
       int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, warp - 2, bar);
+    } else if (warp == 2) {
+      if (ptx::elect_one()) int8_token_loads<Cfg>(p, c, walk, base + Cfg::XCV_OFFSET, bar);
+      __syncwarp();
     }
-  } else if (warp < 8) {
-    if constexpr (Cfg::REGS) ptx::setmaxnreg_dec<Regs::WEIGHT>();
-    int8_weights<Cfg>(p, c, walk, tmem_base, smem, 0, bar);
-  } else if (warp < 12) {
-    if constexpr (Cfg::REGS) ptx::setmaxnreg_inc<Regs::SUM>();
+  } else if (warp < 8 || warp >= 12) {
+    if constexpr (Cfg::WEIGHT_REGS > Cfg::LAUNCH_REGS) ptx::setmaxnreg_inc<Cfg::WEIGHT_REGS>();
+    else ptx::setmaxnreg_dec<Cfg::WEIGHT_REGS>();
+    int8_weights<Cfg>(p, c, walk, tmem_base, smem, warp < 8 ? 0 : 1, bar);
+  } else {
+    if constexpr (Cfg::SUM_REGS > Cfg::LAUNCH_REGS) ptx::setmaxnreg_inc<Cfg::SUM_REGS>();
     int8_epilogue<Cfg, OUT>(p, c, walk, tmem_base, base + Cfg::RED_OFFSET, bar);
-  } else if constexpr (Cfg::WIDER) {
-    if (warp < 16) {
-      ptx::setmaxnreg_dec<Regs::TOKEN>();
-      int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, warp - 12, bar);
-    } else {
-      ptx::setmaxnreg_dec<Regs::WEIGHT>();
-      int8_weights<Cfg>(p, c, walk, tmem_base, smem, 1, bar);
-    }
   }
 
   ptx::tc_fence_before();

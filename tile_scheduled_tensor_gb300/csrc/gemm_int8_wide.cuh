@@ -59,17 +59,6 @@ __device__ __forceinline__ bool wait_phase_pair_warp(const KernelParams& p, cons
   return __all_sync(0xFFFFFFFFu, wait_phase<2>(p, c, bar, parity, role));
 }
 
-// bounded wait until the copies of an aborting producer have landed
-template <int N>
-__device__ __forceinline__ void int8_land(const KernelParams& p, uint32_t full, uint32_t issued, uint32_t parity) {
-  const uint64_t t0 = ptx::globaltimer();
-  for (int s = 0; s < N; ++s) {
-    if (!(issued & (1u << s))) continue;
-    while (!ptx::mbar_try_wait(full + 8 * s, (parity >> s) & 1u))
-      if (ptx::globaltimer() - t0 > p.timeout_ns) return;
-  }
-}
-
 template <class Cfg>
 __device__ __forceinline__ void int8_wide_weight_loads(const KernelParams& p, const Ctx& c, Walk walk, uint32_t smem, const Int8WideBars<Cfg>& bar) {
   RingAt<Cfg::WS> r;
