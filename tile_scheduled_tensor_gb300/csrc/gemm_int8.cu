@@ -12,7 +12,7 @@ TstInt8Kernel kernel_of(int out_type) {
   using Cfg = tst::Int8Cfg<NT, false>;
   const void* f = out_type == tst::OUT_BF16 ? reinterpret_cast<const void*>(&tst::gemm_int8_kernel<Cfg, tst::OUT_BF16>)
                                             : reinterpret_cast<const void*>(&tst::gemm_int8_kernel<Cfg, tst::OUT_F32>);
-  return {f, Cfg::SMEM_BYTES, Cfg::THREADS, Cfg::PER_SM};
+  return {f, Cfg::SMEM_BYTES, Cfg::THREADS};
 }
 }  // namespace
 
@@ -28,7 +28,7 @@ TstInt8Kernel tst_int8_kernel(int tokens, int out_type, bool split) {
   using Cfg = tst::Int8WideCfg<kInt8WideTokens>;
   const void* f = out_type == tst::OUT_BF16 ? reinterpret_cast<const void*>(&tst::gemm_int8_wide_kernel<Cfg, tst::OUT_BF16>)
                                             : reinterpret_cast<const void*>(&tst::gemm_int8_wide_kernel<Cfg, tst::OUT_F32>);
-  return {f, Cfg::SMEM_BYTES, tst::kInt8WideThreads, 1};
+  return {f, Cfg::SMEM_BYTES, tst::kInt8WideThreads};
 }
 
 bool tst_int8_widen(const void* a, void* half, int64_t rows, int64_t K, const int32_t* group_rows, int32_t groups, int32_t num_sms,

@@ -18,16 +18,18 @@
 // A byte x becomes FP16 as 0x6400 | (x ^ 0x80), which is 1024 + (x + 128), less 1152: for four bytes
 // one exclusive or, two byte permutes, two packed subtractions.
 //
-// Roles, 384 threads (of 128 tokens: 512), persistent over NT x 128 tiles of D, k-blocks of 128:
+// Roles, 768 threads (of 128 tokens: 512), one CTA per SM, persistent over NT x 128 tiles of D, k-blocks
+// of 128:
 //   warp 0      TMA producer: 128 x 128 bytes of B per stage of the byte ring, and up to 32 tokens' bytes
 //   warp 1      MMA issuer: eight K = 16 MMAs per k-block and, every eighth k-block, a new accumulator
 //   warps 2-3   tokens.  Up to 32: bytes of the ring -> FP16 in shared memory (the 128-byte swizzle that
 //               the MMA reads).  From 64 on the conversion would cost more than the weights' (two
 //               warps took 1400 cycles per k-block of 64 tokens, its MMAs take 256): a kernel before
 //               makes A FP16, as for the wide form, and warp 2 brings that by TMA
-//   warps 4-7   weights: a thread per channel, 128 bytes -> 64 columns of Tensor Memory (of 128 tokens
-//               also the last four warps, every second k-block)
 //   warps 8-11  a thread per channel: accumulator -> integer sums; scales, bias, ReLU, cast, store
+//   the others  weights: a thread per channel, 128 bytes -> 64 columns of Tensor Memory.  One k-block
+//               takes a warpgroup 800 to 1000 cycles, most of them latencies, where its 16 KB come in
+//               700 at the copy rate: four warpgroups (of 128 tokens: two) take k-blocks in turn
 // Where the tiles do not fill the SMs, a cluster of 2, 4 or 8 CTAs shares a tile, each taking a part of K.
 // Each CTA then finishes a slice of the tile's tokens: the others write their integer sums of it into its
 // shared memory.  Sums of integers are the same in any order, so a split changes no bit of D.
@@ -45,24 +47,23 @@ struct Int8Cfg {
   static constexpr int NT = NT_;
   static constexpr bool SPLITS = SPLITS_;
   static constexpr bool HALVES = NT >= 64;
-  static constexpr int PER_SM = NT <= 32 || (NT == 64 && !SPLITS) ? 2 : 1;   // CTAs per SM
-  static constexpr int WSETS = NT == 128 ? 2 : 1;          // warpgroups that convert weights, k-blocks in turn
+  static constexpr int WSETS = NT == 128 ? 2 : 4;          // warpgroups that convert weights, k-blocks in turn
   static constexpr int THREADS = 256 + 128 * WSETS;
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_BYTES = NT * 128;                 // a 128-byte column of the tokens' tile
   static constexpr int XCV_BYTES = 2 * X_BYTES;            // FP16 tokens of a k-block: two 64-element atoms
   static constexpr int STAGE_BYTES = HALVES ? W_BYTES : W_BYTES + X_BYTES;   // of the byte ring
-  static constexpr int CV = NT == 64 ? 2 : 3;              // converted k-blocks of weights: 64 TMEM columns each
-  static constexpr int XS = !HALVES ? CV : NT == 64 && !SPLITS ? 2 : 3;      // FP16 k-blocks of tokens
+  static constexpr int CV = NT == 128 ? 4 : NT == 32 ? 5 : 6;   // converted k-blocks of weights: 64 TMEM columns each
+  static constexpr int XS = !HALVES ? CV : 3;              // FP16 k-blocks of tokens
   static constexpr int BUFS = 2;                           // accumulators
   static constexpr int A_COL = BUFS * NT;                  // first TMEM column of the weights
-  static constexpr int USED_COLS = A_COL + CV * 64;
-  static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
+  static constexpr int TMEM_COLS = 512;
   static constexpr int RED_BYTES = SPLITS ? NT * 128 * 4 : 0;   // the cluster's sums of this CTA's slice
-  static constexpr int LIMIT = PER_SM == 2 ? (228 * 1024 - 2 * 1024) / 2 : kSmemLimit;
   static constexpr int FIXED = 1024 + XS * XCV_BYTES + RED_BYTES + kWalkBytes + 512;
-  static constexpr int RAW_STAGES = (LIMIT - FIXED) / STAGE_BYTES;
-  static constexpr int STAGES = RAW_STAGES > 8 ? 8 : RAW_STAGES;
+  // A warpgroup that converts weights meets every WSETS-th k-block alone, and loads land in any order.  A wait
+  // tells a phase only from the one before it, so a stage is always the same warpgroup's (STAGES a multiple
+  // of WSETS), and so many converted k-blocks are there that the one two turns ago is used up (CV >= WSETS).
+  static constexpr int STAGES = (kSmemLimit - FIXED) / STAGE_BYTES / WSETS * WSETS;
   static constexpr int XCV_OFFSET = STAGES * STAGE_BYTES;
   static constexpr int RED_OFFSET = XCV_OFFSET + XS * XCV_BYTES;
   static constexpr int WALK_OFFSET = RED_OFFSET + RED_BYTES;
@@ -71,10 +72,11 @@ struct Int8Cfg {
   static constexpr int MISC_OFFSET = BAR_OFFSET + BARS * 8;
   static constexpr int SMEM_BYTES = 1024 + MISC_OFFSET + 16;
   static_assert(STAGE_BYTES % 1024 == 0 && XCV_BYTES % 1024 == 0, "swizzled tiles start on 1024 bytes");
-  static_assert(SMEM_BYTES <= LIMIT && STAGES >= 2 && PER_SM * TMEM_COLS <= 512 && USED_COLS <= TMEM_COLS, "fits an SM");
+  static_assert(SMEM_BYTES <= kSmemLimit && STAGES >= 4 && STAGES <= 32 && A_COL + CV * 64 <= TMEM_COLS, "fits an SM");
+  static_assert(STAGES % WSETS == 0 && CV >= WSETS, "phases are told apart");
   // registers per thread of the warpgroups: roles (and 2 warps of tokens), weights, sums
-  static constexpr int ROLE_REGS = NT <= 32 ? 72 : 56, WEIGHT_REGS = 88, SUM_REGS = NT <= 32 ? 80 : NT == 64 ? 96 : 184;
-  static constexpr int LAUNCH_REGS = PER_SM == 2 ? 80 : NT == 128 ? 128 : 80;
+  static constexpr int LAUNCH_REGS = NT == 128 ? 128 : 80;
+  static constexpr int ROLE_REGS = HALVES ? 56 : 72, WEIGHT_REGS = NT == 128 ? 88 : 80, SUM_REGS = NT == 128 ? 184 : NT == 64 ? 104 : 88;
   static_assert(ROLE_REGS + WSETS * WEIGHT_REGS + SUM_REGS <= (2 + WSETS) * LAUNCH_REGS, "the split fits the launch");
 };
 
@@ -473,7 +475,7 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
 }
 
 template <class Cfg, int OUT>
-__global__ void __launch_bounds__(Cfg::THREADS, Cfg::NT == 128 ? 1 : 2) gemm_int8_kernel(const __grid_constant__ KernelParams p) {
+__global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid_constant__ KernelParams p) {
   extern __shared__ uint8_t smem_raw[];
   // the same offset in every CTA of a cluster: the window's start is
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -545,11 +547,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::NT == 128 ? 1 : 2) gemm_int
       __syncwarp();
     }
   } else if (warp < 8 || warp >= 12) {
-    if constexpr (Cfg::WEIGHT_REGS > Cfg::LAUNCH_REGS) ptx::setmaxnreg_inc<Cfg::WEIGHT_REGS>();
-    else ptx::setmaxnreg_dec<Cfg::WEIGHT_REGS>();
-    int8_weights<Cfg>(p, c, walk, tmem_base, smem, warp < 8 ? 0 : 1, bar);
+    if constexpr (Cfg::WEIGHT_REGS < Cfg::LAUNCH_REGS) ptx::setmaxnreg_dec<Cfg::WEIGHT_REGS>();
+    int8_weights<Cfg>(p, c, walk, tmem_base, smem, warp < 8 ? 0 : (warp >> 2) - 2, bar);
   } else {
-    if constexpr (Cfg::SUM_REGS > Cfg::LAUNCH_REGS) ptx::setmaxnreg_inc<Cfg::SUM_REGS>();
+    ptx::setmaxnreg_inc<Cfg::SUM_REGS>();
     int8_epilogue<Cfg, OUT>(p, c, walk, tmem_base, base + Cfg::RED_OFFSET, bar);
   }
 

@@ -7,7 +7,7 @@ TstInt8Kernel kernel_of(int out_type) {
   using Cfg = tst::Int8Cfg<NT, true>;
   const void* f = out_type == tst::OUT_BF16 ? reinterpret_cast<const void*>(&tst::gemm_int8_kernel<Cfg, tst::OUT_BF16>)
                                             : reinterpret_cast<const void*>(&tst::gemm_int8_kernel<Cfg, tst::OUT_F32>);
-  return {f, Cfg::SMEM_BYTES, Cfg::THREADS, Cfg::PER_SM};
+  return {f, Cfg::SMEM_BYTES, Cfg::THREADS};
 }
 }  // namespace
 

@@ -104,12 +104,11 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   // a tile's K over as many CTAs as are left idle, each with two k-blocks or more
   const int64_t kt = ceil_div(K, 128);
   const int out_type = opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32;
-  const int64_t slots = int64_t(p->num_sms) * tst_int8_kernel(tokens, out_type, tokens <= kInt8SplitTokens).per_sm;   // of split tiles, where they can be
   if (opts->split > 0) {
     p->split = static_cast<int32_t>(std::min<int64_t>(opts->split, kt));
     while (p->split & (p->split - 1)) --p->split;
   }
-  while (opts->split == 0 && tokens <= kInt8SplitTokens && p->split < 8 && 2 * p->split * tiles <= slots && kt >= 4 * p->split) p->split *= 2;
+  while (opts->split == 0 && tokens <= kInt8SplitTokens && p->split < 8 && 2 * p->split * tiles <= p->num_sms && kt >= 4 * p->split) p->split *= 2;
   p->kernel = tst_int8_kernel(tokens, out_type, p->split > 1);
   const int32_t ctas = pairs ? 2 : p->split;   // of a cluster
   p->dev_bytes = 256 + (tokens >= kInt8HalfTokens ? 2 * static_cast<size_t>(M) * K : 0);
@@ -138,7 +137,7 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   s.map_kind = tst::MAP_GROUPED_M;
   s.group = 8;
   s.dp_tiles = static_cast<int32_t>(mt * nt);
-  s.grid = static_cast<int32_t>(std::min<int64_t>(int64_t(p->num_sms) * p->kernel.per_sm / ctas, tiles));
+  s.grid = static_cast<int32_t>(std::min<int64_t>(p->num_sms / ctas, tiles));
   if (s.grid < 1) s.grid = 1;
   s.sk_groups = 1;
   s.rows = static_cast<int32_t>(M);

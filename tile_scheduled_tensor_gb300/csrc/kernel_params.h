@@ -316,7 +316,7 @@ constexpr int kInt8WideTokens = 192, kInt8SplitTokens = 64;
 constexpr int kInt8HalfTokens = 64;   // from here on A is FP16, made by tst_int8_widen
 struct TstInt8Kernel {
   const void* kernel;
-  int smem_bytes, threads, per_sm;
+  int smem_bytes, threads;
 };
 TstInt8Kernel tst_int8_kernel(int tokens, int out_type, bool split);
 // A's M x K bytes as FP16, those of the groups' rows alone (group_rows not null)
