@@ -18,15 +18,18 @@
 // A byte x becomes FP16 as 0x6400 | (x ^ 0x80), which is 1024 + (x + 128), less 1152: for four bytes
 // one exclusive or, two byte permutes, two packed subtractions.
 //
+// The tokens, far fewer bytes, are made FP16 once per call by int8_widen_kernel, into the plan's workspace,
+// and come by TMA.  (Two warps that converted them beside the weights took 1400 cycles per k-block of 64
+// tokens, and 450 of 16, most of it waiting for their writes to be seen by the tensor core.)
+//
 // Roles, 768 threads (of 128 tokens: 512), one CTA per SM, persistent over NT x 128 tiles of D, k-blocks
 // of 128:
-//   warp 0      TMA producer: 128 x 128 bytes of B per stage of the byte ring, and up to 32 tokens' bytes
-//   warp 1      MMA issuer: eight K = 16 MMAs per k-block and, every eighth k-block, a new accumulator
-//   warps 2-3   tokens.  Up to 32: bytes of the ring -> FP16 in shared memory (the 128-byte swizzle that
-//               the MMA reads).  From 64 on the conversion would cost more than the weights' (two
-//               warps took 1400 cycles per k-block of 64 tokens, its MMAs take 256): a kernel before
-//               makes A FP16, as for the wide form, and warp 2 brings that by TMA
-//   warps 8-11  a thread per channel: accumulator -> integer sums; scales, bias, ReLU, cast, store
+//   warp 0      TMA: 128 x 128 bytes of B per stage of the byte ring
+//   warps 1, 3  MMA issuers of every second k-block, into accumulators of their own: eight K = 16 MMAs,
+//               which one thread issues in about 64 cycles each, however few tokens they have; every
+//               eighth k-block of theirs into a new accumulator
+//   warp 2      TMA: NT tokens, FP16, two 64-element atoms per k-block
+//   warps 8-11  a thread per channel: accumulators -> integer sums; scales, bias, ReLU, cast, store
 //   the others  weights: a thread per channel, 128 bytes -> 64 columns of Tensor Memory.  One k-block
 //               takes a warpgroup 800 to 1000 cycles, most of them latencies, where its 16 KB come in
 //               700 at the copy rate: four warpgroups (of 128 tokens: two) take k-blocks in turn
@@ -41,42 +44,40 @@ namespace tst {
 
 constexpr int kInt8Fold = 8;   // k-blocks of 128 per accumulator: 1024 products of at most 2^14
 
-// SPLITS: a cluster of CTAs shares each tile along K.  HALVES: A has been made FP16 before (int8_widen_kernel).
+// SPLITS: a cluster of CTAs shares each tile along K.
 template <int NT_, bool SPLITS_>
 struct Int8Cfg {
   static constexpr int NT = NT_;
   static constexpr bool SPLITS = SPLITS_;
-  static constexpr bool HALVES = NT >= 64;
   static constexpr int WSETS = NT == 128 ? 2 : 4;          // warpgroups that convert weights, k-blocks in turn
   static constexpr int THREADS = 256 + 128 * WSETS;
   static constexpr int W_BYTES = 128 * 128;
-  static constexpr int X_BYTES = NT * 128;                 // a 128-byte column of the tokens' tile
-  static constexpr int XCV_BYTES = 2 * X_BYTES;            // FP16 tokens of a k-block: two 64-element atoms
-  static constexpr int STAGE_BYTES = HALVES ? W_BYTES : W_BYTES + X_BYTES;   // of the byte ring
-  static constexpr int CV = NT == 128 ? 4 : NT == 32 ? 5 : 6;   // converted k-blocks of weights: 64 TMEM columns each
-  static constexpr int XS = !HALVES ? CV : 3;              // FP16 k-blocks of tokens
-  static constexpr int BUFS = 2;                           // accumulators
-  static constexpr int A_COL = BUFS * NT;                  // first TMEM column of the weights
-  static constexpr int TMEM_COLS = 512;
+  static constexpr int X_ATOM = NT * 128;                  // 64 elements of the tokens' tile
+  static constexpr int X_BYTES = 2 * X_ATOM;
+  static constexpr int BUFS = NT == 128 ? 1 : 2;           // accumulators per issuer
+  static constexpr int A_COL = 2 * BUFS * NT;              // first TMEM column of the weights
+  static constexpr int CV = (512 - A_COL) / 128 * 2;       // converted k-blocks of weights: 64 TMEM columns each
+  static constexpr int XS = NT <= 32 ? 6 : 4;              // k-blocks of tokens
   static constexpr int RED_BYTES = SPLITS ? NT * 128 * 4 : 0;   // the cluster's sums of this CTA's slice
-  static constexpr int FIXED = 1024 + XS * XCV_BYTES + RED_BYTES + kWalkBytes + 512;
-  // A warpgroup that converts weights meets every WSETS-th k-block alone, and loads land in any order.  A wait
-  // tells a phase only from the one before it, so a stage is always the same warpgroup's (STAGES a multiple
-  // of WSETS), and so many converted k-blocks are there that the one two turns ago is used up (CV >= WSETS).
-  static constexpr int STAGES = (kSmemLimit - FIXED) / STAGE_BYTES / WSETS * WSETS;
-  static constexpr int XCV_OFFSET = STAGES * STAGE_BYTES;
-  static constexpr int RED_OFFSET = XCV_OFFSET + XS * XCV_BYTES;
+  static constexpr int FIXED = 1024 + XS * X_BYTES + RED_BYTES + kWalkBytes + 512;
+  // A warpgroup that converts weights meets every WSETS-th k-block alone, an issuer every second one, and
+  // loads land and warpgroups finish in any order.  A wait tells a phase only from the one before it, so a
+  // stage is always the same warpgroup's (STAGES a multiple of WSETS) and the same issuer's (CV and XS even),
+  // and so many converted k-blocks are there that the one two turns ago is used up (CV >= WSETS).
+  static constexpr int STAGES = (kSmemLimit - FIXED) / W_BYTES / WSETS * WSETS;
+  static constexpr int X_OFFSET = STAGES * W_BYTES;
+  static constexpr int RED_OFFSET = X_OFFSET + XS * X_BYTES;
   static constexpr int WALK_OFFSET = RED_OFFSET + RED_BYTES;
   static constexpr int BAR_OFFSET = (WALK_OFFSET + kWalkBytes + 7) / 8 * 8;
-  static constexpr int BARS = 2 * STAGES + 2 * CV + 2 * XS + 2 * BUFS + 3;
+  static constexpr int BARS = 2 * STAGES + 2 * CV + 2 * XS + 4 * BUFS + 3;
   static constexpr int MISC_OFFSET = BAR_OFFSET + BARS * 8;
   static constexpr int SMEM_BYTES = 1024 + MISC_OFFSET + 16;
-  static_assert(STAGE_BYTES % 1024 == 0 && XCV_BYTES % 1024 == 0, "swizzled tiles start on 1024 bytes");
-  static_assert(SMEM_BYTES <= kSmemLimit && STAGES >= 4 && STAGES <= 32 && A_COL + CV * 64 <= TMEM_COLS, "fits an SM");
-  static_assert(STAGES % WSETS == 0 && CV >= WSETS, "phases are told apart");
-  // registers per thread of the warpgroups: roles (and 2 warps of tokens), weights, sums
+  static_assert(X_ATOM % 1024 == 0, "swizzled tiles start on 1024 bytes");
+  static_assert(SMEM_BYTES <= kSmemLimit && STAGES >= 4 && STAGES <= 32, "fits an SM");
+  static_assert(STAGES % WSETS == 0 && CV >= WSETS && CV % 2 == 0 && XS % 2 == 0, "phases are told apart");
+  // registers per thread of the warpgroups: roles, weights, sums
   static constexpr int LAUNCH_REGS = NT == 128 ? 128 : 80;
-  static constexpr int ROLE_REGS = HALVES ? 56 : 72, WEIGHT_REGS = NT == 128 ? 88 : 80, SUM_REGS = NT == 128 ? 184 : NT == 64 ? 104 : 88;
+  static constexpr int ROLE_REGS = 56, WEIGHT_REGS = NT == 128 ? 88 : 80, SUM_REGS = NT == 128 ? 184 : 104;
   static_assert(ROLE_REGS + WSETS * WEIGHT_REGS + SUM_REGS <= (2 + WSETS) * LAUNCH_REGS, "the split fits the launch");
 };
 
@@ -97,14 +98,14 @@ struct OutOf { using T = float; };
 template <>
 struct OutOf<OUT_BF16> { using T = __nv_bfloat16; };
 
-// The shared addresses of the barriers: byte ring, converted k-blocks, accumulators, drain.
+// The shared addresses of the barriers: byte ring, converted k-blocks, tokens, each issuer's accumulators.
 template <class Cfg>
 struct Int8Bars {
   uint32_t full, empty, cv_full, cv_empty, x_full, x_empty, acc_full, acc_empty, drain, red_full, red_empty;
   __device__ __forceinline__ explicit Int8Bars(uint32_t base)
       : full(base), empty(full + 8 * Cfg::STAGES), cv_full(empty + 8 * Cfg::STAGES), cv_empty(cv_full + 8 * Cfg::CV),
-        x_full(cv_empty + 8 * Cfg::CV), x_empty(x_full + 8 * Cfg::XS), acc_full(x_empty + 8 * Cfg::XS), acc_empty(acc_full + 8 * Cfg::BUFS), drain(acc_empty + 8 * Cfg::BUFS),
-        red_full(drain + 8), red_empty(red_full + 8) {}
+        x_full(cv_empty + 8 * Cfg::CV), x_empty(x_full + 8 * Cfg::XS), acc_full(x_empty + 8 * Cfg::XS),
+        acc_empty(acc_full + 16 * Cfg::BUFS), drain(acc_empty + 16 * Cfg::BUFS), red_full(drain + 8), red_empty(red_full + 8) {}
 };
 
 // this CTA's k-blocks: all, or its part of a split tile's
@@ -148,10 +149,9 @@ __device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& 
     const int32_t b_row0 = w.group * p.sched.group_b_rows + w.n * 128;
     for (int32_t kb = k.first; kb < k.end; ++kb) {
       if (!wait_phase<1>(p, c, bar.empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
-      const uint32_t full = bar.full + 8 * r.at, dst = smem + r.at * Cfg::STAGE_BYTES;
-      ptx::mbar_arrive_expect_tx(full, Cfg::STAGE_BYTES);
+      const uint32_t full = bar.full + 8 * r.at, dst = smem + r.at * Cfg::W_BYTES;
+      ptx::mbar_arrive_expect_tx(full, Cfg::W_BYTES);
       ptx::tma_load_2d(dst, &p.tmap_b, full, kb * 128, b_row0);
-      if constexpr (!Cfg::HALVES) ptx::tma_load_2d(dst + Cfg::W_BYTES, &p.tmap_a, full, kb * 128, w.row0);
       issued |= 1u << r.at;
       issued_parity = (issued_parity & ~(1u << r.at)) | (r.phase << r.at);
       r.next();
@@ -160,7 +160,7 @@ __device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& 
   if (!ok) int8_land<Cfg::STAGES>(p, bar.full, issued, issued_parity);
 }
 
-// FP16 tokens: NT rows of two 64-element atoms per k-block.
+// NT rows of two 64-element atoms per k-block.
 template <class Cfg>
 __device__ __forceinline__ void int8_token_loads(const KernelParams& p, const Ctx& c, Walk walk, uint32_t xs, const Int8Bars<Cfg>& bar) {
   const KRange k(p, c);
@@ -172,10 +172,10 @@ __device__ __forceinline__ void int8_token_loads(const KernelParams& p, const Ct
   while (ok && walk.next(w)) {
     for (int32_t kb = k.first; kb < k.end; ++kb) {
       if (!wait_phase<1>(p, c, bar.x_empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
-      const uint32_t full = bar.x_full + 8 * r.at, dst = xs + r.at * Cfg::XCV_BYTES;
-      ptx::mbar_arrive_expect_tx(full, Cfg::XCV_BYTES);
+      const uint32_t full = bar.x_full + 8 * r.at, dst = xs + r.at * Cfg::X_BYTES;
+      ptx::mbar_arrive_expect_tx(full, Cfg::X_BYTES);
       ptx::tma_load_2d(dst, &p.tmap_a, full, kb * 128, w.row0);
-      ptx::tma_load_2d(dst + Cfg::X_BYTES, &p.tmap_a, full, kb * 128 + 64, w.row0);
+      ptx::tma_load_2d(dst + Cfg::X_ATOM, &p.tmap_a, full, kb * 128 + 64, w.row0);
       issued |= 1u << r.at;
       issued_parity = (issued_parity & ~(1u << r.at)) | (r.phase << r.at);
       r.next();
@@ -184,36 +184,37 @@ __device__ __forceinline__ void int8_token_loads(const KernelParams& p, const Ct
   if (!ok) int8_land<Cfg::XS>(p, bar.x_full, issued, issued_parity);
 }
 
+// issuer: of the two that take the k-blocks in turn, each into its own accumulators
 template <class Cfg>
-__device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, uint32_t xcv,
+__device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, uint32_t xs, int issuer,
                                          const Int8Bars<Cfg>& bar) {
   const uint32_t idesc = ptx::make_idesc(0u, 128, Cfg::NT);   // FP16 operands
-  const uint64_t x_desc0 = ptx::sw128_kmajor_desc(xcv);
+  const uint64_t x_desc0 = ptx::sw128_kmajor_desc(xs);
   const KRange k(p, c);
+  const int32_t blocks = k.end - k.first;
+  const uint32_t acc_full = bar.acc_full + 8 * Cfg::BUFS * issuer, acc_empty = bar.acc_empty + 8 * Cfg::BUFS * issuer;
   RingAt<Cfg::CV> r;
-  RingAt<Cfg::XS> xr;   // of tokens: by TMA, or beside the weights of the same k-block
+  RingAt<Cfg::XS> x;
   RingAt<Cfg::BUFS> acc;
   bool ok = true;
   while (ok && walk.skip()) {
-    for (int32_t kb = k.first; kb < k.end; ++kb) {
-      const int32_t in_fold = (kb - k.first) % kInt8Fold;
-      if (in_fold == 0 && !wait_phase<1>(p, c, bar.acc_empty + 8 * acc.at, acc.phase ^ 1u, ROLE_MMA)) { ok = false; break; }
-      if constexpr (Cfg::HALVES)
-        if (!wait_phase<1>(p, c, bar.x_full + 8 * xr.at, xr.phase, ROLE_MMA)) { ok = false; break; }
+    for (int32_t i = 0; i < blocks; ++i, r.next(), x.next()) {
+      if ((i & 1) != issuer) continue;
+      const int32_t in_fold = (i >> 1) % kInt8Fold;
+      if (in_fold == 0 && !wait_phase<1>(p, c, acc_empty + 8 * acc.at, acc.phase ^ 1u, ROLE_MMA)) { ok = false; break; }
+      if (!wait_phase<1>(p, c, bar.x_full + 8 * x.at, x.phase, ROLE_MMA)) { ok = false; break; }
       if (!wait_phase<1>(p, c, bar.cv_full + 8 * r.at, r.phase, ROLE_MMA)) { ok = false; break; }
       ptx::tc_fence_after();
-      const uint32_t d = tmem_base + static_cast<uint32_t>(acc.at * Cfg::NT);
+      const uint32_t d = tmem_base + static_cast<uint32_t>((issuer * Cfg::BUFS + acc.at) * Cfg::NT);
       const uint32_t a = tmem_base + static_cast<uint32_t>(Cfg::A_COL + r.at * 64);
-      const uint64_t x = x_desc0 + static_cast<uint64_t>(xr.at * (Cfg::XCV_BYTES >> 4));
+      const uint64_t xd = x_desc0 + static_cast<uint64_t>(x.at * (Cfg::X_BYTES >> 4));
 #pragma unroll
-      for (int i = 0; i < 8; ++i)   // 16 of K: 8 TMEM columns, 32 bytes of an atom
-        ptx::mma_f16_ts(d, a + 8 * i, x + (i >> 2) * (Cfg::X_BYTES >> 4) + (i & 3) * 2, idesc, in_fold != 0 || i != 0);
+      for (int q = 0; q < 8; ++q)   // 16 of K: 8 TMEM columns, 32 bytes of an atom
+        ptx::mma_f16_ts(d, a + 8 * q, xd + (q >> 2) * (Cfg::X_ATOM >> 4) + (q & 3) * 2, idesc, in_fold != 0 || q != 0);
       ptx::mma_commit(bar.cv_empty + 8 * r.at);
-      if constexpr (Cfg::HALVES) ptx::mma_commit(bar.x_empty + 8 * xr.at);
-      r.next();
-      xr.next();
-      if (in_fold == kInt8Fold - 1 || kb == k.end - 1) {
-        ptx::mma_commit(bar.acc_full + 8 * acc.at);
+      ptx::mma_commit(bar.x_empty + 8 * x.at);
+      if (in_fold == kInt8Fold - 1 || i + 2 >= blocks) {
+        ptx::mma_commit(acc_full + 8 * acc.at);
         acc.next();
       }
     }
@@ -225,53 +226,6 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
     if (ptx::globaltimer() - t0 > p.timeout_ns) {
       raise_error<1>(p, c, ST_TIMEOUT, ROLE_MMA);
       break;
-    }
-  }
-}
-
-// Eight lanes take the same 16-byte piece of eight rows, which the swizzle puts in eight different
-// banks' worth of shared memory, reading and writing.
-template <class Cfg>
-__device__ __forceinline__ void int8_tokens(const KernelParams& p, const Ctx& c, Walk walk, uint8_t* smem, uint8_t* xcv, int warp,
-                                            const Int8Bars<Cfg>& bar) {
-  constexpr int PIECES = Cfg::NT / 8;   // of 16 bytes, per thread of two warps and k-block: 2 or 4
-  constexpr int ROWS = 8;               // rows between a thread's pieces
-  constexpr int FLIGHT = PIECES;
-  const int lane = threadIdx.x & 31;
-  const int j = warp * 4 + (lane >> 3), sub = lane & 7;   // piece of the row, row of eight
-  const KRange k(p, c);
-  RingAt<Cfg::STAGES> r;
-  RingAt<Cfg::CV> t;
-  const uint8_t* const src0 = smem + Cfg::W_BYTES + sub * 128 + ((j ^ sub) << 4);
-  uint8_t* const dst0 = xcv + (j >> 2) * Cfg::X_BYTES + sub * 128;
-  const int c0 = (((2 * j) & 7) ^ sub) << 4, c1 = (((2 * j + 1) & 7) ^ sub) << 4;
-  while (walk.skip()) {
-    for (int32_t kb = k.first; kb < k.end; ++kb) {
-      if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return;
-      const uint8_t* const src = src0 + r.at * Cfg::STAGE_BYTES;
-      uint8_t* const dst = dst0 + t.at * Cfg::XCV_BYTES;
-#pragma unroll
-      for (int i = 0; i < PIECES; i += FLIGHT) {
-        uint4 v[FLIGHT];
-#pragma unroll
-        for (int q = 0; q < FLIGHT; ++q) v[q] = *reinterpret_cast<const uint4*>(src + (i + q) * ROWS * 128);
-        if (i == 0 && !wait_phase_warp(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE)) return;
-#pragma unroll
-        for (int q = 0; q < FLIGHT; ++q) {
-          uint32_t h[8];
-          int8_to_half(v[q], h);
-          *reinterpret_cast<uint4*>(dst + (i + q) * ROWS * 128 + c0) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + (i + q) * ROWS * 128 + c1) = make_uint4(h[4], h[5], h[6], h[7]);
-        }
-      }
-      ptx::fence_proxy_async_smem();   // the MMA reads these writes through the async proxy
-      __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive(bar.empty + 8 * r.at);
-        ptx::mbar_arrive(bar.cv_full + 8 * t.at);
-      }
-      r.next();
-      t.next();
     }
   }
 }
@@ -293,7 +247,7 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
   uint4 v[8];
   auto read = [&] {   // a k-block's bytes, which frees its stage
     if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return false;
-    const uint8_t* const src = src0 + r.at * Cfg::STAGE_BYTES;
+    const uint8_t* const src = src0 + r.at * Cfg::W_BYTES;
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = *reinterpret_cast<const uint4*>(src + ((q ^ sub) << 4));
     return true;
@@ -439,29 +393,33 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
   const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
   const KRange k(p, c);
   uint32_t red_phase = 0;
-  RingAt<Cfg::BUFS> acc;
+  RingAt<Cfg::BUFS> acc0, acc1;   // the issuers'
   Tile w;
   while (walk.next_warp(w)) {
     RowScales<Cfg::NT> scale;
     scale.load(p, w.row0);
     int32_t sum[Cfg::NT];
-    for (int32_t kb = k.first; kb < k.end; kb += kInt8Fold) {
-      if (!wait_phase_warp(p, c, bar.acc_full + 8 * acc.at, acc.phase, ROLE_EPILOGUE)) return;
+    bool first = true;
+    for (int32_t i = 0; i < k.end - k.first; i += (i & 1) ? 2 * kInt8Fold - 1 : 1) {   // the first k-block of each accumulator
+      const int issuer = i & 1, at = issuer * Cfg::BUFS + (issuer ? acc1.at : acc0.at);
+      if (!wait_phase_warp(p, c, bar.acc_full + 8 * at, issuer ? acc1.phase : acc0.phase, ROLE_EPILOGUE)) return;
       ptx::tc_fence_after();
 #pragma unroll
       for (int q = 0; q < Cfg::NT; q += 16) {
         float v[16];
-        ptx::tmem_load_16cols(taddr0 + static_cast<uint32_t>(acc.at * Cfg::NT + q), v);
+        ptx::tmem_load_16cols(taddr0 + static_cast<uint32_t>(at * Cfg::NT + q), v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int32_t x = __float2int_rn(v[i]);   // a whole number already
-          sum[q + i] = kb == k.first ? x : sum[q + i] + x;
+        for (int j = 0; j < 16; ++j) {
+          const int32_t x = __float2int_rn(v[j]);   // a whole number already
+          sum[q + j] = first ? x : sum[q + j] + x;
         }
       }
+      first = false;
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar.acc_empty + 8 * acc.at);
-      acc.next();
+      if (lane == 0) ptx::mbar_arrive(bar.acc_empty + 8 * at);
+      if (issuer) acc1.next();
+      else acc0.next();
     }
     if constexpr (Cfg::SPLITS) {
       if (c.csize > 1) {
@@ -496,21 +454,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
       ptx::mbar_init(bar.full + 8 * s, 1);
-      ptx::mbar_init(bar.empty + 8 * s, Cfg::HALVES ? 4 : 6);   // the converting warps
+      ptx::mbar_init(bar.empty + 8 * s, 4);      // the warpgroup that converts it
     }
     for (int s = 0; s < Cfg::CV; ++s) {
-      ptx::mbar_init(bar.cv_full + 8 * s, Cfg::HALVES ? 4 : 6);
+      ptx::mbar_init(bar.cv_full + 8 * s, 4);
       ptx::mbar_init(bar.cv_empty + 8 * s, 1);
     }
     for (int s = 0; s < Cfg::XS; ++s) {
       ptx::mbar_init(bar.x_full + 8 * s, 1);
       ptx::mbar_init(bar.x_empty + 8 * s, 1);
     }
-    for (int b = 0; b < Cfg::BUFS; ++b) {
+    for (int b = 0; b < 2 * Cfg::BUFS; ++b) {
       ptx::mbar_init(bar.acc_full + 8 * b, 1);
       ptx::mbar_init(bar.acc_empty + 8 * b, 4);
     }
-    ptx::mbar_init(bar.drain, 1);
+    ptx::mbar_init(bar.drain, 2);                 // both issuers
     ptx::mbar_init(bar.red_full, 4 * c.csize);    // the summing warps of the cluster
     ptx::mbar_init(bar.red_empty, 4 * c.csize);
     ctl->abort = 0;
@@ -520,7 +478,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid
     ptx::prefetch_tmap(&p.tmap_b);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), Cfg::TMEM_COLS);
+    ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), 512);
     ptx::tmem_relinquish();
   }
   const GroupTable table(smem + Cfg::WALK_OFFSET);
@@ -536,16 +494,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid
     ptx::setmaxnreg_dec<Cfg::ROLE_REGS>();
     if (warp == 0) {
       if (ptx::elect_one()) int8_producer<Cfg>(p, c, walk, base, bar);
-      __syncwarp();
-    } else if (warp == 1) {
-      if (ptx::elect_one()) int8_mma<Cfg>(p, c, walk, tmem_base, base + Cfg::XCV_OFFSET, bar);
-      __syncwarp();
-    } else if constexpr (!Cfg::HALVES) {
-      int8_tokens<Cfg>(p, c, walk, smem, smem + Cfg::XCV_OFFSET, warp - 2, bar);
     } else if (warp == 2) {
-      if (ptx::elect_one()) int8_token_loads<Cfg>(p, c, walk, base + Cfg::XCV_OFFSET, bar);
-      __syncwarp();
+      if (ptx::elect_one()) int8_token_loads<Cfg>(p, c, walk, base + Cfg::X_OFFSET, bar);
+    } else if (ptx::elect_one()) {
+      int8_mma<Cfg>(p, c, walk, tmem_base, base + Cfg::X_OFFSET, warp >> 1, bar);
     }
+    __syncwarp();
   } else if (warp < 8 || warp >= 12) {
     if constexpr (Cfg::WEIGHT_REGS < Cfg::LAUNCH_REGS) ptx::setmaxnreg_dec<Cfg::WEIGHT_REGS>();
     int8_weights<Cfg>(p, c, walk, tmem_base, smem, warp < 8 ? 0 : (warp >> 2) - 2, bar);
@@ -560,7 +514,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid
   if (warp == 1) {
     __syncwarp();
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+    ptx::tmem_dealloc(tmem_base, 512);
   }
 }
 

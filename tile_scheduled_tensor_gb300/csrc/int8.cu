@@ -19,7 +19,7 @@ struct tst_int8_plan {
   bool pairs = false;          // the wide form
   int32_t split = 1;           // CTAs that share a tile along K
   tst::Sched sched{};
-  unsigned long long* d_status = nullptr;   // 256 bytes, then A in FP16 from kInt8HalfTokens on
+  unsigned long long* d_status = nullptr;   // 256 bytes, then A in FP16
   size_t dev_bytes = 0;
   cudaStream_t last_stream = nullptr;
   bool ran = false;
@@ -111,7 +111,7 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   while (opts->split == 0 && tokens <= kInt8SplitTokens && p->split < 8 && 2 * p->split * tiles <= p->num_sms && kt >= 4 * p->split) p->split *= 2;
   p->kernel = tst_int8_kernel(tokens, out_type, p->split > 1);
   const int32_t ctas = pairs ? 2 : p->split;   // of a cluster
-  p->dev_bytes = 256 + (tokens >= kInt8HalfTokens ? 2 * static_cast<size_t>(M) * K : 0);
+  p->dev_bytes = 256 + 2 * static_cast<size_t>(M) * K;
   if (!opts->host_only) {
     if (cudaFuncSetAttribute(p->kernel.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p->kernel.smem_bytes) != cudaSuccess) {
       cudaGetLastError();
@@ -206,8 +206,7 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
   const bool pairs = p->pairs;
   const int32_t ctas = pairs ? 2 : p->split;   // of a cluster
   void* const half = p->d_status + 32;
-  const bool halves = p->tokens >= kInt8HalfTokens;
-  if (!(halves ? tst_encode_halves(&kp.tmap_a, half, p->M, p->K, pairs ? p->tokens / 2 : p->tokens) : tst_encode_bytes(&kp.tmap_a, A, p->M, p->K, p->tokens)) ||
+  if (!tst_encode_halves(&kp.tmap_a, half, p->M, p->K, pairs ? p->tokens / 2 : p->tokens) ||
       !tst_encode_bytes(&kp.tmap_b, B, std::max<int64_t>(p->sched.groups, 1) * p->N, p->K, 128))
     return TST_ERR_CUDA;
   kp.C = D;
@@ -240,16 +239,14 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
     attr[na].val.clusterDim.z = 1;
     ++na;
   }
-  if (halves) {
-    // it may start while A is made FP16, and waits for that itself
-    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[na].val.programmaticStreamSerializationAllowed = 1;
-    ++na;
-  }
-  cfg.attrs = na ? attr : nullptr;
+  // it may start while A is made FP16, and waits for that itself
+  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[na].val.programmaticStreamSerializationAllowed = 1;
+  ++na;
+  cfg.attrs = attr;
   cfg.numAttrs = na;
   void* args[] = {&kp};
-  if (halves && !tst_int8_widen(A, half, p->M, p->K, group_rows, p->sched.groups, p->num_sms, s)) return TST_ERR_CUDA;
+  if (!tst_int8_widen(A, half, p->M, p->K, group_rows, p->sched.groups, p->num_sms, s)) return TST_ERR_CUDA;
   if (cudaLaunchKernelExC(&cfg, p->kernel.kernel, args) != cudaSuccess) {
     cudaGetLastError();
     return TST_ERR_CUDA;

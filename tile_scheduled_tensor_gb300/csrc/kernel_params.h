@@ -311,9 +311,8 @@ TstBsKernel tst_bs_narrow(int rows, int out_type, bool shared);
 
 // GEMM of 8-bit integers (gemm_int8.cu): `tokens` = 16, 32, 64 or 128 rows of A per 128-column tile of a CTA
 // (up to 64: of a cluster of KernelParams::sk_slots CTAs that split the tile along K), or kInt8WideTokens per
-// 256-column tile of a CTA pair
+// 256-column tile of a CTA pair; A is FP16, made by tst_int8_widen
 constexpr int kInt8WideTokens = 192, kInt8SplitTokens = 64;
-constexpr int kInt8HalfTokens = 64;   // from here on A is FP16, made by tst_int8_widen
 struct TstInt8Kernel {
   const void* kernel;
   int smem_bytes, threads;
