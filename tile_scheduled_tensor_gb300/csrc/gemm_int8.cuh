@@ -54,10 +54,10 @@ struct Int8Cfg {
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_ATOM = NT * 128;                  // 64 elements of the tokens' tile
   static constexpr int X_BYTES = 2 * X_ATOM;
-  static constexpr int BUFS = NT == 128 ? 1 : 2;           // accumulators per issuer
+  static constexpr int BUFS = NT >= 64 ? 1 : 2;            // accumulators per issuer
   static constexpr int A_COL = 2 * BUFS * NT;              // first TMEM column of the weights
   static constexpr int CV = (512 - A_COL) / 128 * 2;       // converted k-blocks of weights: 64 TMEM columns each
-  static constexpr int XS = NT <= 32 ? 6 : 4;              // k-blocks of tokens
+  static constexpr int XS = NT <= 64 ? 6 : 4;              // k-blocks of tokens
   static constexpr int RED_BYTES = SPLITS ? NT * 128 * 4 : 0;   // the cluster's sums of this CTA's slice
   static constexpr int FIXED = 1024 + XS * X_BYTES + RED_BYTES + kWalkBytes + 512;
   // A warpgroup that converts weights meets every WSETS-th k-block alone, an issuer every second one, and
@@ -116,6 +116,27 @@ struct KRange {
         end(p.sched.kt * static_cast<int32_t>(c.rank + 1) / static_cast<int32_t>(c.csize)) {}
 };
 
+// wait_phase with the waiting thread suspended.  Many warps wait here beside those that work, and tries that
+// return at once take their places in the queue to shared memory.
+constexpr uint32_t kInt8Suspend = 1000;   // ns
+template <int CG>
+__device__ __forceinline__ bool int8_wait(const KernelParams& p, const Ctx& c, uint32_t bar, uint32_t parity, uint32_t role) {
+  if (ptx::mbar_try_wait_for(bar, parity, kInt8Suspend)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  while (true) {
+    if (ptx::mbar_try_wait_for(bar, parity, kInt8Suspend)) return true;
+    if (*c.abort) return false;
+    if (ptx::globaltimer() - t0 > p.timeout_ns) {
+      raise_error<CG>(p, c, ST_TIMEOUT, role);
+      return false;
+    }
+  }
+}
+template <int CG>
+__device__ __forceinline__ bool int8_wait_warp(const KernelParams& p, const Ctx& c, uint32_t bar, uint32_t parity, uint32_t role) {
+  return __all_sync(0xFFFFFFFFu, int8_wait<CG>(p, c, bar, parity, role));
+}
+
 // position in a ring of N
 template <int N>
 struct RingAt {
@@ -148,7 +169,7 @@ __device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& 
     if (w.clamped && c.rank == 0) record_status(p, ST_DEVICE_CHECK, ROLE_PRODUCER);
     const int32_t b_row0 = w.group * p.sched.group_b_rows + w.n * 128;
     for (int32_t kb = k.first; kb < k.end; ++kb) {
-      if (!wait_phase<1>(p, c, bar.empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
+      if (!int8_wait<1>(p, c, bar.empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
       const uint32_t full = bar.full + 8 * r.at, dst = smem + r.at * Cfg::W_BYTES;
       ptx::mbar_arrive_expect_tx(full, Cfg::W_BYTES);
       ptx::tma_load_2d(dst, &p.tmap_b, full, kb * 128, b_row0);
@@ -171,7 +192,7 @@ __device__ __forceinline__ void int8_token_loads(const KernelParams& p, const Ct
   ptx::griddep_wait();   // they are the kernel's before
   while (ok && walk.next(w)) {
     for (int32_t kb = k.first; kb < k.end; ++kb) {
-      if (!wait_phase<1>(p, c, bar.x_empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
+      if (!int8_wait<1>(p, c, bar.x_empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
       const uint32_t full = bar.x_full + 8 * r.at, dst = xs + r.at * Cfg::X_BYTES;
       ptx::mbar_arrive_expect_tx(full, Cfg::X_BYTES);
       ptx::tma_load_2d(dst, &p.tmap_a, full, kb * 128, w.row0);
@@ -197,13 +218,14 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
   RingAt<Cfg::XS> x;
   RingAt<Cfg::BUFS> acc;
   bool ok = true;
+  uint32_t count = 0;   // k-blocks so far, of all tiles: a tile's first is either issuer's
   while (ok && walk.skip()) {
-    for (int32_t i = 0; i < blocks; ++i, r.next(), x.next()) {
-      if ((i & 1) != issuer) continue;
+    for (int32_t i = 0; i < blocks; ++i, ++count, r.next(), x.next()) {
+      if ((count & 1u) != static_cast<uint32_t>(issuer)) continue;
       const int32_t in_fold = (i >> 1) % kInt8Fold;
-      if (in_fold == 0 && !wait_phase<1>(p, c, acc_empty + 8 * acc.at, acc.phase ^ 1u, ROLE_MMA)) { ok = false; break; }
-      if (!wait_phase<1>(p, c, bar.x_full + 8 * x.at, x.phase, ROLE_MMA)) { ok = false; break; }
-      if (!wait_phase<1>(p, c, bar.cv_full + 8 * r.at, r.phase, ROLE_MMA)) { ok = false; break; }
+      if (in_fold == 0 && !int8_wait<1>(p, c, acc_empty + 8 * acc.at, acc.phase ^ 1u, ROLE_MMA)) { ok = false; break; }
+      if (!int8_wait<1>(p, c, bar.x_full + 8 * x.at, x.phase, ROLE_MMA)) { ok = false; break; }
+      if (!int8_wait<1>(p, c, bar.cv_full + 8 * r.at, r.phase, ROLE_MMA)) { ok = false; break; }
       ptx::tc_fence_after();
       const uint32_t d = tmem_base + static_cast<uint32_t>((issuer * Cfg::BUFS + acc.at) * Cfg::NT);
       const uint32_t a = tmem_base + static_cast<uint32_t>(Cfg::A_COL + r.at * 64);
@@ -230,8 +252,7 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
   }
 }
 
-// set: of WSETS that take the k-blocks in turn.  The next k-block's bytes are read while this one's stores
-// into Tensor Memory complete.
+// set: of WSETS that take the k-blocks in turn.
 template <class Cfg>
 __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, const uint8_t* smem,
                                              int set, const Int8Bars<Cfg>& bar) {
@@ -244,18 +265,14 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
   while (walk.skip()) blocks += k.end - k.first;
   RingAt<Cfg::STAGES> r;
   RingAt<Cfg::CV> t;
-  uint4 v[8];
-  auto read = [&] {   // a k-block's bytes, which frees its stage
-    if (!wait_phase_warp(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return false;
+  for (int i = 0; i < set; ++i) { r.next(); t.next(); }
+  for (int64_t i = set; i < blocks; i += Cfg::WSETS) {
+    if (!int8_wait_warp<1>(p, c, bar.full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return;
     const uint8_t* const src = src0 + r.at * Cfg::W_BYTES;
+    uint4 v[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = *reinterpret_cast<const uint4*>(src + ((q ^ sub) << 4));
-    return true;
-  };
-  for (int i = 0; i < set; ++i) { r.next(); t.next(); }
-  if (set < blocks && !read()) return;
-  for (int64_t i = set; i < blocks; i += Cfg::WSETS) {
-    if (!wait_phase_warp(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE)) return;
+    if (!int8_wait_warp<1>(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE)) return;
     ptx::tc_fence_after();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {   // 64 of K: 32 columns
@@ -264,17 +281,15 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
       for (int q = 0; q < 4; ++q) int8_to_half(v[4 * half + q], h + 8 * q);
       ptx::tmem_store_32cols(taddr0 + static_cast<uint32_t>(t.at * 64 + half * 32), h);
     }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bar.empty + 8 * r.at);   // every lane has its bytes
-#pragma unroll
-    for (int s = 0; s < Cfg::WSETS; ++s) r.next();
-    if (i + Cfg::WSETS < blocks && !read()) return;
     ptx::tmem_wait_stores();
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(bar.cv_full + 8 * t.at);
+    if (lane == 0) {
+      ptx::mbar_arrive(bar.cv_full + 8 * t.at);
+      ptx::mbar_arrive(bar.empty + 8 * r.at);
+    }
 #pragma unroll
-    for (int s = 0; s < Cfg::WSETS; ++s) t.next();
+    for (int s = 0; s < Cfg::WSETS; ++s) { r.next(); t.next(); }
   }
 }
 
@@ -350,7 +365,7 @@ __device__ __forceinline__ bool int8_exchange(const KernelParams& p, const Ctx& 
   const int lane = threadIdx.x & 31, channel = quad * 32 + lane;
   const int32_t size = static_cast<int32_t>(c.csize), rank = static_cast<int32_t>(c.rank);
   const int32_t slice = Cfg::NT / size, rows = w.row_end - w.row0 < Cfg::NT ? w.row_end - w.row0 : Cfg::NT;
-  if (!wait_phase_warp(p, c, bar.red_empty, phase ^ 1u, ROLE_EPILOGUE)) return false;
+  if (!int8_wait_warp<1>(p, c, bar.red_empty, phase ^ 1u, ROLE_EPILOGUE)) return false;
 #pragma unroll
   for (int i = 0; i < Cfg::NT; ++i)
     if (i < rows) {
@@ -360,7 +375,7 @@ __device__ __forceinline__ bool int8_exchange(const KernelParams& p, const Ctx& 
     }
   __syncwarp();
   if (lane < size) ptx::mbar_arrive_cluster(ptx::mapa(bar.red_full, lane));
-  if (!wait_phase_warp(p, c, bar.red_full, phase, ROLE_EPILOGUE)) return false;
+  if (!int8_wait_warp<1>(p, c, bar.red_full, phase, ROLE_EPILOGUE)) return false;
   ptx::mbar_try_wait_cluster(bar.red_full, phase);   // complete: the other CTAs' writes are visible
   const int32_t col = w.n * 128 + channel;
   const bool on = col < p.N;
@@ -394,6 +409,7 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
   const KRange k(p, c);
   uint32_t red_phase = 0;
   RingAt<Cfg::BUFS> acc0, acc1;   // the issuers'
+  uint32_t count = 0;             // k-blocks of the tiles before
   Tile w;
   while (walk.next_warp(w)) {
     RowScales<Cfg::NT> scale;
@@ -401,8 +417,8 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
     int32_t sum[Cfg::NT];
     bool first = true;
     for (int32_t i = 0; i < k.end - k.first; i += (i & 1) ? 2 * kInt8Fold - 1 : 1) {   // the first k-block of each accumulator
-      const int issuer = i & 1, at = issuer * Cfg::BUFS + (issuer ? acc1.at : acc0.at);
-      if (!wait_phase_warp(p, c, bar.acc_full + 8 * at, issuer ? acc1.phase : acc0.phase, ROLE_EPILOGUE)) return;
+      const int issuer = static_cast<int>((count + static_cast<uint32_t>(i)) & 1u), at = issuer * Cfg::BUFS + (issuer ? acc1.at : acc0.at);
+      if (!int8_wait_warp<1>(p, c, bar.acc_full + 8 * at, issuer ? acc1.phase : acc0.phase, ROLE_EPILOGUE)) return;
       ptx::tc_fence_after();
 #pragma unroll
       for (int q = 0; q < Cfg::NT; q += 16) {
@@ -421,6 +437,7 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
       if (issuer) acc1.next();
       else acc0.next();
     }
+    count += static_cast<uint32_t>(k.end - k.first);
     if constexpr (Cfg::SPLITS) {
       if (c.csize > 1) {
         if (!int8_exchange<Cfg, OUT>(p, c, w, quad, sum, scale, bar, red, red_phase)) return;

@@ -54,8 +54,9 @@ struct Int8WideBars {
         acc_empty(acc_full + 8 * Cfg::BUFS), drain(acc_empty + 8 * Cfg::BUFS) {}
 };
 
-// wait_phase for a pair's warp, which follows one verdict
-__device__ __forceinline__ bool wait_phase_pair_warp(const KernelParams& p, const Ctx& c, uint32_t bar, uint32_t parity, uint32_t role) {
+// wait_phase for a pair's warp, which follows one verdict (suspended waits, as in the kernel of single CTAs, cost 3 %
+// here, where few warps wait)
+__device__ __forceinline__ bool int8_wait_pair(const KernelParams& p, const Ctx& c, uint32_t bar, uint32_t parity, uint32_t role) {
   return __all_sync(0xFFFFFFFFu, wait_phase<2>(p, c, bar, parity, role));
 }
 
@@ -166,7 +167,7 @@ __device__ __forceinline__ void int8_wide_weights(const KernelParams& p, const C
   RingAt<Cfg::CV> t;
   while (walk.skip()) {
     for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
-      if (!wait_phase_pair_warp(p, c, bar.w_full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return;
+      if (!int8_wait_pair(p, c, bar.w_full + 8 * r.at, r.phase, ROLE_EPILOGUE)) return;
       const uint8_t* const src = src0 + r.at * Cfg::W_BYTES;
       uint4 v[4];
 #pragma unroll
@@ -183,7 +184,7 @@ __device__ __forceinline__ void int8_wide_weights(const KernelParams& p, const C
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar.w_empty + 8 * r.at);   // the bytes are in registers
         }
-        if (!wait_phase_pair_warp(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE)) return;
+        if (!int8_wait_pair(p, c, bar.cv_empty + 8 * t.at, t.phase ^ 1u, ROLE_EPILOGUE)) return;
         ptx::tc_fence_after();
         ptx::tmem_store_32cols(taddr0 + static_cast<uint32_t>(t.at * 32), f);
         ptx::tmem_wait_stores();
@@ -210,7 +211,7 @@ __device__ __forceinline__ void int8_wide_epilogue(const KernelParams& p, const 
     scale.load(p, w.row0 + half * HALF);
     int32_t sum[HALF];
     for (int32_t kb = 0; kb < p.sched.kt; kb += kInt8Fold) {
-      if (!wait_phase_pair_warp(p, c, bar.acc_full + 8 * acc.at, acc.phase, ROLE_EPILOGUE)) return;
+      if (!int8_wait_pair(p, c, bar.acc_full + 8 * acc.at, acc.phase, ROLE_EPILOGUE)) return;
       ptx::tc_fence_after();
 #pragma unroll
       for (int q = 0; q < HALF; q += 16) {
