@@ -593,26 +593,24 @@ typedef struct {
     int32_t relu;        /* 1: max(z, 0), a NaN stays */
     int32_t host_only;   /* 1: no GPU (the runs then fail with TST_ERR_NO_DEVICE); num_sms must be set */
     int32_t num_sms;     /* SMs to use: 0 = all */
-    int32_t tile_rows;   /* rows of A per tile: 0 = choose, else 16, 32, 64, 128, or 192 (CTA pairs) */
-    int32_t split;       /* CTAs that share a tile along K: 0 = choose, else 1, or 2, 4 or 8 (at most
-                            the 128-element k-blocks) with tile_rows of 16, 32 or 64.  No choice
-                            of tile or split changes a bit of D. */
+    int32_t tile_rows;   /* rows of A per tile: 0 = choose, else 16, 32, 64, 128, or 192 (CTA pairs), or 1:
+                            no tiles, for few rows (of each group).  No choice changes a bit of D. */
     int64_t timeout_ns;  /* limit of every device-side wait: 0 = 10 s */
 } tst_int8_options;
 
 typedef struct {
     int64_t M, N, K;
     int32_t groups;
-    int32_t tile_rows, tile_cols;   /* rows of A (tokens) and columns of D per tile */
-    int32_t split;                  /* CTAs that share a tile along K, 1, 2, 4 or 8 */
-    int32_t grid;                   /* CTAs launched */
+    int32_t tile_rows, tile_cols;   /* rows of A (tokens) and columns of D per tile; 1: no tiles */
+    int32_t grid;                   /* CTAs of tiles launched */
     int32_t smem_bytes;             /* dynamic shared memory per CTA */
-    int64_t workspace_bytes;        /* device bytes owned by the plan: with many tokens A in FP16, 2 M K */
+    int64_t workspace_bytes;        /* device bytes owned by the plan: A in FP16, 2 M K, but for tile_rows 1 */
 } tst_int8_plan_info;
 
 /* Errors: INVALID_ARG (null plan or opts, sizes < 1 or beyond int32, groups < 0, an out_dtype
  * other than the two, host_only without num_sms), ALIGNMENT (K not a multiple of 16),
- * UNSUPPORTED (a tile_rows or split other than those, 192 rows on one SM, M or groups * N beyond 2^31 - 256, K beyond 131056 (the 32-bit sums), more than
+ * UNSUPPORTED (a tile_rows other than those, 192 on one SM, 1 for more than
+ * 2^20 rows, M or groups * N beyond 2^31 - 256, K beyond 131056 (the 32-bit sums), more than
  * 512 groups, or a GPU other than sm_103), OOM, CUDA, NO_DEVICE. */
 tst_status gemm_int8_plan_create(tst_int8_plan **plan, int64_t M, int64_t N, int64_t K, const tst_int8_options *opts);
 tst_status gemm_int8_plan_get_info(const tst_int8_plan *plan, tst_int8_plan_info *info);

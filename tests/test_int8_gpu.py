@@ -48,17 +48,17 @@ SHAPES = [(1, 1, 16), (1, 128, 128), (2, 3, 48), (16, 130, 1024), (17, 129, 1040
           (64, 128, 4096), (65, 127, 1008), (128, 256, 1152), (129, 300, 4112), (256, 384, 512), (257, 1000, 8208), (700, 513, 3088)]
 
 
-# every form: rows per tile, CTAs that split a tile along K.  num_sms 16: each CTA (or pair) takes many tiles
-FORMS = [(0, 0), (16, 1), (16, 2), (16, 8), (32, 1), (32, 4), (64, 1), (64, 2), (64, 8), (128, 0), (192, 0)]
+# every form: rows per tile, 1 without tiles.  num_sms 16: each CTA (or pair) takes many tiles
+FORMS = [0, 1, 16, 32, 64, 128, 192]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
-@pytest.mark.parametrize("rows,split", FORMS)
+@pytest.mark.parametrize("rows", FORMS)
 @pytest.mark.parametrize("num_sms", [0, 16])
-def test_sums_are_exact(M, N, K, rows, split, num_sms):
+def test_sums_are_exact(M, N, K, rows, num_sms):
     A, B, _, _, _ = _operands(M + N + K, M, N, K, low=-128)
-    plan = tst.gemm_int8_plan_create(M, N, K, out_dtype="f32", num_sms=num_sms, tile_rows=rows, split=split)
-    assert rows in (0, plan.info.tile_rows) and plan.info.split <= max(split, 1 if rows else 8)
+    plan = tst.gemm_int8_plan_create(M, N, K, out_dtype="f32", num_sms=num_sms, tile_rows=rows)
+    assert rows in (0, plan.info.tile_rows)
     D = _run(plan, A, B, np.ones(M, np.float32), np.ones(N, np.float32))
     assert tst.gemm_int8_status_query(plan) == tst.TST_OK
     assert np.array_equal(D.cpu().numpy(), int8.sums(A, B).astype(np.float32))
@@ -66,12 +66,12 @@ def test_sums_are_exact(M, N, K, rows, split, num_sms):
 
 @pytest.mark.parametrize("M,N,K", [(3, 5, 1024), (20, 140, 8192), (130, 260, 1040), (2, 3, 131056), (300, 260, 16384)])
 @pytest.mark.parametrize("a,b", [(-128, -128), (-128, 127), (127, 127)])
-@pytest.mark.parametrize("rows,split", [(0, 0), (16, 4), (64, 1), (128, 0), (192, 0)])
-def test_largest_magnitudes(M, N, K, a, b, rows, split):
+@pytest.mark.parametrize("rows", FORMS)
+def test_largest_magnitudes(M, N, K, a, b, rows):
     # every partial sum as large as it can be: 2^24 per accumulator, close to 2^31 over the longest K
     A, B = np.full((M, K), a, np.int8), np.full((N, K), b, np.int8)
     A[0, ::7], B[0, 1::5] = 1, -1   # and sums that are no multiple of a power of two
-    plan = tst.gemm_int8_plan_create(M, N, K, out_dtype="f32", tile_rows=rows, split=split)
+    plan = tst.gemm_int8_plan_create(M, N, K, out_dtype="f32", tile_rows=rows)
     D = _run(plan, A, B, np.ones(M, np.float32), np.ones(N, np.float32))
     assert np.array_equal(D.cpu().numpy(), int8.sums(A, B).astype(np.float32))
 
@@ -80,14 +80,14 @@ def test_largest_magnitudes(M, N, K, a, b, rows, split):
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_scales_bias_relu(M, N, K, out):
     A, B, ra, cb, bias = _operands(7 * M + N, M, N, K)
-    for use_bias, relu, rows, split in ((False, False, 0, 0), (True, True, 16, 1), (True, False, 32, 2), (True, True, 64, 1), (True, False, 128, 0),
-                                        (True, True, 192, 0)):
-        plan = tst.gemm_int8_plan_create(M, N, K, out_dtype=out, has_bias=use_bias, relu=relu, tile_rows=rows, split=split)
+    for use_bias, relu, rows in ((False, False, 0), (True, True, 1), (True, True, 16), (True, False, 32), (True, True, 64), (True, False, 128),
+                                 (True, True, 192)):
+        plan = tst.gemm_int8_plan_create(M, N, K, out_dtype=out, has_bias=use_bias, relu=relu, tile_rows=rows)
         D = _run(plan, A, B, ra, cb, bias if use_bias else None)
         _check(D, *int8.gemm(A, B, ra, cb, bias if use_bias else None, relu))
 
 
-GROUPS = [("one", 1, 5, 130, 272, [5]), ("split over K", 3, 40, 384, 4112, [7, 0, 33]), ("empty first and last", 5, 40, 200, 1040, [0, 17, 0, 23, 0]),
+GROUPS = [("one", 1, 5, 130, 272, [5]), ("long K", 3, 40, 384, 4112, [7, 0, 33]), ("empty first and last", 5, 40, 200, 1040, [0, 17, 0, 23, 0]),
           ("one row each", 60, 60, 96, 144, [1] * 60), ("uneven", 7, 333, 257, 2064, [1, 200, 0, 33, 64, 32, 3]),
           ("many", 300, 700, 130, 128, [(i * 7) % 5 for i in range(300)]), ("large", 3, 1500, 384, 1536, [129, 1000, 371]), ("large with rows to spare", 4, 1700, 300, 1040, [0, 600, 1, 500]),
           ("none", 4, 9, 64, 64, [0, 0, 0, 0])]
@@ -95,10 +95,11 @@ GROUPS = [("one", 1, 5, 130, 272, [5]), ("split over K", 3, 40, 384, 4112, [7, 0
 
 @pytest.mark.parametrize("name,G,M,N,K,rows", GROUPS, ids=[g[0] for g in GROUPS])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-@pytest.mark.parametrize("tile,split,num_sms", [(t, s, 0) for t, s in FORMS] + [(16, 2, 16), (32, 1, 16), (64, 8, 16), (128, 0, 16), (192, 0, 16)])
-def test_grouped(name, G, M, N, K, rows, out, tile, split, num_sms):
+@pytest.mark.parametrize("tile", FORMS)
+@pytest.mark.parametrize("num_sms", [0, 16])
+def test_grouped(name, G, M, N, K, rows, out, tile, num_sms):
     A, B, ra, cb, bias = _operands(G + M, M, N, K, parts=G)
-    plan = tst.gemm_int8_plan_create(M, N, K, groups=G, out_dtype=out, has_bias=True, num_sms=num_sms, tile_rows=tile, split=split)
+    plan = tst.gemm_int8_plan_create(M, N, K, groups=G, out_dtype=out, has_bias=True, num_sms=num_sms, tile_rows=tile)
     D = _run(plan, A, B, ra, cb, bias, rows, fill=-77.0)
     assert tst.gemm_int8_status_query(plan) == tst.TST_OK
     used = sum(rows)
@@ -107,11 +108,11 @@ def test_grouped(name, G, M, N, K, rows, out, tile, split, num_sms):
     _check(D[:used], want, size)
 
 
-@pytest.mark.parametrize("scale,rows,split", [(1, 0, 0), (1, 16, 1), (1, 32, 1), (10, 64, 1), (10, 128, 0), (10, 192, 0)])
-def test_rows_past_the_matrix_are_reported(scale, rows, split):
+@pytest.mark.parametrize("scale,rows", [(1, 0), (1, 1), (1, 16), (1, 32), (10, 64), (10, 128), (10, 192)])
+def test_rows_past_the_matrix_are_reported(scale, rows):
     M = 100 * scale
     A, B, ra, cb, _ = _operands(3, M, 64, 128, parts=3)
-    plan = tst.gemm_int8_plan_create(M, 64, 128, groups=3, out_dtype="f32", tile_rows=rows, split=split)
+    plan = tst.gemm_int8_plan_create(M, 64, 128, groups=3, out_dtype="f32", tile_rows=rows)
     D = _run(plan, A, B, ra, cb, None, [60 * scale, -4, 70 * scale])
     assert tst.gemm_int8_status_query(plan) == tst.TST_ERR_DEVICE_CHECK
     assert tst.gemm_int8_status_query(plan) == tst.TST_OK   # reported once
@@ -126,13 +127,13 @@ def test_scales_that_are_not_numbers_stay_visible():
     assert np.isnan(D[1]).all() and np.isnan(D[:, 3]).all() and np.isfinite(D[0, 4:]).all()
 
 
-@pytest.mark.parametrize("scale,tile,split", [(1, 0, 0), (1, 16, 8), (1, 32, 1), (1, 64, 2), (10, 64, 1), (10, 128, 0), (10, 192, 0)])
-def test_streams_and_graphs(scale, tile, split):
+@pytest.mark.parametrize("scale,tile", [(1, 0), (1, 1), (1, 16), (1, 32), (10, 64), (10, 128), (10, 192)])
+def test_streams_and_graphs(scale, tile):
     # a plan on another stream, and captured: the replay reads what its inputs hold then
     G, M, N, K = 4, 90 * scale, 192, 1168
     A, B, ra, cb, bias = _operands(9, M, N, K, parts=G)
     A2 = _operands(10, M, N, K)[0]
-    plan = tst.gemm_int8_plan_create(M, N, K, groups=G, out_dtype="f32", has_bias=True, tile_rows=tile, split=split)
+    plan = tst.gemm_int8_plan_create(M, N, K, groups=G, out_dtype="f32", has_bias=True, tile_rows=tile)
     first, second = ([n * scale for n in rows] for rows in ([10, 0, 50, 30], [40, 41, 0, 9]))
     a, b, r, c, bs = (_dev(x) for x in (A, B, ra, cb, bias))
     rows = torch.tensor(first, dtype=torch.int32, device="cuda")

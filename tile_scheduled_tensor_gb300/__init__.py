@@ -406,14 +406,14 @@ class Int8Plan:
 
 def gemm_int8_plan_create(M: int, N: int, K: int, groups: int = 0, out_dtype="bf16", has_bias: bool = False,
                           relu: bool = False, host_only: bool = False, num_sms: int = 0, tile_rows: int = 0,
-                          split: int = 0, timeout_ns: int = 0) -> Int8Plan:
+                          timeout_ns: int = 0) -> Int8Plan:
     """Plan D = relu?(row_scale * col_scale * (A x B) + bias) of int8 A (M x K) and B (N x K), the integer
     sum exact.  groups > 0: that many GEMMs sharing N and K, A and D holding the groups' rows one after
-    another (at most M), B, col_scale and bias one part per group.  tile_rows, split: the tile's rows of A and
-    the CTAs that share its K (0: the plan chooses; the results are the same)."""
+    another (at most M), B, col_scale and bias one part per group.  tile_rows: the tile's rows of A (0: the plan
+    chooses; the results are the same)."""
     out = _enum(_OUT, out_dtype, "out_dtype")
     opts = _capi.tst_int8_options(int(groups), out, int(bool(has_bias)), int(bool(relu)), int(bool(host_only)),
-                                  int(num_sms), int(tile_rows), int(split), int(timeout_ns))
+                                  int(num_sms), int(tile_rows), int(timeout_ns))
     h = ctypes.c_void_p()
     _check(lib.gemm_int8_plan_create(ctypes.byref(h), int(M), int(N), int(K), ctypes.byref(opts)),
            "gemm_int8_plan_create")

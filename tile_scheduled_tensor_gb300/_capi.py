@@ -108,12 +108,12 @@ class tst_moe_score_options(ctypes.Structure):
 
 class tst_int8_options(ctypes.Structure):
     _fields_ = [("groups", _I32), ("out_dtype", _I32), ("has_bias", _I32), ("relu", _I32), ("host_only", _I32),
-                ("num_sms", _I32), ("tile_rows", _I32), ("split", _I32), ("timeout_ns", _I64)]
+                ("num_sms", _I32), ("tile_rows", _I32), ("timeout_ns", _I64)]
 
 
 class tst_int8_plan_info(ctypes.Structure):
     _fields_ = [("M", _I64), ("N", _I64), ("K", _I64), ("groups", _I32), ("tile_rows", _I32), ("tile_cols", _I32),
-                ("split", _I32), ("grid", _I32), ("smem_bytes", _I32), ("workspace_bytes", _I64)]
+                ("grid", _I32), ("smem_bytes", _I32), ("workspace_bytes", _I64)]
 
 
 _SIGNATURES = {

@@ -33,9 +33,6 @@
 //   the others  weights: a thread per channel, 128 bytes -> 64 columns of Tensor Memory.  One k-block
 //               takes a warpgroup 800 to 1000 cycles, most of them latencies, where its 16 KB come in
 //               700 at the copy rate: four warpgroups (of 128 tokens: two) take k-blocks in turn
-// Where the tiles do not fill the SMs, a cluster of 2, 4 or 8 CTAs shares a tile, each taking a part of K.
-// Each CTA then finishes a slice of the tile's tokens: the others write their integer sums of it into its
-// shared memory.  Sums of integers are the same in any order, so a split changes no bit of D.
 // Every wait is bounded as in the other kernels.
 #pragma once
 #include "gemm_bs_tile.cuh"
@@ -44,11 +41,9 @@ namespace tst {
 
 constexpr int kInt8Fold = 8;   // k-blocks of 128 per accumulator: 1024 products of at most 2^14
 
-// SPLITS: a cluster of CTAs shares each tile along K.
-template <int NT_, bool SPLITS_>
+template <int NT_>
 struct Int8Cfg {
   static constexpr int NT = NT_;
-  static constexpr bool SPLITS = SPLITS_;
   static constexpr int WSETS = NT == 128 ? 2 : 4;          // warpgroups that convert weights, k-blocks in turn
   static constexpr int THREADS = 256 + 128 * WSETS;
   static constexpr int W_BYTES = 128 * 128;
@@ -57,19 +52,17 @@ struct Int8Cfg {
   static constexpr int BUFS = NT >= 64 ? 1 : 2;            // accumulators per issuer
   static constexpr int A_COL = 2 * BUFS * NT;              // first TMEM column of the weights
   static constexpr int CV = (512 - A_COL) / 128 * 2;       // converted k-blocks of weights: 64 TMEM columns each
-  static constexpr int XS = NT <= 64 ? 6 : 4;              // k-blocks of tokens
-  static constexpr int RED_BYTES = SPLITS ? NT * 128 * 4 : 0;   // the cluster's sums of this CTA's slice
-  static constexpr int FIXED = 1024 + XS * X_BYTES + RED_BYTES + kWalkBytes + 512;
+  static constexpr int XS = NT <= 32 ? 6 : 4;              // k-blocks of tokens
+  static constexpr int FIXED = 1024 + XS * X_BYTES + kWalkBytes + 512;
   // A warpgroup that converts weights meets every WSETS-th k-block alone, an issuer every second one, and
   // loads land and warpgroups finish in any order.  A wait tells a phase only from the one before it, so a
   // stage is always the same warpgroup's (STAGES a multiple of WSETS) and the same issuer's (CV and XS even),
   // and so many converted k-blocks are there that the one two turns ago is used up (CV >= WSETS).
   static constexpr int STAGES = (kSmemLimit - FIXED) / W_BYTES / WSETS * WSETS;
   static constexpr int X_OFFSET = STAGES * W_BYTES;
-  static constexpr int RED_OFFSET = X_OFFSET + XS * X_BYTES;
-  static constexpr int WALK_OFFSET = RED_OFFSET + RED_BYTES;
+  static constexpr int WALK_OFFSET = X_OFFSET + XS * X_BYTES;
   static constexpr int BAR_OFFSET = (WALK_OFFSET + kWalkBytes + 7) / 8 * 8;
-  static constexpr int BARS = 2 * STAGES + 2 * CV + 2 * XS + 4 * BUFS + 3;
+  static constexpr int BARS = 2 * STAGES + 2 * CV + 2 * XS + 4 * BUFS + 1;
   static constexpr int MISC_OFFSET = BAR_OFFSET + BARS * 8;
   static constexpr int SMEM_BYTES = 1024 + MISC_OFFSET + 16;
   static_assert(X_ATOM % 1024 == 0, "swizzled tiles start on 1024 bytes");
@@ -101,19 +94,11 @@ struct OutOf<OUT_BF16> { using T = __nv_bfloat16; };
 // The shared addresses of the barriers: byte ring, converted k-blocks, tokens, each issuer's accumulators.
 template <class Cfg>
 struct Int8Bars {
-  uint32_t full, empty, cv_full, cv_empty, x_full, x_empty, acc_full, acc_empty, drain, red_full, red_empty;
+  uint32_t full, empty, cv_full, cv_empty, x_full, x_empty, acc_full, acc_empty, drain;
   __device__ __forceinline__ explicit Int8Bars(uint32_t base)
       : full(base), empty(full + 8 * Cfg::STAGES), cv_full(empty + 8 * Cfg::STAGES), cv_empty(cv_full + 8 * Cfg::CV),
         x_full(cv_empty + 8 * Cfg::CV), x_empty(x_full + 8 * Cfg::XS), acc_full(x_empty + 8 * Cfg::XS),
-        acc_empty(acc_full + 16 * Cfg::BUFS), drain(acc_empty + 16 * Cfg::BUFS), red_full(drain + 8), red_empty(red_full + 8) {}
-};
-
-// this CTA's k-blocks: all, or its part of a split tile's
-struct KRange {
-  int32_t first, end;
-  __device__ __forceinline__ KRange(const KernelParams& p, const Ctx& c)
-      : first(p.sched.kt * static_cast<int32_t>(c.rank) / static_cast<int32_t>(c.csize)),
-        end(p.sched.kt * static_cast<int32_t>(c.rank + 1) / static_cast<int32_t>(c.csize)) {}
+        acc_empty(acc_full + 16 * Cfg::BUFS), drain(acc_empty + 16 * Cfg::BUFS) {}
 };
 
 // wait_phase with the waiting thread suspended.  Many warps wait here beside those that work, and tries that
@@ -160,15 +145,14 @@ __device__ __forceinline__ void int8_land(const KernelParams& p, uint32_t full, 
 
 template <class Cfg>
 __device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& c, Walk walk, uint32_t smem, const Int8Bars<Cfg>& bar) {
-  const KRange k(p, c);
   RingAt<Cfg::STAGES> r;
   uint32_t issued = 0, issued_parity = 0;
   bool ok = true;
   Tile w;
   while (ok && walk.next(w)) {
-    if (w.clamped && c.rank == 0) record_status(p, ST_DEVICE_CHECK, ROLE_PRODUCER);
+    if (w.clamped) record_status(p, ST_DEVICE_CHECK, ROLE_PRODUCER);
     const int32_t b_row0 = w.group * p.sched.group_b_rows + w.n * 128;
-    for (int32_t kb = k.first; kb < k.end; ++kb) {
+    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
       if (!int8_wait<1>(p, c, bar.empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
       const uint32_t full = bar.full + 8 * r.at, dst = smem + r.at * Cfg::W_BYTES;
       ptx::mbar_arrive_expect_tx(full, Cfg::W_BYTES);
@@ -184,14 +168,13 @@ __device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& 
 // NT rows of two 64-element atoms per k-block.
 template <class Cfg>
 __device__ __forceinline__ void int8_token_loads(const KernelParams& p, const Ctx& c, Walk walk, uint32_t xs, const Int8Bars<Cfg>& bar) {
-  const KRange k(p, c);
   RingAt<Cfg::XS> r;
   uint32_t issued = 0, issued_parity = 0;
   bool ok = true;
   Tile w;
   ptx::griddep_wait();   // they are the kernel's before
   while (ok && walk.next(w)) {
-    for (int32_t kb = k.first; kb < k.end; ++kb) {
+    for (int32_t kb = 0; kb < p.sched.kt; ++kb) {
       if (!int8_wait<1>(p, c, bar.x_empty + 8 * r.at, r.phase ^ 1u, ROLE_PRODUCER)) { ok = false; break; }
       const uint32_t full = bar.x_full + 8 * r.at, dst = xs + r.at * Cfg::X_BYTES;
       ptx::mbar_arrive_expect_tx(full, Cfg::X_BYTES);
@@ -211,8 +194,7 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
                                          const Int8Bars<Cfg>& bar) {
   const uint32_t idesc = ptx::make_idesc(0u, 128, Cfg::NT);   // FP16 operands
   const uint64_t x_desc0 = ptx::sw128_kmajor_desc(xs);
-  const KRange k(p, c);
-  const int32_t blocks = k.end - k.first;
+  const int32_t blocks = p.sched.kt;
   const uint32_t acc_full = bar.acc_full + 8 * Cfg::BUFS * issuer, acc_empty = bar.acc_empty + 8 * Cfg::BUFS * issuer;
   RingAt<Cfg::CV> r;
   RingAt<Cfg::XS> x;
@@ -260,9 +242,8 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
   const uint8_t* const src0 = smem + (quad * 32 + lane) * 128;
   const int sub = lane & 7;
   const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + Cfg::A_COL;
-  const KRange k(p, c);
   int64_t blocks = 0;   // k-blocks of this CTA
-  while (walk.skip()) blocks += k.end - k.first;
+  while (walk.skip()) blocks += p.sched.kt;
   RingAt<Cfg::STAGES> r;
   RingAt<Cfg::CV> t;
   for (int i = 0; i < set; ++i) { r.next(); t.next(); }
@@ -281,13 +262,12 @@ __device__ __forceinline__ void int8_weights(const KernelParams& p, const Ctx& c
       for (int q = 0; q < 4; ++q) int8_to_half(v[4 * half + q], h + 8 * q);
       ptx::tmem_store_32cols(taddr0 + static_cast<uint32_t>(t.at * 64 + half * 32), h);
     }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar.empty + 8 * r.at);   // every lane has its bytes
     ptx::tmem_wait_stores();
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) {
-      ptx::mbar_arrive(bar.cv_full + 8 * t.at);
-      ptx::mbar_arrive(bar.empty + 8 * r.at);
-    }
+    if (lane == 0) ptx::mbar_arrive(bar.cv_full + 8 * t.at);
 #pragma unroll
     for (int s = 0; s < Cfg::WSETS; ++s) { r.next(); t.next(); }
   }
@@ -357,57 +337,10 @@ __device__ __forceinline__ void int8_store(const KernelParams& p, const Tile& w,
   }
 }
 
-// A split tile: this CTA's sums go to the CTAs that finish their rows, and it finishes its own slice of
-// NT / csize rows from what the cluster has written here.  red: csize x slice x 128 sums.
 template <class Cfg, int OUT>
-__device__ __forceinline__ bool int8_exchange(const KernelParams& p, const Ctx& c, const Tile& w, int quad, int32_t (&sum)[Cfg::NT],
-                                              const RowScales<Cfg::NT>& scale, const Int8Bars<Cfg>& bar, uint32_t red, uint32_t phase) {
-  const int lane = threadIdx.x & 31, channel = quad * 32 + lane;
-  const int32_t size = static_cast<int32_t>(c.csize), rank = static_cast<int32_t>(c.rank);
-  const int32_t slice = Cfg::NT / size, rows = w.row_end - w.row0 < Cfg::NT ? w.row_end - w.row0 : Cfg::NT;
-  if (!int8_wait_warp<1>(p, c, bar.red_empty, phase ^ 1u, ROLE_EPILOGUE)) return false;
-#pragma unroll
-  for (int i = 0; i < Cfg::NT; ++i)
-    if (i < rows) {
-      const int32_t to = i / slice;
-      ptx::st_cluster_u32(ptx::mapa(red + static_cast<uint32_t>(((rank * slice + i - to * slice) * 128 + channel) * 4), to),
-                          static_cast<uint32_t>(sum[i]));
-    }
-  __syncwarp();
-  if (lane < size) ptx::mbar_arrive_cluster(ptx::mapa(bar.red_full, lane));
-  if (!int8_wait_warp<1>(p, c, bar.red_full, phase, ROLE_EPILOGUE)) return false;
-  ptx::mbar_try_wait_cluster(bar.red_full, phase);   // complete: the other CTAs' writes are visible
-  const int32_t col = w.n * 128 + channel;
-  const bool on = col < p.N;
-  const int64_t at = static_cast<int64_t>(w.group) * p.N + (on ? col : 0);
-  const float cb = __ldg(p.ext.col_scale + at);
-  const float b = p.has_bias ? __ldg(p.bias + at) : 0.0f;
-  using Out = typename OutOf<OUT>::T;
-  for (int32_t i = 0; i < slice; ++i) {
-    const int32_t row = rank * slice + i;
-    if (row >= rows) break;
-    int32_t s = 0;
-    for (int32_t q = 0; q < size; ++q) s += static_cast<int32_t>(ptx::ld_shared_u32(red + static_cast<uint32_t>(((q * slice + i) * 128 + channel) * 4)));
-    float ra = scale.v[0];
-#pragma unroll
-    for (int v = 1; v < RowScales<Cfg::NT>::V; ++v) ra = (row >> 5) == v ? scale.v[v] : ra;
-    ra = __shfl_sync(0xFFFFFFFFu, ra, row & 31);
-    float z = fmaf(__int2float_rn(s) * ra, cb, b);
-    if (p.relu) z = relu_nan(z);
-    if (on) static_cast<Out*>(p.C)[static_cast<int64_t>(w.row0 + row) * p.N + col] = static_cast<Out>(z);
-  }
-  __syncwarp();
-  if (lane < size) ptx::mbar_arrive_cluster(ptx::mapa(bar.red_empty, lane));   // read: the next tile's may come
-  return true;
-}
-
-template <class Cfg, int OUT>
-__device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, uint32_t red,
-                                              const Int8Bars<Cfg>& bar) {
+__device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& c, Walk walk, uint32_t tmem_base, const Int8Bars<Cfg>& bar) {
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-  const KRange k(p, c);
-  uint32_t red_phase = 0;
   RingAt<Cfg::BUFS> acc0, acc1;   // the issuers'
   uint32_t count = 0;             // k-blocks of the tiles before
   Tile w;
@@ -416,7 +349,7 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
     scale.load(p, w.row0);
     int32_t sum[Cfg::NT];
     bool first = true;
-    for (int32_t i = 0; i < k.end - k.first; i += (i & 1) ? 2 * kInt8Fold - 1 : 1) {   // the first k-block of each accumulator
+    for (int32_t i = 0; i < p.sched.kt; i += (i & 1) ? 2 * kInt8Fold - 1 : 1) {   // the first k-block of each accumulator
       const int issuer = static_cast<int>((count + static_cast<uint32_t>(i)) & 1u), at = issuer * Cfg::BUFS + (issuer ? acc1.at : acc0.at);
       if (!int8_wait_warp<1>(p, c, bar.acc_full + 8 * at, issuer ? acc1.phase : acc0.phase, ROLE_EPILOGUE)) return;
       ptx::tc_fence_after();
@@ -437,14 +370,7 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
       if (issuer) acc1.next();
       else acc0.next();
     }
-    count += static_cast<uint32_t>(k.end - k.first);
-    if constexpr (Cfg::SPLITS) {
-      if (c.csize > 1) {
-        if (!int8_exchange<Cfg, OUT>(p, c, w, quad, sum, scale, bar, red, red_phase)) return;
-        red_phase ^= 1u;
-        continue;
-      }
-    }
+    count += static_cast<uint32_t>(p.sched.kt);
     int8_store<Cfg::NT, OUT>(p, w, w.row0, w.n * 128 + quad * 32 + lane, sum, scale);
   }
 }
@@ -452,7 +378,6 @@ __device__ __forceinline__ void int8_epilogue(const KernelParams& p, const Ctx& 
 template <class Cfg, int OUT>
 __global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid_constant__ KernelParams p) {
   extern __shared__ uint8_t smem_raw[];
-  // the same offset in every CTA of a cluster: the window's start is
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = ptx::smem_addr(smem);
   const Int8Bars<Cfg> bar(base + Cfg::BAR_OFFSET);
@@ -462,11 +387,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid
   Ctx c;
   c.abort = &ctl->abort;
   c.abort_addr = ptx::smem_addr(&ctl->abort);
-  c.csize = Cfg::SPLITS ? static_cast<uint32_t>(p.sk_slots) : 1u;
-  c.rank = c.csize > 1 ? ptx::cluster_ctarank() : 0u;
+  c.rank = 0;
   c.rank_m = 0;
   c.rank_n = 0;
-  c.unit = static_cast<int32_t>(blockIdx.x / c.csize);
+  c.csize = 1;
+  c.unit = static_cast<int32_t>(blockIdx.x);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
@@ -486,8 +411,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid
       ptx::mbar_init(bar.acc_empty + 8 * b, 4);
     }
     ptx::mbar_init(bar.drain, 2);                 // both issuers
-    ptx::mbar_init(bar.red_full, 4 * c.csize);    // the summing warps of the cluster
-    ptx::mbar_init(bar.red_empty, 4 * c.csize);
     ctl->abort = 0;
     ctl->ep_ok = 0;
     ptx::fence_mbar_init();
@@ -502,7 +425,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid
   if (warp == 2) fill_group_table(p.sched, table);
   ptx::tc_fence_before();
   __syncthreads();
-  if (c.csize > 1) ptx::cluster_sync();   // the other CTAs' barriers exist before anyone signals them
   ptx::tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
   const Walk walk(p.sched, table, c.unit);
@@ -522,12 +444,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) gemm_int8_kernel(const __grid
     int8_weights<Cfg>(p, c, walk, tmem_base, smem, warp < 8 ? 0 : (warp >> 2) - 2, bar);
   } else {
     ptx::setmaxnreg_inc<Cfg::SUM_REGS>();
-    int8_epilogue<Cfg, OUT>(p, c, walk, tmem_base, base + Cfg::RED_OFFSET, bar);
+    int8_epilogue<Cfg, OUT>(p, c, walk, tmem_base, bar);
   }
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (c.csize > 1) ptx::cluster_sync();   // no CTA leaves while another may still write its shared memory
   if (warp == 1) {
     __syncwarp();
     ptx::tc_fence_after();

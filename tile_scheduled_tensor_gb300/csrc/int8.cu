@@ -13,11 +13,10 @@
 struct tst_int8_plan {
   int64_t M = 0, N = 0, K = 0;
   tst_int8_options opts{};
-  int32_t tokens = 0;          // rows of A per tile
+  int32_t tokens = 0;          // rows of A per tile; kFewTokens: no tiles
   int32_t num_sms = 0, device = -1;
   TstInt8Kernel kernel{};
   bool pairs = false;          // the wide form
-  int32_t split = 1;           // CTAs that share a tile along K
   tst::Sched sched{};
   unsigned long long* d_status = nullptr;   // 256 bytes, then A in FP16
   size_t dev_bytes = 0;
@@ -31,6 +30,9 @@ namespace {
 constexpr uint32_t kStatusTag = 1;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 256;   // the last tile's rows and columns are 32-bit, past the matrix too
 constexpr int64_t kMaxK = 131056;                        // 131071 products of up to 2^14 fit 32 bits; K is a multiple of 16
+
+constexpr int32_t kFewTokens = 1;                        // tile_rows of the form without tiles
+constexpr int64_t kMaxFewRows = 1 << 20;                 // 16 to a block
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -62,10 +64,10 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   if (opts->groups < 0 || opts->num_sms < 0 || opts->timeout_ns < 0) return TST_ERR_INVALID_ARG;
   if (opts->out_dtype != TST_OUT_F32 && opts->out_dtype != TST_OUT_BF16) return TST_ERR_INVALID_ARG;
   if (opts->host_only && opts->num_sms == 0) return TST_ERR_INVALID_ARG;
-  const int32_t tr = opts->tile_rows, sp = opts->split;
-  if (tr < 0 || sp < 0) return TST_ERR_INVALID_ARG;
-  if ((tr != 0 && tr != 16 && tr != 32 && tr != 64 && tr != 128 && tr != kInt8WideTokens) || (sp != 0 && sp != 1 && sp != 2 && sp != 4 && sp != 8) ||
-      (sp > 1 && (tr == 0 || tr > kInt8SplitTokens)) || (tr == kInt8WideTokens && opts->num_sms == 1))
+  const int32_t tr = opts->tile_rows;
+  if (tr < 0) return TST_ERR_INVALID_ARG;
+  if ((tr != 0 && tr != kFewTokens && tr != 16 && tr != 32 && tr != 64 && tr != 128 && tr != kInt8WideTokens) ||
+      (tr == kInt8WideTokens && opts->num_sms == 1) || (tr == kFewTokens && M > kMaxFewRows))
     return TST_ERR_UNSUPPORTED;
   if (K % 16 != 0) return TST_ERR_ALIGNMENT;   // a row of K bytes is a row of the tensor map
   const int64_t groups = opts->groups;
@@ -93,7 +95,7 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
     p->device = dev;
     p->num_sms = opts->num_sms > 0 ? std::min(opts->num_sms, sms) : sms;
   }
-  const int32_t tokens = opts->tile_rows > 0 ? opts->tile_rows : tile_tokens(ceil_div(M, std::max<int64_t>(groups, 1)), M, N, p->num_sms);
+  const int32_t tokens = tr > 0 ? tr : tile_tokens(ceil_div(M, std::max<int64_t>(groups, 1)), M, N, p->num_sms);
   p->tokens = tokens;
   p->pairs = tokens == kInt8WideTokens;
   const bool pairs = p->pairs;
@@ -101,19 +103,12 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   const int64_t mt = ceil_div(M, tokens), nt = ceil_div(N, cols);
   const int64_t tiles = (mt + groups) * nt;   // grouped: at most, whatever the split
   if (tiles >= (int64_t(1) << 30)) { delete p; return TST_ERR_UNSUPPORTED; }
-  // a tile's K over as many CTAs as are left idle, each with two k-blocks or more
   const int64_t kt = ceil_div(K, 128);
-  const int out_type = opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32;
-  if (opts->split > 0) {
-    p->split = static_cast<int32_t>(std::min<int64_t>(opts->split, kt));
-    while (p->split & (p->split - 1)) --p->split;
-  }
-  while (opts->split == 0 && tokens <= kInt8SplitTokens && p->split < 8 && 2 * p->split * tiles <= p->num_sms && kt >= 4 * p->split) p->split *= 2;
-  p->kernel = tst_int8_kernel(tokens, out_type, p->split > 1);
-  const int32_t ctas = pairs ? 2 : p->split;   // of a cluster
-  p->dev_bytes = 256 + 2 * static_cast<size_t>(M) * K;
+  const bool few = tokens == kFewTokens;
+  if (!few) p->kernel = tst_int8_kernel(tokens, opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32);
+  p->dev_bytes = 256 + (few ? 0 : 2 * static_cast<size_t>(M) * K);
   if (!opts->host_only) {
-    if (cudaFuncSetAttribute(p->kernel.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p->kernel.smem_bytes) != cudaSuccess) {
+    if (!few && cudaFuncSetAttribute(p->kernel.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p->kernel.smem_bytes) != cudaSuccess) {
       cudaGetLastError();
       delete p;
       return TST_ERR_CUDA;
@@ -137,7 +132,7 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   s.map_kind = tst::MAP_GROUPED_M;
   s.group = 8;
   s.dp_tiles = static_cast<int32_t>(mt * nt);
-  s.grid = static_cast<int32_t>(std::min<int64_t>(p->num_sms / ctas, tiles));
+  s.grid = static_cast<int32_t>(std::min<int64_t>(p->num_sms / (pairs ? 2 : 1), tiles));
   if (s.grid < 1) s.grid = 1;
   s.sk_groups = 1;
   s.rows = static_cast<int32_t>(M);
@@ -166,8 +161,7 @@ tst_status gemm_int8_plan_get_info(const tst_int8_plan* p, tst_int8_plan_info* i
   info->groups = p->sched.groups;
   info->tile_rows = p->tokens;
   info->tile_cols = p->sched.bn;
-  info->grid = p->sched.grid * (p->pairs ? 2 : p->split);
-  info->split = p->split;
+  info->grid = p->sched.grid * (p->pairs ? 2 : 1);
   info->smem_bytes = p->kernel.smem_bytes;
   info->workspace_bytes = static_cast<int64_t>(p->dev_bytes);
   return TST_OK;
@@ -204,11 +198,7 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
   tst::KernelParams kp = {};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool pairs = p->pairs;
-  const int32_t ctas = pairs ? 2 : p->split;   // of a cluster
   void* const half = p->d_status + 32;
-  if (!tst_encode_halves(&kp.tmap_a, half, p->M, p->K, pairs ? p->tokens / 2 : p->tokens) ||
-      !tst_encode_bytes(&kp.tmap_b, B, std::max<int64_t>(p->sched.groups, 1) * p->N, p->K, 128))
-    return TST_ERR_CUDA;
   kp.C = D;
   kp.bias = p->opts.has_bias ? bias : nullptr;
   kp.has_bias = p->opts.has_bias ? 1 : 0;
@@ -222,19 +212,25 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
   kp.K = static_cast<int32_t>(p->K);
   kp.sched = p->sched;
   kp.sched.group_rows = group_rows;
-  kp.sk_slots = p->split;
   kp.tma_store = aligned(D, 4) && p->N % 2 == 0;   // BF16 rows of whole words
   kp.timeout_ns = p->opts.timeout_ns > 0 ? static_cast<uint64_t>(p->opts.timeout_ns) : 10ull * 1000 * 1000 * 1000;
+  p->last_stream = s;
+  p->ran = true;
+  if (p->tokens == kFewTokens)
+    return tst_int8_few(kp, A, B, p->opts.out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32, s) ? TST_OK : TST_ERR_CUDA;
+  if (!tst_encode_halves(&kp.tmap_a, half, p->M, p->K, pairs ? p->tokens / 2 : p->tokens) ||
+      !tst_encode_bytes(&kp.tmap_b, B, std::max<int64_t>(p->sched.groups, 1) * p->N, p->K, 128))
+    return TST_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p->sched.grid * ctas), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p->sched.grid * (pairs ? 2 : 1)), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(p->kernel.threads), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(p->kernel.smem_bytes);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   unsigned na = 0;
-  if (ctas > 1) {
+  if (pairs) {
     attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[na].val.clusterDim.x = 2;
     attr[na].val.clusterDim.y = 1;
     attr[na].val.clusterDim.z = 1;
     ++na;
@@ -251,8 +247,6 @@ tst_status gemm_int8_run(tst_int8_plan* p, const int32_t* group_rows, const int8
     cudaGetLastError();
     return TST_ERR_CUDA;
   }
-  p->last_stream = s;
-  p->ran = true;
   return TST_OK;
 }
 
