@@ -13,7 +13,7 @@ def _plan(M=100, N=256, K=512, **kw):
 
 
 def test_plan_rules_and_info():
-    p = _plan(groups=4)
+    p = _plan(groups=4, tile_rows=16)
     assert (p.info.M, p.info.N, p.info.K, p.info.groups) == (100, 256, 512, 4)
     assert p.info.tile_cols >= 128 and p.info.grid >= 1 and 0 < p.info.smem_bytes <= 232448
     invalid, align, unsupported = tst.TST_ERR_INVALID_ARG, tst.TST_ERR_ALIGNMENT, tst.TST_ERR_UNSUPPORTED

@@ -27,17 +27,26 @@ __device__ __forceinline__ void int8_few_rows(const KernelParams& p, const int8_
   const int8_t* w[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) w[c] = b + (static_cast<int64_t>(group) * p.N + (col0 + c < p.N ? col0 + c : p.N - 1)) * p.K;
-  for (int32_t k = warp * 512 + lane * 16; k < p.K; k += WARPS * 512) {   // K is a multiple of 16
-    int4 v[C];
+  constexpr int U = R <= 4 ? 4 : R == 8 ? 2 : 1;   // steps of K in flight, as registers allow
+  for (int32_t k0 = warp * 512 + lane * 16; k0 < p.K; k0 += U * WARPS * 512) {   // K is a multiple of 16
+    int4 v[U][C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) v[c] = __ldg(reinterpret_cast<const int4*>(w[c] + k));
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int32_t row = row0 + (r < rows ? r : rows - 1);
-      const int4 x = __ldg(reinterpret_cast<const int4*>(a + static_cast<int64_t>(row) * p.K + k));
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        sum[r][c] = __dp4a(x.x, v[c].x, __dp4a(x.y, v[c].y, __dp4a(x.z, v[c].z, __dp4a(x.w, v[c].w, sum[r][c]))));
+        v[u][c] = k0 + u * WARPS * 512 < p.K ? __ldg(reinterpret_cast<const int4*>(w[c] + k0 + u * WARPS * 512)) : make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t k = k0 + u * WARPS * 512;
+      if (k >= p.K) break;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int32_t row = row0 + (r < rows ? r : rows - 1);
+        const int4 x = __ldg(reinterpret_cast<const int4*>(a + static_cast<int64_t>(row) * p.K + k));
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          sum[r][c] = __dp4a(x.x, v[u][c].x, __dp4a(x.y, v[u][c].y, __dp4a(x.z, v[u][c].z, __dp4a(x.w, v[u][c].w, sum[r][c]))));
+      }
     }
   }
 #pragma unroll
