@@ -74,7 +74,7 @@ int32_t score_warps(int32_t vpl, int32_t chunk, int64_t chunks) {
   return chunk == 32 && chunks <= 152 && vpl <= 8 ? 32 : tst::kRouteWarps;
 }
 size_t score_smem(int32_t experts, int32_t chunk, int32_t warps) {
-  return (static_cast<size_t>(experts) * (chunk / 32 + warps + 2) + 1) * 4;
+  return (static_cast<size_t>(experts) * (chunk / 32 + warps + 2) + 1 + 3) * 4;
 }
 
 // Zero device memory before returning, on a stream of its own: cudaMemset is ordered with the default

@@ -98,6 +98,12 @@ struct Sigmoid {
     rest = x >= 0.0f ? t * d : d;
   }
 };
+// the same without 1 - s, in four operations: 0 for -inf, a NaN for a NaN
+__device__ __forceinline__ float fast_sigmoid(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + RowExp::exp2_approx(-x * kLog2e)));
+  return r;
+}
 // e^-min(m, 0) / (1 + e^-x) for x <= m: scores of which the largest is at least 1/2, however far below 0 the logits are
 __device__ __forceinline__ float shifted_sigmoid(float x, float m) {
   return x >= 0.0f ? Sigmoid(x).s : __fdividef(__expf(x - fminf(m, 0.0f)), 1.0f + __expf(x));
@@ -113,9 +119,6 @@ __device__ __forceinline__ float score_gap(bool sigmoid, float s, float c) {
   const float mine = s * 1.52587890625e-5f;   // 2^-16
   return (sigmoid ? fminf(mine, 1.9073486e-6f) : mine) + fabsf(c) * 2.3841858e-7f + 1.5046328e-36f;   // 2^-19, 2^-22, 2^-119
 }
-
-// c as a value to compare: a NaN before everything
-__device__ __forceinline__ float choice_value(float c) { return c != c ? __uint_as_float(0x7F800000u) : c; }
 
 // The row's choice on FP64 values, as defined: lane j gets the j-th.
 template <typename T, int VPL>
@@ -199,10 +202,30 @@ __device__ __noinline__ int choose_exact(const ScoreParams& p, const T* src, int
   return chosen;
 }
 
+// A score as defined, of a row without NaN; peak and sum are softmax's.
+__device__ __forceinline__ double score_exact(bool sigmoid, float x, double peak, double sum) {
+  const double e = exp(sigmoid ? -static_cast<double>(x) : static_cast<double>(x) - peak);
+  return (sigmoid ? 1.0 : e) / (sigmoid ? 1.0 + e : sum);
+}
+template <typename T, int VPL>
+__device__ __forceinline__ void softmax_exact(const ScoreMap<T, VPL>& map, const T* src, double& peak, double& sum) {
+  float top = closed_logit();
+#pragma unroll 1
+  for (int v = 0; v < VPL; ++v) top = fmaxf(top, map.has(v) ? logit_value<T>(src[map.expert(v)]) : closed_logit());
+  peak = static_cast<double>(warp_max(top));
+  sum = 0.0;
+#pragma unroll 1
+  for (int v = 0; v < VPL; ++v)
+    if (map.has(v)) sum += exp(static_cast<double>(logit_value<T>(src[map.expert(v)])) - peak);
+#pragma unroll 1
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+}
+
 // What a choice is compared by: its value, and the logit and the bias that gave it.
 struct alignas(16) Ranked {
   float c, logit, bias;
   int32_t expert;
+  __device__ __forceinline__ bool before(const Ranked& o) const { return c > o.c || (c == o.c && expert < o.expert); }
   // whether the values may be in another order than computed (this one before o)
   __device__ __forceinline__ bool near(const Ranked& o, bool sigmoid) const {
     const float gap = score_gap(sigmoid, fmaxf(c - bias, o.c - o.bias), fmaxf(fabsf(c), fabsf(o.c)));
@@ -210,16 +233,230 @@ struct alignas(16) Ranked {
   }
 };
 
-// A warp per row, as route_rows_kernel: the same candidate list, on c.
+// Whether the lane's group stays, on FP64 values as defined.  (Loops that are not unrolled: this runs for one row in
+// thousands, and the time of such a row is that of fetching its code.)
+template <typename T, int VPL>
+__device__ __noinline__ bool choose_groups(const ScoreParams& p, const T* src) {
+  const int lane = threadIdx.x & 31;
+  const ScoreMap<T, VPL> map(lane, p.lanes, p.size, p.groups);
+  const double shut = -__longlong_as_double(0x7FF0000000000000ll);
+  double peak = 0.0, sum = 1.0;
+  if (!p.sigmoid) softmax_exact<T, VPL>(map, src, peak, sum);
+  double a = shut, b = shut;   // the largest two
+#pragma unroll 1
+  for (int v = 0; v < VPL; ++v) {
+    const float x = map.has(v) ? logit_value<T>(src[map.expert(v)]) : closed_logit();
+    double c = score_exact(p.sigmoid, x, peak, sum);
+    if (p.bias != nullptr && map.has(v)) c += static_cast<double>(p.bias[map.expert(v)]);
+    if (x == closed_logit()) c = shut;
+    b = fmax(b, fmin(a, c));
+    a = fmax(a, c);
+  }
+#pragma unroll 1
+  for (int d = p.lanes >> 1; d > 0; d >>= 1) {
+    const double oa = __shfl_xor_sync(kFullMask, a, d), ob = __shfl_xor_sync(kFullMask, b, d);
+    b = fmax(fmin(a, oa), fmax(b, ob));
+    a = fmax(a, oa);
+  }
+  const double mine = p.best == 2 && b != shut ? a + b : a;
+  const int g = lane / p.lanes;
+  int rank = 0;
+#pragma unroll 1
+  for (int i = 0; i < p.groups; ++i) {
+    const double o = __shfl_sync(kFullMask, mine, i * p.lanes);
+    rank += o > mine || (o == mine && i < g) ? 1 : 0;
+  }
+  return rank < p.top_groups && mine != shut;
+}
+
+// The order of at most 32 listed experts (lane i holds the i-th) on FP64 values as defined: the lane's place.
+template <typename T, int VPL>
+__device__ __noinline__ int choose_listed(const ScoreParams& p, const T* src, int n, const Ranked& mine) {
+  const int lane = threadIdx.x & 31;
+  double peak = 0.0, sum = 1.0;
+  if (!p.sigmoid) softmax_exact<T, VPL>(ScoreMap<T, VPL>(lane, p.lanes, p.size, p.groups), src, peak, sum);
+  double c = score_exact(p.sigmoid, mine.logit, peak, sum);
+  if (p.bias != nullptr) c += static_cast<double>(mine.bias);
+  int rank = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const double o = __shfl_sync(kFullMask, c, i);
+    const int at = __shfl_sync(kFullMask, mine.expert, i);
+    rank += o > c || (o == c && at < mine.expert) ? 1 : 0;
+  }
+  return rank;
+}
+
+// A round per choice, and one more, over values c: for rows whose list would be too long.  Lane j gets the j-th, n of
+// them in all; c is used up.
+template <typename T, int VPL>
+__device__ __noinline__ int choose_rounds(const ScoreMap<T, VPL>& map, const T* src, const float* bias, int k, float (&c)[VPL], Ranked& me) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+  for (int j = 0; j <= k; ++j) {
+    float b = closed_logit();
+    int at = 0xFFFF;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      if (c[v] > b) { b = c[v]; at = map.expert(v); }   // a lane's experts rise with v
+    const float m = warp_max(b);
+    if (m == closed_logit()) break;
+    const int who = static_cast<int>(__reduce_min_sync(kFullMask, b == m ? static_cast<uint32_t>(at) : 0xFFFFu));
+    if (lane == j) me = {m, logit_value<T>(src[who]), bias[who], who};
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      if (c[v] == m && map.expert(v) == who) c[v] = closed_logit();
+    ++n;
+  }
+  return n;
+}
+
+// on ? a : b without a branch.  (Where lanes without a kept group took one, the compiler led them through all that
+// follows apart from the others, up to each exchange: 131071 x 256 with 4 of 8 groups 302 us, without 190.)
+__device__ __forceinline__ float select(bool on, float a, float b) {
+  float r;
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\tselp.f32 %0, %1, %2, q;\n\t}"
+               : "=f"(r)
+               : "f"(a), "f"(b), "r"(static_cast<uint32_t>(on)));
+  return r;
+}
+
+// A row's choice out: lane j holds the j-th and its logit (-1 and -inf where there is none); sum and peak: softmax's of the row.
+__device__ __forceinline__ void put_choice(const ScoreParams& p, uint32_t* bitmap, int words, int64_t t0, int r, int chosen, float logit,
+                                           float sum, float peak) {
+  const int lane = threadIdx.x & 31, k = p.r.top_k;
+  float w = 0.0f;
+  if (p.sigmoid) {
+    w = chosen >= 0 ? fast_sigmoid(logit) : 0.0f;
+    if (p.r.normalize) {
+      const float z = warp_sum(w);
+      if (z < kLeastSum) {   // (no choice: not written)
+        const float top = warp_max_nan(logit);
+        w = chosen < 0 ? 0.0f : shifted_sigmoid(logit, top);
+        w = __fdividef(w, warp_sum(w));
+      } else {
+        w = __fdividef(w, z);
+      }
+    }
+  } else if (p.r.normalize) {
+    const float top = warp_max_nan(logit);
+    w = chosen < 0 ? 0.0f : __expf(logit - top);
+    w = __fdividef(w, warp_sum(w));
+  } else if (chosen >= 0) {
+    const RowExp ex(peak);
+    w = __fdividef(ex.any(logit), sum);
+  }
+  if (chosen >= 0) atomicOr(&bitmap[chosen * words + (r >> 5)], 1u << (r & 31));
+  if (lane < k) {
+    p.r.expert[(t0 + r) * k + lane] = chosen;
+    p.r.weight[(t0 + r) * k + lane] = chosen >= 0 ? w * p.weight_scale : 0.0f;
+  }
+}
+
+// A row that the list left open, whose share of the sums is counted already: by the list again, by rounds where more
+// are in reach than it holds, and by choose_exact where a NaN takes part or rounds do not tell.  Loops are not
+// unrolled: one row in hundreds comes here, and its time is that of fetching the code.  `kept`: the lanes whose groups
+// stay, 0 where that is open.
+template <typename T, int VPL>
+__device__ __noinline__ void late_row(const ScoreParams& p, const float* bias, uint32_t* bitmap, int words, int64_t t0, int r, bool odd,
+                                      uint32_t kept, Ranked* list) {
+  const int lane = threadIdx.x & 31, k = p.r.top_k;
+  const ScoreMap<T, VPL> map(lane, p.lanes, p.size, p.groups);
+  const T* const src = static_cast<const T*>(p.r.logits) + (t0 + r) * p.r.ld;
+  const bool sigmoid = p.sigmoid != 0;
+  float c[VPL], sum = 0.0f, peak = closed_logit(), largest = 1.0f;
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    c[v] = map.has(v) ? logit_value<T>(src[map.expert(v)]) : closed_logit();
+    peak = max_nan(peak, c[v]);
+  }
+  peak = warp_max_nan(peak);   // (not -inf: an expert is open)
+  const RowExp ex(peak);
+  float own = closed_logit();
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    const float s = c[v] == closed_logit() ? 0.0f : sigmoid ? fast_sigmoid(c[v]) : ex.any(c[v]);
+    sum += s;
+    c[v] = c[v] == closed_logit() ? closed_logit() : s;
+  }
+  sum = warp_sum(sum);
+  const float inv = sigmoid ? 1.0f : __fdividef(1.0f, sum);
+  if (!sigmoid) largest = fminf(1.0f, 1.1f * inv);
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    c[v] = c[v] * inv + (map.has(v) ? bias[map.expert(v)] : 0.0f);   // -inf stays
+    own = fmaxf(own, c[v]);
+  }
+  Ranked me = {closed_logit(), closed_logit(), 0.0f, -1};   // lane j: the j-th
+  int n = 0;
+  bool exact = odd || sum != sum;
+  if (!exact) {
+    if (!(kept != 0u ? (kept >> lane & 1u) != 0u : choose_groups<T, VPL>(p, src))) {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) c[v] = closed_logit();
+      own = closed_logit();
+    }
+    float bound = warp_max(own);
+#pragma unroll 1
+    for (int j = 1; j < k; ++j) {
+      own = own == bound ? closed_logit() : own;
+      bound = warp_max(own);
+    }
+    bound = fmaxf(bound - 2.0f * score_gap(sigmoid, largest, bound), -3.4028235e38f);
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const bool has = c[v] >= bound;
+      const uint32_t who = __ballot_sync(kFullMask, has);
+      const int slot = n + __popc(who & below);
+      if (has && slot < kRouteCandidates) list[slot] = {c[v], 0.0f, 0.0f, map.expert(v)};
+      n += __popc(who);
+    }
+    __syncwarp();
+    if (n <= kRouteCandidates) {
+      if (lane < n) {
+        me = list[lane];
+        me.logit = logit_value<T>(src[me.expert]);
+        me.bias = bias[me.expert];
+      }
+      const int place = choose_listed<T, VPL>(p, src, n, me);
+      __syncwarp();
+      if (lane < n) list[place] = me;
+      __syncwarp();
+      if (lane < n) me = list[lane];
+      __syncwarp();
+    } else {
+      n = choose_rounds<T, VPL>(map, src, bias, k, c, me);
+      const Ranked after = {__shfl_down_sync(kFullMask, me.c, 1), __shfl_down_sync(kFullMask, me.logit, 1),
+                            __shfl_down_sync(kFullMask, me.bias, 1), 0};
+      exact = __any_sync(kFullMask, lane < k && lane + 1 < n && (lane == 31 || me.near(after, sigmoid)));   // 32 choices: the 33rd has no lane
+    }
+  }
+  if (exact) {
+    me.expert = choose_exact<T, VPL>(p, src, lane);
+    me.logit = me.expert >= 0 ? logit_value<T>(src[me.expert]) : closed_logit();
+    n = 32;
+  }
+  const bool mine = lane < k && lane < n && me.expert >= 0;
+  put_choice(p, bitmap, words, t0, r, mine ? me.expert : -1, mine ? me.logit : closed_logit(), sum, peak);
+}
+
+// A warp per row, with the candidate list of route_rows_kernel on the values c.  Rows that it leaves open (values too
+// close, more than the list holds, a NaN, and every row where a bias is a NaN or +inf) are marked, and chosen by
+// late_row once all others are done: so the rows that come through carry no call (with calls between them, whose
+// registers are then spilled around them, 30 us more of 150).  What bounds it is issue slots, as in route_rows_kernel.
 template <typename T, int VPL, bool VEC, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 3 : VPL == 16 ? 2 : 1) score_rows_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL == 16 ? 2 : 1)
+    score_rows_kernel(const __grid_constant__ ScoreParams p) {
   using Map = ScoreMap<T, VPL>;
   extern __shared__ uint32_t route_smem[];
-  __shared__ alignas(16) Candidate list[WARPS][kRouteCandidates];
+  __shared__ Ranked list[WARPS][kRouteCandidates + 1];   // and one place for what is too much
   __shared__ Ranked ranked[WARPS][kRouteCandidates];
+  __shared__ uint32_t open_rows[8], open_kept[256];      // a bit per row of the chunk; late_row's `kept`
+  __shared__ int odd_bias;
   const int E = p.r.experts, k = p.r.top_k, words = p.r.chunk / 32;
   const RouteShared s(route_smem, E, words, WARPS);
-  float* const bias = reinterpret_cast<float*>(s.live + 1);   // E
+  float* const bias = reinterpret_cast<float*>(route_smem + ((E * (words + WARPS + 1) + 1 + 3) & ~3));   // E
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t below = (1u << lane) - 1u;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.r.chunk;
@@ -227,10 +464,20 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 3 : VPL
   const Map map(lane, p.lanes, p.size, p.groups);
   const bool sigmoid = p.sigmoid != 0;
 
-  for (int i = threadIdx.x; i < E * words; i += 32 * WARPS) s.bitmap[i] = 0u;
-  for (int i = threadIdx.x; i < E; i += 32 * WARPS) bias[i] = p.bias ? p.bias[i] : 0.0f;
-  if (threadIdx.x == 0) *s.live = 0;
+  if (threadIdx.x < 8) open_rows[threadIdx.x] = 0u;
+  if (threadIdx.x == 0) {
+    *s.live = 0;
+    odd_bias = 0;
+  }
   __syncthreads();
+  for (int i = threadIdx.x; i < E * words; i += 32 * WARPS) s.bitmap[i] = 0u;
+  for (int i = threadIdx.x; i < E; i += 32 * WARPS) {
+    const float b = p.bias ? p.bias[i] : 0.0f;
+    bias[i] = b;
+    if (!(b < __uint_as_float(0x7F800000u))) odd_bias = 1;
+  }
+  __syncthreads();
+  const bool odd = odd_bias != 0;
 
   float acc[VPL], next[VPL];
 #pragma unroll
@@ -245,156 +492,192 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 3 : VPL
     for (int v = 0; v < VPL; ++v) x[v] = next[v];
     if (r + WARPS < rows)   // the next row's loads fly while this one is worked on
       map.template load<VEC>(source(r + WARPS), routed(r + WARPS), next);
-    float best = x[0];
-#pragma unroll
-    for (int v = 1; v < VPL; ++v) best = max_nan(best, x[v]);
-    const RowExp ex(warp_max_nan(best));
-    int chosen = -1;
-    float w = 0.0f;
-    if (ex.top != closed_logit()) {
-      ++live;
-      // scores, and their share of the row's
-      float e[VPL], sum = 0.0f, largest = 1.0f;   // no score is above `largest`
+    // scores, and their share of the row's
+    float c[VPL], sum = 0.0f, largest = 1.0f, low = x[0], peak = 0.0f;   // no score is above `largest`; peak: softmax's top
+    bool some = true;                                                    // an expert is open
+    if (sigmoid) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        e[v] = x[v] == closed_logit() ? 0.0f : sigmoid ? Sigmoid(x[v]).s : ex.any(x[v]);
-        sum += e[v];
+        c[v] = fast_sigmoid(x[v]);   // 0 where closed
+        sum += c[v];
       }
       sum = warp_sum(sum);
-      if (sum < kLeastSum) {   // sigmoids of logits below -41: their shares as such
+      if (sum < kLeastSum) {         // logits below -41 or closed: their shares as such
+        float top = x[0];
+#pragma unroll
+        for (int v = 1; v < VPL; ++v) top = max_nan(top, x[v]);
+        top = warp_max_nan(top);
+        some = top != closed_logit();
         float part[VPL], all = 0.0f;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-          part[v] = x[v] == closed_logit() ? 0.0f : shifted_sigmoid(x[v], ex.top);
+          part[v] = x[v] == closed_logit() ? 0.0f : shifted_sigmoid(x[v], top);
           all += part[v];
         }
-        const float inv = 1.0f / warp_sum(all);
+        all = warp_sum(all);
+        const float inv = some ? 1.0f / all : 0.0f;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) acc[v] = fmaf(part[v], inv, acc[v]);
       } else {
-        const float inv = __fdividef(1.0f, sum);   // sum <= 1075
+        const float inv = __fdividef(1.0f, sum);
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          acc[v] = fmaf(e[v], inv, acc[v]);
-          if (!sigmoid) e[v] *= inv;
-        }
-        if (!sigmoid) largest = fminf(1.0f, 1.1f * inv);
+        for (int v = 0; v < VPL; ++v) acc[v] = fmaf(c[v], inv, acc[v]);
       }
-      // the values that choose
-      float c[VPL];
+    } else {
+      peak = x[0];
 #pragma unroll
-      for (int v = 0; v < VPL; ++v)
-        c[v] = x[v] == closed_logit() ? closed_logit() : choice_value(e[v] + (map.has(v) ? bias[map.expert(v)] : 0.0f));
-      bool near = false;
-      if (p.groups > 1) {
-        float a = closed_logit(), b = closed_logit();
+      for (int v = 1; v < VPL; ++v) peak = max_nan(peak, x[v]);
+      peak = warp_max_nan(peak);
+      some = peak != closed_logit();
+      const RowExp ex(some ? peak : 0.0f);
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          b = fmaxf(b, fminf(a, c[v]));
-          a = fmaxf(a, c[v]);
-        }
-        for (int d = p.lanes >> 1; d > 0; d >>= 1) {
-          const float oa = __shfl_xor_sync(kFullMask, a, d), ob = __shfl_xor_sync(kFullMask, b, d);
-          b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-          a = fmaxf(a, oa);
-        }
-        const float mine = p.best == 2 && b != closed_logit() ? a + b : a;
-        const int g = lane / p.lanes;
-        int rank = 0;
-        for (int i = 0; i < p.groups; ++i) {
-          const float o = __shfl_sync(kFullMask, mine, i * p.lanes);
-          rank += o > mine || (o == mine && i < g) ? 1 : 0;
-        }
-        const bool kept = rank < p.top_groups;
-        // the last group kept and the first one not; the gap of a sum of two whose scores are 1 at most
-        const float last = -warp_max(kept && g < p.groups ? -mine : closed_logit()), first = warp_max(kept || g >= p.groups ? closed_logit() : mine);
-        const float most = fmaxf(fabsf(last), fabsf(first));
-        near = first != closed_logit() && !(last - first > 2.0f * score_gap(sigmoid, largest, most));
-        if (!kept) {
+      for (int v = 0; v < VPL; ++v) {
+        c[v] = x[v] == closed_logit() ? 0.0f : ex.any(x[v]);
+        sum += c[v];
+      }
+      sum = warp_sum(sum);
+      const float inv = some ? __fdividef(1.0f, sum) : 0.0f;   // sum <= 1075
 #pragma unroll
-          for (int v = 0; v < VPL; ++v) c[v] = closed_logit();
+      for (int v = 0; v < VPL; ++v) {
+        c[v] *= inv;
+        acc[v] += c[v];
+      }
+      largest = fminf(1.0f, 1.1f * inv);
+    }
+    if (!some) {
+      put_choice(p, s.bitmap, words, t0, r, -1, closed_logit(), 1.0f, 0.0f);
+      continue;
+    }
+    ++live;
+    // the values that choose
+    if (p.bias != nullptr) {
+#pragma unroll
+      for (int q = 0; q < VPL / Map::W; ++q) {
+        struct alignas(VEC ? 4 * Map::W < 16 ? 4 * Map::W : 16 : 4) Biases { float v[Map::W]; };
+        if (VEC) {
+          if (map.has(q * Map::W)) {
+            const Biases b = *reinterpret_cast<const Biases*>(bias + map.expert(q * Map::W));
+#pragma unroll
+            for (int i = 0; i < Map::W; ++i) c[q * Map::W + i] += b.v[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < Map::W; ++i)
+            if (map.has(q * Map::W + i)) c[q * Map::W + i] += bias[map.expert(q * Map::W + i)];
         }
       }
-      if (!near) {
-        float own = c[0];
+    }
+#pragma unroll
+    for (int v = 1; v < VPL; ++v) low = fminf(low, x[v]);
+    if (__any_sync(kFullMask, low == closed_logit())) {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) c[v] = x[v] == closed_logit() ? closed_logit() : c[v];
+    }
+    bool near = odd || sum != sum, kept = true, groups_near = false;
+    float own = c[0];   // the lane's largest
+    if (p.groups > 1) {
+      float b = closed_logit();
+      if (p.best == 2) {
+#pragma unroll
+        for (int v = 1; v < VPL; ++v) {
+          b = fmaxf(b, fminf(own, c[v]));
+          own = fmaxf(own, c[v]);
+        }
+      } else {
 #pragma unroll
         for (int v = 1; v < VPL; ++v) own = fmaxf(own, c[v]);
-        float bound = warp_max(own);
-        for (int j = 1; j < k; ++j) {
-          own = own == bound ? closed_logit() : own;
-          bound = warp_max(own);
-        }
-        // what is listed: all that may reach the bound; a closed expert reaches none
-        bound = fmaxf(bound - 2.0f * score_gap(sigmoid, largest, bound), -3.4028235e38f);
-        int n = 0;
+      }
+      float a = own;
+      for (int d = p.lanes >> 1; d > 0; d >>= 1) {
+        const float oa = __shfl_xor_sync(kFullMask, a, d);
+        if (p.best == 2) b = fmaxf(fminf(a, oa), fmaxf(b, __shfl_xor_sync(kFullMask, b, d)));
+        a = fmaxf(a, oa);
+      }
+      const float mine = p.best == 2 ? select(b != closed_logit(), a + b, a) : a;   // closed for a lane without a group
+      // the last value kept, by rounds; equal values are left to choose_groups
+      float left = mine, last = warp_max(left);
+      for (int j = 1; j < p.top_groups; ++j) {
+        left = left == last ? closed_logit() : left;
+        const float m = warp_max(left);
+        if (m == closed_logit()) break;   // fewer groups are open
+        last = m;
+      }
+      kept = mine >= last && mine != closed_logit();
+      const float first = warp_max(select(kept, closed_logit(), mine)), most = fmaxf(fabsf(last), fabsf(first));
+      groups_near = __popc(__ballot_sync(kFullMask, kept)) > p.top_groups * p.lanes ||
+                    (first != closed_logit() && !(last - first > 2.0f * score_gap(sigmoid, largest, most)));
+      near = near || groups_near;
+      own = select(kept, own, closed_logit());
+    } else {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          const bool has = c[v] >= bound;
-          const uint32_t who = __ballot_sync(kFullMask, has);
-          const int slot = n + __popc(who & below);
-          if (has && slot < kRouteCandidates) list[warp][slot] = {c[v], map.expert(v)};
-          n += __popc(who);
+      for (int v = 1; v < VPL; ++v) own = fmaxf(own, c[v]);
+    }
+    Ranked me = {closed_logit(), closed_logit(), 0.0f, -1};   // lane j: the j-th
+    int n = 0;
+    if (!near) {
+      float bound = warp_max(own);
+      for (int j = 1; j < k; ++j) {
+        own = own == bound ? closed_logit() : own;
+        bound = warp_max(own);
+      }
+      // what is listed: all that may reach the bound; a closed expert reaches none
+      bound = fmaxf(bound - 2.0f * score_gap(sigmoid, largest, bound), -3.4028235e38f);
+      bound = select(kept, bound, __uint_as_float(0x7F800000u));   // (no value is +inf here)
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) {
+        const bool has = c[v] >= bound;
+        const uint32_t who = __ballot_sync(kFullMask, has);
+        const int slot = n + __popc(who & below);
+        if (has) list[warp][slot < kRouteCandidates ? slot : kRouteCandidates] = {c[v], x[v], 0.0f, map.expert(v)};
+        n += __popc(who);
+      }
+      __syncwarp();
+      near = n > kRouteCandidates;
+      if (!near) {
+        // each finds its rank by comparing itself with the others, two lanes to one when at most 16 are listed
+        const bool halves = n <= 16;
+        const int at = halves ? lane & 15 : lane, share = halves ? (n + 1) >> 1 : n, from = halves && lane >= 16 ? share : 0;
+        Ranked mine = list[warp][at < n ? at : 0];
+        int rank = 0;
+        for (int i = from; i < from + share; ++i) {
+          const Ranked o = list[warp][i < n ? i : 0];
+          rank += (static_cast<int>(o.c > mine.c) | (static_cast<int>(o.c == mine.c) & static_cast<int>(o.expert < mine.expert))) &
+                  static_cast<int>(i < n);
+        }
+        if (halves) rank += __shfl_xor_sync(kFullMask, rank, 16);
+        if (lane < n) {
+          mine.bias = bias[mine.expert];
+          ranked[warp][rank] = mine;
         }
         __syncwarp();
-        Ranked me = {};
-        if (n <= kRouteCandidates) {
-          // each finds its rank by comparing itself with the others
-          Candidate mine = {closed_logit(), E};
-          int rank = 0;
-          if (lane < n) mine = list[warp][lane];
-          for (int i = 0; i < n; ++i) rank += list[warp][i].before(mine) ? 1 : 0;
-          if (lane < n) ranked[warp][rank] = {mine.logit, logit_value<T>(source(r)[mine.expert]), bias[mine.expert], mine.expert};
-          __syncwarp();
-          if (lane < n) me = ranked[warp][lane];
-          near = lane < k && lane + 1 < n && me.near(ranked[warp][lane + 1], sigmoid);
-          __syncwarp();
-        } else {
-          // more than the list holds (few lanes left by the groups, many equal values): a round per choice, and one more
-          n = 0;
-          for (int j = 0; j <= k; ++j) {
-            float b = closed_logit();
-            int at = E;
-#pragma unroll
-            for (int v = 0; v < VPL; ++v)
-              if (c[v] > b) { b = c[v]; at = map.expert(v); }   // a lane's experts rise with v
-            const float m = warp_max(b);
-            if (m == closed_logit()) break;
-            const int who = static_cast<int>(__reduce_min_sync(kFullMask, b == m ? static_cast<uint32_t>(at) : 0xFFFFu));
-            if (lane == j) me = {m, logit_value<T>(source(r)[who]), bias[who], who};
-#pragma unroll
-            for (int v = 0; v < VPL; ++v)
-              if (c[v] == m && map.expert(v) == who) c[v] = closed_logit();
-            ++n;
-          }
-          const Ranked after = {__shfl_down_sync(kFullMask, me.c, 1), __shfl_down_sync(kFullMask, me.logit, 1),
-                                __shfl_down_sync(kFullMask, me.bias, 1), 0};
-          near = lane < k && lane + 1 < n && (lane == 31 || me.near(after, sigmoid));   // 32 choices: the 33rd has no lane
-        }
-        near = __any_sync(kFullMask, near);
-        if (lane < k && lane < n) chosen = me.expert;
+        if (lane < n) me = ranked[warp][lane];
+        near = __any_sync(kFullMask, lane < k && lane + 1 < n && me.near(ranked[warp][lane + 1 < n ? lane + 1 : lane], sigmoid));
       }
-      if (near) chosen = choose_exact<T, VPL>(p, source(r), lane);   // (the whole warp)
-      // the weights, from the chosen logits themselves
-      const float logit = chosen >= 0 ? logit_value<T>(source(r)[chosen]) : closed_logit();
-      if (p.r.normalize) {
-        const float top = warp_max_nan(logit);
-        w = chosen < 0 ? 0.0f : sigmoid ? shifted_sigmoid(logit, top) : __expf(logit - top);
-        w = __fdividef(w, warp_sum(w)) * p.weight_scale;
-      } else if (chosen >= 0) {
-        w = (sigmoid ? Sigmoid(logit).s : __fdividef(ex.any(logit), sum)) * p.weight_scale;
+      __syncwarp();
+    }
+    if (near) {
+      const uint32_t who = __ballot_sync(kFullMask, kept);
+      if (lane == 0) {
+        open_kept[r] = groups_near ? 0u : who;
+        atomicOr(&open_rows[r >> 5], 1u << (r & 31));
       }
-      if (chosen >= 0) atomicOr(&s.bitmap[chosen * words + (r >> 5)], 1u << (r & 31));
-      else w = 0.0f;
+      continue;
     }
-    if (lane < k) {
-      p.r.expert[(t0 + r) * k + lane] = chosen;
-      p.r.weight[(t0 + r) * k + lane] = w;
-    }
+    const bool mine = lane < k && lane < n;
+    put_choice(p, s.bitmap, words, t0, r, mine ? me.expert : -1, mine ? me.logit : closed_logit(), sum, peak);
   }
 #pragma unroll
   for (int v = 0; v < VPL; ++v)
     if (map.has(v)) s.prob[warp * E + map.expert(v)] = acc[v];
   if (lane == 0 && live > 0) atomicAdd(s.live, live);
+  __syncthreads();
+  int turn = 0;
+  for (int i = 0; i < words; ++i)
+    for (uint32_t left = open_rows[i]; left != 0u; left &= left - 1u)
+      if (turn++ % WARPS == warp) {
+        const int r = i * 32 + __ffs(left) - 1;
+        late_row<T, VPL>(p, bias, s.bitmap, words, t0, r, odd, open_kept[r], list[warp]);
+      }
   finish_chunk(p.r, s, words, WARPS, t0, rows);
 }
 
@@ -427,73 +710,96 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
   };
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps;
   auto routed = [&](int64_t t) { return p.r.mask == nullptr || p.r.mask[t] != 0; };
+  auto row = [&](int64_t t) { return static_cast<const T*>(p.r.logits) + t * p.r.ld; };
+  // row t's choice of this lane, and that expert's logit: read a row ahead
+  auto choice = [&](int64_t t) {
+    const int c = t < p.r.tokens && lane < k ? p.r.expert[t * k + lane] : -1;
+    return c < E ? c : -1;
+  };
+  auto logit_of = [&](int64_t t, int c) { return c >= 0 ? logit_value<T>(row(t)[c]) : closed_logit(); };
   float next[VPL];
   int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-  if (t < p.r.tokens) map.template load<VEC>(static_cast<const T*>(p.r.logits) + t * p.r.ld, routed(t), next);
+  int chosen_next = choice(t);
+  float logit_next = logit_of(t, chosen_next);
+  if (t < p.r.tokens) map.template load<VEC>(row(t), routed(t), next);
   for (; t < p.r.tokens; t += step) {
-    const T* src = static_cast<const T*>(p.r.logits) + t * p.r.ld;
     T* dst = static_cast<T*>(p.r.d_logits) + t * p.r.d_ld;
-    float x[VPL];
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) x[v] = next[v];
-    int chosen = lane < k ? p.r.expert[t * k + lane] : -1;
-    if (chosen >= E) chosen = -1;
-    float dw = chosen >= 0 && p.r.d_weight != nullptr ? p.r.d_weight[t * k + lane] * p.weight_scale : 0.0f;
-    if (t + step < p.r.tokens)
-      map.template load<VEC>(static_cast<const T*>(p.r.logits) + (t + step) * p.r.ld, routed(t + step), next);
-    float best = x[0];
-#pragma unroll
-    for (int v = 1; v < VPL; ++v) best = max_nan(best, x[v]);
-    const RowExp ex(warp_max_nan(best));
-    if (ex.top == closed_logit()) {   // nothing was routed: the row has no part in any output
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) x[v] = 0.0f;
-      map.template store<VEC>(dst, x);
-      continue;
-    }
-    float e[VPL], rest[VPL], sum = 0.0f, dot = 0.0f;
+    float e[VPL], top = next[0];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const bool on = x[v] != closed_logit();
-      if (sigmoid) {
-        const Sigmoid sg(x[v]);
-        e[v] = on ? sg.s : 0.0f;
-        rest[v] = on ? sg.rest : 0.0f;
-      } else {
-        e[v] = on ? ex.any(x[v]) : 0.0f;
-        rest[v] = 0.0f;
-      }
-      sum += e[v];
-      dot = fmaf(e[v], g[v], dot);
+      e[v] = next[v];
+      top = max_nan(top, e[v]);
     }
-    const float logit = chosen >= 0 ? logit_value<T>(src[chosen]) : closed_logit();
-    sum = warp_sum(sum);
-    if (sum < kLeastSum) {   // as in the forward pass
-      sum = dot = 0.0f;
+    const int chosen = chosen_next;
+    const float logit = logit_next;
+    float dw = chosen >= 0 && p.r.d_weight != nullptr ? p.r.d_weight[t * k + lane] * p.weight_scale : 0.0f;
+    chosen_next = choice(t + step);
+    if (t + step < p.r.tokens) map.template load<VEC>(row(t + step), routed(t + step), next);
+    top = warp_max_nan(top);
+    if (top == closed_logit()) {   // nothing was routed: the row has no part in any output
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) e[v] = 0.0f;
+      map.template store<VEC>(dst, e);
+      logit_next = logit_of(t + step, chosen_next);
+      continue;
+    }
+    const RowExp ex(top);
+    const float first = p.r.normalize ? warp_max_nan(logit) : 0.0f;   // of the chosen; -inf without any
+    float own = 0.0f, sum = 0.0f, dot = 0.0f;   // the choice's score; the row's sums
+    if (sigmoid) {
+      if (chosen >= 0) own = p.r.normalize ? shifted_sigmoid(logit, first) : Sigmoid(logit).s;
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        e[v] = x[v] == closed_logit() ? 0.0f : shifted_sigmoid(x[v], ex.top);
+        const float s = fast_sigmoid(e[v]);   // 0 where closed
+        sum += s;
+        dot = fmaf(s, g[v], dot);
+      }
+    } else {
+      if (chosen >= 0) own = p.r.normalize ? __expf(logit - first) : ex.any(logit);
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) {
+        e[v] = e[v] == closed_logit() ? 0.0f : ex.any(e[v]);
         sum += e[v];
         dot = fmaf(e[v], g[v], dot);
       }
-      sum = warp_sum(sum);
     }
-    const float inv = 1.0f / sum;
-    dot = warp_sum(dot) * inv;
-    // the weights' part of u at the chosen experts
-    float all = 0.0f;   // its sum (softmax without normalisation)
+    // the sums that the row needs in one pass over the lanes, so that their latencies overlap
+    float kept = own, kept_dot = own * dw;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+      sum += __shfl_xor_sync(kFullMask, sum, m);
+      dot += __shfl_xor_sync(kFullMask, dot, m);
+      kept += __shfl_xor_sync(kFullMask, kept, m);
+      kept_dot += __shfl_xor_sync(kFullMask, kept_dot, m);
+    }
+    bool small = false;
+    if (sigmoid && sum < kLeastSum) {   // as in the forward pass: shares with a shift
+      small = true;
+      sum = dot = 0.0f;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) {
+        const float s = e[v] == closed_logit() ? 0.0f : shifted_sigmoid(e[v], top);
+        sum += s;
+        dot = fmaf(s, g[v], dot);
+      }
+      sum = warp_sum(sum);
+      dot = warp_sum(dot);
+    }
+    const float inv = __fdividef(1.0f, sum);
+    dot *= inv;
+    // the weights' part of u at the chosen experts, and its sum
+    float all = 0.0f;
     if (p.r.normalize) {
-      const float top = warp_max_nan(logit);
-      float q = chosen < 0 ? 0.0f : sigmoid ? shifted_sigmoid(logit, top) : __expf(logit - top);
-      const float z = warp_sum(q);
-      q = z > 0.0f || z != z ? __fdividef(q, z) : 0.0f;   // no choice: 0
-      dw = q * (dw - warp_sum(q * dw));
+      const float over = kept > 0.0f || kept != kept ? __fdividef(1.0f, kept) : 0.0f;   // no choice: 0
+      dw = own * over * (dw - kept_dot * over);
     } else {
-      if (chosen >= 0) dw *= sigmoid ? Sigmoid(logit).s : ex.any(logit) * inv;
-      all = warp_sum(dw);
+      const float by = sigmoid ? 1.0f : inv;
+      dw *= own * by;
+      all = kept_dot * by;
     }
     const int at = chosen >= 0 ? place(chosen) : 0;
     if (chosen >= 0) part[at] = dw;
+    logit_next = logit_of(t + step, chosen_next);
     __syncwarp();
 #pragma unroll
     for (int q = 0; q < VPL / Map::W; ++q) {
@@ -502,9 +808,15 @@ __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 
 #pragma unroll
       for (int i = 0; i < Map::W; ++i) {
         const int v = q * Map::W + i;
-        const float pe = e[v] * inv;
-        const float u = fmaf(pe, g[v] - dot, add.v[i]);
-        e[v] = sigmoid ? u * rest[v] : u - pe * all;
+        if (sigmoid) {
+          const Sigmoid s(e[v]);
+          const float share = small ? e[v] == closed_logit() ? 0.0f : shifted_sigmoid(e[v], top) : s.s;
+          const float u = fmaf(share * inv, g[v] - dot, add.v[i]);
+          e[v] = e[v] == closed_logit() ? 0.0f : u * s.rest;
+        } else {
+          const float pe = e[v] * inv;
+          e[v] = fmaf(pe, g[v] - dot, add.v[i]) - pe * all;
+        }
       }
     }
     __syncwarp();
