@@ -207,17 +207,22 @@ __device__ __forceinline__ double score_exact(bool sigmoid, float x, double peak
   const double e = exp(sigmoid ? -static_cast<double>(x) : static_cast<double>(x) - peak);
   return (sigmoid ? 1.0 : e) / (sigmoid ? 1.0 + e : sum);
 }
+// Softmax's top and sum.  Without a bias the scores are compared before the division, which all share: a sum of 1.
 template <typename T, int VPL>
-__device__ __forceinline__ void softmax_exact(const ScoreMap<T, VPL>& map, const T* src, double& peak, double& sum) {
-  float top = closed_logit();
-#pragma unroll 1
-  for (int v = 0; v < VPL; ++v) top = fmaxf(top, map.has(v) ? logit_value<T>(src[map.expert(v)]) : closed_logit());
+__device__ __forceinline__ void softmax_exact(const ScoreParams& p, const ScoreMap<T, VPL>& map, const T* src, double& peak, double& sum) {
+  float x[VPL], top = closed_logit();
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    x[v] = map.has(v) ? logit_value<T>(src[map.expert(v)]) : closed_logit();
+    top = fmaxf(top, x[v]);
+  }
   peak = static_cast<double>(warp_max(top));
+  sum = 1.0;
+  if (p.bias == nullptr) return;
   sum = 0.0;
-#pragma unroll 1
-  for (int v = 0; v < VPL; ++v)
-    if (map.has(v)) sum += exp(static_cast<double>(logit_value<T>(src[map.expert(v)])) - peak);
-#pragma unroll 1
+#pragma unroll 4   // that many exponentials side by side
+  for (int v = 0; v < VPL; ++v) sum += x[v] != closed_logit() ? exp(static_cast<double>(x[v]) - peak) : 0.0;
+#pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
 }
 
@@ -233,22 +238,25 @@ struct alignas(16) Ranked {
   }
 };
 
-// Whether the lane's group stays, on FP64 values as defined.  (Loops that are not unrolled: this runs for one row in
-// thousands, and the time of such a row is that of fetching its code.)
+// Whether the lane's group stays, on FP64 values as defined, of which `need` has those of the lane that may be among its
+// group's largest two.  (Loops that are not unrolled: this runs for one row in thousands, and much of the time of such
+// a row is that of fetching its code.)
 template <typename T, int VPL>
-__device__ __noinline__ bool choose_groups(const ScoreParams& p, const T* src) {
+__device__ __noinline__ bool choose_groups(const ScoreParams& p, const T* src, uint32_t need) {
   const int lane = threadIdx.x & 31;
   const ScoreMap<T, VPL> map(lane, p.lanes, p.size, p.groups);
   const double shut = -__longlong_as_double(0x7FF0000000000000ll);
   double peak = 0.0, sum = 1.0;
-  if (!p.sigmoid) softmax_exact<T, VPL>(map, src, peak, sum);
+  if (!p.sigmoid) softmax_exact<T, VPL>(p, map, src, peak, sum);
   double a = shut, b = shut;   // the largest two
 #pragma unroll 1
-  for (int v = 0; v < VPL; ++v) {
-    const float x = map.has(v) ? logit_value<T>(src[map.expert(v)]) : closed_logit();
-    double c = score_exact(p.sigmoid, x, peak, sum);
-    if (p.bias != nullptr && map.has(v)) c += static_cast<double>(p.bias[map.expert(v)]);
-    if (x == closed_logit()) c = shut;
+  for (; __any_sync(kFullMask, need != 0u); need &= need - 1u) {
+    double c = shut;
+    if (need != 0u) {
+      const int e = map.expert(__ffs(need) - 1);
+      c = score_exact(p.sigmoid, logit_value<T>(src[e]), peak, sum);
+      if (p.bias != nullptr) c += static_cast<double>(p.bias[e]);
+    }
     b = fmax(b, fmin(a, c));
     a = fmax(a, c);
   }
@@ -274,7 +282,7 @@ template <typename T, int VPL>
 __device__ __noinline__ int choose_listed(const ScoreParams& p, const T* src, int n, const Ranked& mine) {
   const int lane = threadIdx.x & 31;
   double peak = 0.0, sum = 1.0;
-  if (!p.sigmoid) softmax_exact<T, VPL>(ScoreMap<T, VPL>(lane, p.lanes, p.size, p.groups), src, peak, sum);
+  if (!p.sigmoid) softmax_exact<T, VPL>(p, ScoreMap<T, VPL>(lane, p.lanes, p.size, p.groups), src, peak, sum);
   double c = score_exact(p.sigmoid, mine.logit, peak, sum);
   if (p.bias != nullptr) c += static_cast<double>(mine.bias);
   int rank = 0;
@@ -391,7 +399,28 @@ __device__ __noinline__ void late_row(const ScoreParams& p, const float* bias, u
   int n = 0;
   bool exact = odd || sum != sum;
   if (!exact) {
-    if (!(kept != 0u ? (kept >> lane & 1u) != 0u : choose_groups<T, VPL>(p, src))) {
+    bool stays = (kept >> lane & 1u) != 0u;
+    if (kept == 0u) {
+      float a = closed_logit(), b = closed_logit();   // the group's largest two
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) {
+        b = fmaxf(b, fminf(a, c[v]));
+        a = fmaxf(a, c[v]);
+      }
+#pragma unroll 1
+      for (int d = p.lanes >> 1; d > 0; d >>= 1) {
+        const float oa = __shfl_xor_sync(kFullMask, a, d), ob = __shfl_xor_sync(kFullMask, b, d);
+        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+        a = fmaxf(a, oa);
+      }
+      const float least = p.best == 2 && b != closed_logit() ? b : a;
+      const float reach = fmaxf(least - 2.0f * score_gap(sigmoid, largest, least), -3.4028235e38f);
+      uint32_t need = 0u;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) need |= (c[v] >= reach ? 1u : 0u) << v;
+      stays = choose_groups<T, VPL>(p, src, need);
+    }
+    if (!stays) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) c[v] = closed_logit();
       own = closed_logit();
