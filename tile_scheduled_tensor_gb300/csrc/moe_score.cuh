@@ -329,6 +329,15 @@ __device__ __forceinline__ float select(bool on, float a, float b) {
   return r;
 }
 
+// *at = r where `on`, in shared memory, without a branch
+__device__ __forceinline__ void put_ranked(bool on, Ranked* at, const Ranked& r) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t@q st.shared.v4.b32 [%1], {%2, %3, %4, %5};\n\t}"
+               :
+               : "r"(static_cast<uint32_t>(on)), "r"(static_cast<uint32_t>(__cvta_generic_to_shared(at))), "f"(r.c), "f"(r.logit),
+                 "f"(r.bias), "r"(r.expert)
+               : "memory");
+}
+
 // A row's choice out: lane j holds the j-th and its logit (-1 and -inf where there is none); sum and peak: softmax's of the row.
 __device__ __forceinline__ void put_choice(const ScoreParams& p, uint32_t* bitmap, int words, int64_t t0, int r, int chosen, float logit,
                                            float sum, float peak) {
@@ -481,6 +490,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
   extern __shared__ uint32_t route_smem[];
   __shared__ Ranked list[WARPS][kRouteCandidates + 1];   // and one place for what is too much
   __shared__ Ranked ranked[WARPS][kRouteCandidates];
+  __shared__ alignas(16) float listed[WARPS][kRouteCandidates];
   __shared__ uint32_t open_rows[8], open_kept[256];      // a bit per row of the chunk; late_row's `kept`
   __shared__ int odd_bias;
   const int E = p.r.experts, k = p.r.top_k, words = p.r.chunk / 32;
@@ -657,23 +667,29 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
         const bool has = c[v] >= bound;
         const uint32_t who = __ballot_sync(kFullMask, has);
         const int slot = n + __popc(who & below);
-        if (has) list[warp][slot < kRouteCandidates ? slot : kRouteCandidates] = {c[v], x[v], 0.0f, map.expert(v)};
+        put_ranked(has, &list[warp][slot < kRouteCandidates ? slot : kRouteCandidates], {c[v], x[v], 0.0f, map.expert(v)});
         n += __popc(who);
       }
       __syncwarp();
       near = n > kRouteCandidates;
       if (!near) {
         // each finds its rank by comparing itself with the others, two lanes to one when at most 16 are listed
+        Ranked mine = list[warp][lane];
+        listed[warp][lane] = lane < n ? mine.c : closed_logit();
+        __syncwarp();
         const bool halves = n <= 16;
-        const int at = halves ? lane & 15 : lane, share = halves ? (n + 1) >> 1 : n, from = halves && lane >= 16 ? share : 0;
-        Ranked mine = list[warp][at < n ? at : 0];
+        const float value = halves ? __shfl_sync(kFullMask, mine.c, lane & 15) : mine.c;
         int rank = 0;
-        for (int i = from; i < from + share; ++i) {
-          const Ranked o = list[warp][i < n ? i : 0];
-          rank += (static_cast<int>(o.c > mine.c) | (static_cast<int>(o.c == mine.c) & static_cast<int>(o.expert < mine.expert))) &
-                  static_cast<int>(i < n);
+        for (int i = 0; i < n; i += halves ? 8 : 4) {
+          const float4 o = *reinterpret_cast<const float4*>(&listed[warp][i + (halves ? lane >> 4 << 2 : 0)]);
+          rank += static_cast<int>(o.x > value) + static_cast<int>(o.y > value) + static_cast<int>(o.z > value) + static_cast<int>(o.w > value);
         }
         if (halves) rank += __shfl_xor_sync(kFullMask, rank, 16);
+        if (__popc(__reduce_or_sync(kFullMask, lane < n ? 1u << rank : 0u)) != n) {   // equal ones: the lower expert first
+#pragma unroll 1
+          for (int i = 0; i < n; ++i)
+            rank += static_cast<int>(list[warp][i].c == mine.c) & static_cast<int>(list[warp][i].expert < mine.expert);
+        }
         if (lane < n) {
           mine.bias = bias[mine.expert];
           ranked[warp][rank] = mine;
