@@ -169,7 +169,7 @@ def simulate(seed, blocks, stages, cv, xs, wsets, bufs, global_parity=True):
 
 
 #      rows: stages, cv, xs, wsets, bufs
-FORMS = {16: (12, 6, 6, 4, 2), 32: (8, 6, 6, 4, 2), 64: (8, 6, 4, 4, 1), 128: (4, 4, 4, 2, 1)}
+FORMS = {16: (12, 6, 6, 3, 2), 32: (9, 6, 8, 3, 2), 64: (6, 6, 6, 3, 1), 128: (4, 4, 4, 2, 1)}
 TILES = [[1] * 9, [2, 1, 3, 1, 1, 2], [17] * 4, [33, 32, 31], [4, 5, 16, 17, 18, 1], [64, 3]]
 
 
@@ -193,7 +193,7 @@ def test_broken_forms_are_caught(broken):
 def test_the_forms_are_the_kernels():
     """FORMS against the constants of Int8Cfg, recomputed from its definition."""
     for nt, (stages, cv, xs, wsets, bufs) in FORMS.items():
-        assert wsets == (2 if nt == 128 else 4) and bufs == (1 if nt >= 64 else 2) and xs == (6 if nt <= 32 else 4)
+        assert wsets == (2 if nt == 128 else 3) and bufs == (1 if nt >= 64 else 2) and xs == {32: 8, 128: 4}.get(nt, 6)
         assert cv == (512 - 2 * bufs * nt) // 128 * 2
         fixed = 1024 + xs * nt * 256 + (3 * 512 + 4) * 4 + 512
         assert stages == (232448 - fixed) // 16384 // wsets * wsets

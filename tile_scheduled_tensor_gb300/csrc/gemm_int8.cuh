@@ -22,7 +22,7 @@
 // and come by TMA.  (Two warps that converted them beside the weights took 1400 cycles per k-block of 64
 // tokens, and 450 of 16, most of it waiting for their writes to be seen by the tensor core.)
 //
-// Roles, 768 threads (of 128 tokens: 512), one CTA per SM, persistent over NT x 128 tiles of D, k-blocks
+// Roles, 640 threads (of 128 tokens: 512), one CTA per SM, persistent over NT x 128 tiles of D, k-blocks
 // of 128:
 //   warp 0      TMA: 128 x 128 bytes of B per stage of the byte ring
 //   warps 1, 3  MMA issuers of every second k-block, into accumulators of their own: eight K = 16 MMAs,
@@ -32,7 +32,11 @@
 //   warps 8-11  a thread per channel: accumulators -> integer sums; scales, bias, ReLU, cast, store
 //   the others  weights: a thread per channel, 128 bytes -> 64 columns of Tensor Memory.  One k-block
 //               takes a warpgroup 800 to 1000 cycles, most of them latencies, where its 16 KB come in
-//               700 at the copy rate: four warpgroups (of 128 tokens: two) take k-blocks in turn
+//               700 at the copy rate: three warpgroups (of 128 tokens: two) take k-blocks in turn.  A
+//               fourth is in the others' way: 16 tokens x 8192 x 8192 in 22.9 us with it, 22.0 without
+// What bounds it: the copy rate while each weight is read once (64 rows over 32 experts of 4096 x 4096 in
+// 85 us, 0.93 of it); else the tensor core, whose eight MMAs of a k-block take 480 cycles of 16 or 32 tokens,
+// 620 of 64 and 910 of 128 (512 x 9728 x 4096, its weights from L2: 72, 49 and 40 us).
 // Every wait is bounded as in the other kernels.
 #pragma once
 #include "gemm_bs_tile.cuh"
@@ -44,7 +48,7 @@ constexpr int kInt8Fold = 8;   // k-blocks of 128 per accumulator: 1024 products
 template <int NT_>
 struct Int8Cfg {
   static constexpr int NT = NT_;
-  static constexpr int WSETS = NT == 128 ? 2 : 4;          // warpgroups that convert weights, k-blocks in turn
+  static constexpr int WSETS = NT == 128 ? 2 : 3;          // warpgroups that convert weights, k-blocks in turn
   static constexpr int THREADS = 256 + 128 * WSETS;
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int X_ATOM = NT * 128;                  // 64 elements of the tokens' tile
@@ -52,7 +56,7 @@ struct Int8Cfg {
   static constexpr int BUFS = NT >= 64 ? 1 : 2;            // accumulators per issuer
   static constexpr int A_COL = 2 * BUFS * NT;              // first TMEM column of the weights
   static constexpr int CV = (512 - A_COL) / 128 * 2;       // converted k-blocks of weights: 64 TMEM columns each
-  static constexpr int XS = NT <= 32 ? 6 : 4;              // k-blocks of tokens
+  static constexpr int XS = NT == 128 ? 4 : NT == 32 ? 8 : 6;   // k-blocks of tokens
   static constexpr int FIXED = 1024 + XS * X_BYTES + kWalkBytes + 512;
   // A warpgroup that converts weights meets every WSETS-th k-block alone, an issuer every second one, and
   // loads land and warpgroups finish in any order.  A wait tells a phase only from the one before it, so a
@@ -69,8 +73,8 @@ struct Int8Cfg {
   static_assert(SMEM_BYTES <= kSmemLimit && STAGES >= 4 && STAGES <= 32, "fits an SM");
   static_assert(STAGES % WSETS == 0 && CV >= WSETS && CV % 2 == 0 && XS % 2 == 0, "phases are told apart");
   // registers per thread of the warpgroups: roles, weights, sums
-  static constexpr int LAUNCH_REGS = NT == 128 ? 128 : 80;
-  static constexpr int ROLE_REGS = 56, WEIGHT_REGS = NT == 128 ? 88 : 80, SUM_REGS = NT == 128 ? 184 : 104;
+  static constexpr int LAUNCH_REGS = NT == 128 ? 128 : 96;
+  static constexpr int ROLE_REGS = 56, WEIGHT_REGS = 88, SUM_REGS = NT == 128 ? 184 : 160;
   static_assert(ROLE_REGS + WSETS * WEIGHT_REGS + SUM_REGS <= (2 + WSETS) * LAUNCH_REGS, "the split fits the launch");
 };
 

@@ -49,13 +49,14 @@ bool zero_now(void* p, size_t bytes) {
 //
 // Few rows go without tiles where that takes less time, estimated from measurements (us): without tiles
 // 2.5, and the weights at 5 bytes per ps or the products at 36 per ps; with tiles 5, and 0.27 per k-block
-// and wave, or the weights at 6.2 bytes per ps.  4096 x 4096: 1 row 4.2 and 13.2 with tiles, 16 rows 9.6
-// and 13.2, 32 rows 16.5 and 13.3; 8192 x 8192: 1 row 13.6 and 23, 16 rows 32 and 23; 2 rows each for 32
-// groups of 4096 x 4096 134 and 86.  (A group may hold all rows, 16 at a time: M is small then.)
+// and wave, or the weights at 6.2 bytes per ps.  4096 x 4096: 1 row 4.2 and 12.8 with tiles, 16 rows 9.6
+// and 12.8, 32 rows 16.5 and 12.9; 8192 x 8192: 1 row 13.4 and 22, 16 rows 32 and 22; 2 rows each for 32
+// groups of 4096 x 4096 134 and 85.  (A group may hold all rows, 16 at a time: M is small then.)
 //
-// Tiles: pairs where they fill the SMs (2048 x 4096 x 4096 58 and 71 with 128 rows); else by a group's rows (32
-// groups of 4096 x 4096: of 32 rows each 95 at 32 and 107 at 64, of 64 rows 136 and 112), and narrower while
-// one wave holds them (128 x 4096 x 4096: 15 at 32, 17 at 64, 21 at 128; 256 x 4096 x 4096: 24, 18 and 22).
+// Tiles: pairs where they fill the SMs (2048 x 4096 x 4096 58 and 72 with 128 rows); else by a group's rows (32
+// groups of 4096 x 4096: of 32 rows each 94 at 32 and 100 at 64, of 40 rows 128 and 101, of 64 rows 104 at 64
+// and 135 at 128, of 96 rows 167 and 139), and narrower while one wave holds them (128 x 4096 x 4096: 15 at 32,
+// 16 at 64, 21 at 128; 256 x 4096 x 4096: 23, 18 and 22).
 int32_t tile_tokens(int64_t M, int64_t N, int64_t K, int64_t groups, int32_t num_sms) {
   const int64_t parts = std::max<int64_t>(groups, 1), rows = ceil_div(M, parts), kt = ceil_div(K, 128);
   const double weights = static_cast<double>(parts) * N * K;
@@ -70,7 +71,7 @@ int32_t tile_tokens(int64_t M, int64_t N, int64_t K, int64_t groups, int32_t num
   }
   const int64_t wide = ceil_div(M, kInt8WideTokens) * ceil_div(N, 256);
   if (rows > 96 && 2 * wide >= num_sms) return kInt8WideTokens;
-  int32_t t = rows <= 16 ? 16 : rows <= 40 ? 32 : rows <= 96 ? 64 : 128;
+  int32_t t = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   while (t > 16 && parts * ceil_div(rows, t / 2) * ceil_div(N, 128) <= num_sms) t /= 2;
   return t;
 }
