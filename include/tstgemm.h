@@ -582,7 +582,8 @@ tst_status gemm_plan_set_debug(tst_plan *plan, int32_t flags, void *trace_buf, i
  * group (groups * N rows or elements), and the groups' row counts are read from device memory
  * at run time.  Rows of D behind the last group's stay as they were.
  *
- * Conventions as for the other calls; a plan is not re-entrant and belongs to the GPU that
+ * Conventions as for the other calls; a plan is not re-entrant: its runs share a workspace, so on
+ * several streams, or in several graphs, they must follow one another.  It belongs to the GPU that
  * was current when it was made (a run with another current GPU is INVALID_ARG). */
 typedef struct tst_int8_plan tst_int8_plan;
 
@@ -610,7 +611,7 @@ typedef struct {
 /* Errors: INVALID_ARG (null plan or opts, sizes < 1 or beyond int32, groups < 0, an out_dtype
  * other than the two, host_only without num_sms), ALIGNMENT (K not a multiple of 16),
  * UNSUPPORTED (a tile_rows other than those, 192 on one SM, 1 for more than
- * 2^20 rows, M or groups * N beyond 2^31 - 256, K beyond 131056 (the 32-bit sums), more than
+ * 2^20 - 16 rows, M or groups * N beyond 2^31 - 256, K beyond 131056 (the 32-bit sums), more than
  * 512 groups, or a GPU other than sm_103), OOM, CUDA, NO_DEVICE. */
 tst_status gemm_int8_plan_create(tst_int8_plan **plan, int64_t M, int64_t N, int64_t K, const tst_int8_options *opts);
 tst_status gemm_int8_plan_get_info(const tst_int8_plan *plan, tst_int8_plan_info *info);

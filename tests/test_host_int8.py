@@ -20,13 +20,13 @@ def test_plan_rules_and_info():
     for kw, status in ((dict(M=0), invalid), (dict(N=0), invalid), (dict(K=0), invalid), (dict(M=1 << 31), invalid), (dict(groups=-1), invalid),
                        (dict(out_dtype="e4m3"), invalid), (dict(out_dtype=9), invalid), (dict(num_sms=0), invalid), (dict(num_sms=-1), invalid),
                        (dict(timeout_ns=-1), invalid), (dict(tile_rows=-1), invalid), (dict(tile_rows=48), unsupported),
-                       (dict(tile_rows=1, M=(1 << 20) + 1), unsupported),
+                       (dict(tile_rows=1, M=(1 << 20) + 1), unsupported), (dict(tile_rows=1, M=65535 * 16 + 1), unsupported),
                        (dict(tile_rows=192, num_sms=1), unsupported), (dict(K=520), align), (dict(K=131072), unsupported), (dict(groups=513), unsupported),
                        (dict(M=(1 << 31) - 255), unsupported), (dict(N=1 << 23, groups=256), unsupported)):
         with pytest.raises(tst.TstError) as e:
             _plan(**kw)
         assert e.value.status == status, kw
-    _plan(K=131056), _plan(groups=512)
+    _plan(K=131056), _plan(groups=512), _plan(tile_rows=1, M=65535 * 16)
     for rows in (1, 16, 32, 64, 128, 192):
         assert _plan(tile_rows=rows).info.tile_rows == rows
     assert _plan(M=16384, N=4096).info.workspace_bytes >= 2 * 16384 * 512 > _plan(M=8).info.workspace_bytes   # A in FP16

@@ -32,7 +32,7 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 256;   // the last tile's rows
 constexpr int64_t kMaxK = 131056;                        // 131071 products of up to 2^14 fit 32 bits; K is a multiple of 16
 
 constexpr int32_t kFewTokens = 1;                        // tile_rows of the form without tiles
-constexpr int64_t kMaxFewRows = 1 << 20;                 // 16 to a block
+constexpr int64_t kMaxFewRows = 65535 * 16;              // 16 to a block, 65535 blocks in y
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
