@@ -35,8 +35,10 @@
 //               700 at the copy rate: three warpgroups (of 128 tokens: two) take k-blocks in turn.  A
 //               fourth is in the others' way: 16 tokens x 8192 x 8192 in 22.9 us with it, 22.0 without
 // What bounds it: the copy rate while each weight is read once (64 rows over 32 experts of 4096 x 4096 in
-// 85 us, 0.93 of it); else the tensor core, whose eight MMAs of a k-block take 480 cycles of 16 or 32 tokens,
-// 620 of 64 and 910 of 128 (512 x 9728 x 4096, its weights from L2: 72, 49 and 40 us).
+// 85 us, 0.93 of it).  Where tiles of several tokens' rows read it again, from L2 (512 x 9728 x 4096: 72 us in
+// tiles of 32 tokens, 49 of 64, 40 of 128), a k-block takes 460, 610 and 910 cycles, in which all SMs take in
+// 16 TB/s of bytes and FP16 tokens; half of the MMAs left out changes that by 1 to 5 %, the conversion left out
+// by 10 to 20.  2047 ragged rows over 60 experts of 1416 x 2064 take 55 us: six tiles of 17 k-blocks an SM.
 // Every wait is bounded as in the other kernels.
 #pragma once
 #include "gemm_bs_tile.cuh"
