@@ -23,6 +23,7 @@
 #include <cstring>
 #include <new>
 
+#include "int8_params.h"
 #include "kernel_params.h"
 #include "tile_sched.h"
 #include "tstgemm.h"

@@ -42,6 +42,8 @@
 // Every wait is bounded as in the other kernels.
 #pragma once
 #include "gemm_bs_tile.cuh"
+#include "int8_params.h"
+#include "ptx_int8.cuh"
 
 namespace tst {
 

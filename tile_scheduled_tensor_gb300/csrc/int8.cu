@@ -7,7 +7,7 @@
 #include <cstdint>
 #include <new>
 
-#include "kernel_params.h"
+#include "int8_params.h"
 #include "tstgemm.h"
 
 struct tst_int8_plan {
