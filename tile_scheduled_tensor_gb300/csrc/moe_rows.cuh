@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kRowsThreads) dispatch_e4m3_kernel(const RowsP
 // the nearest whole number, ties to even.  amax as above (a NaN or an infinity leaves its mark in the scale).
 // TPT threads hold a token, U pieces of 16 elements each, TPT pieces apart; what a token has beyond them is
 // read again for the values.  Adding 1.5 * 2^23 rounds a value of up to 127 and leaves its two's complement in
-// the low byte.
+// the low byte.  Bound by memory: 16384 BF16 tokens of 4096 to 8 rows each in 101 us in a graph, 0.98 of the copy rate;
+// 8190 FP32 rows of 1424 in 9.0, 0.96; 16 tokens to 8 rows each in 3.6.
 constexpr float kInt8Max = 127.0f;
 template <typename T, bool VEC, int TPT, int U>
 __global__ void __launch_bounds__(TPT < 128 ? 128 : TPT) dispatch_int8_kernel(const RowsParams p) {

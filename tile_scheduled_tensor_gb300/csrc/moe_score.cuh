@@ -12,7 +12,7 @@
 // The choice is discontinuous, and rounded scores would make it depend on how a score was computed.  So
 // it is defined on FP64 values, and computed in FP32 with a bound on the error: where two values that
 // decide something (the choice, its order, the last group kept) lie within the bound of each other, and
-// are not the same logit with the same bias, the row is chosen again in FP64 (choose_exact).
+// are not the same logit with the same bias, the row is chosen again by their FP64 values (late_row).
 //
 // A row is held by a warp, 32 / G lanes per group (G rounded up to a power of two), so that a group's
 // largest values are found by exchanges among its own lanes.  Counts, ranks and offsets as in
@@ -482,7 +482,9 @@ __device__ __noinline__ void late_row(const ScoreParams& p, const float* bias, u
 // A warp per row, with the candidate list of route_rows_kernel on the values c.  Rows that it leaves open (values too
 // close, more than the list holds, a NaN, and every row where a bias is a NaN or +inf) are marked, and chosen by
 // late_row once all others are done: so the rows that come through carry no call (with calls between them, whose
-// registers are then spilled around them, 30 us more of 150).  What bounds it is issue slots, as in route_rows_kernel.
+// registers are then spilled around them, 30 us more of 150).  What bounds it is issue slots, as in route_rows_kernel:
+// 131071 x 256 FP32, 4 of 8 groups, k 8, takes 147 us in a graph with the two launches after it, 138 of them here, in
+// 855 instructions a row at 0.74 of the slots; without groups 115.
 template <typename T, int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL == 16 ? 2 : 1)
     score_rows_kernel(const __grid_constant__ ScoreParams p) {
@@ -730,7 +732,10 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
 //   u_e = p_e (g_e - <p, g>), g_e = dL coef E c_e / (R n), and at the chosen experts
 //   + f q_j (dw_j - <q, dw>), q = s / sum_S s   (normalized)   or   + f s_j dw_j,
 //   sigmoid: d_l = u (1 - s);  softmax: d_l = u - p sum u.
-// A warp per row; the chosen experts' parts pass through shared memory to the lanes that hold them.
+// A warp per row; the chosen experts' parts pass through shared memory to the lanes that hold them.  The scores are
+// computed twice, for the sums and for the gradient, which costs less than registers for them (spilled at 64).  Bound by
+// issue slots, 504 instructions a row at 0.67 of them, then by its bytes: 65536 x 256 FP32 in 42 us in a graph, 0.48 of the
+// copy rate (48 with the sums over the lanes one after another and the choice read when it was needed).
 template <typename T, int VPL, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads, VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) score_grad_kernel(const ScoreGradParams p) {
   using Map = ScoreMap<T, VPL>;
