@@ -238,43 +238,61 @@ struct alignas(16) Ranked {
   }
 };
 
+// FP64 numbers as integers of the same order, and back: comparisons in integers, as one in FP64 takes an SM 16 cycles
+// (131071 x 256 zeros in 4 of 8 groups, each row chosen here: 2.3 ms with those and an exponential per expert, 0.7 so).
+__device__ __forceinline__ long long order64(double x) {
+  const long long b = __double_as_longlong(x);
+  return b ^ ((b >> 63) & 0x7FFFFFFFFFFFFFFFll);
+}
+__device__ __forceinline__ double value64(long long k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7FFFFFFFFFFFFFFFll)); }
+constexpr long long kShut64 = static_cast<long long>(0x800FFFFFFFFFFFFFull);   // order64(-inf)
+
 // Whether the lane's group stays, on FP64 values as defined, of which `need` has those of the lane that may be among its
-// group's largest two.  (Loops that are not unrolled: this runs for one row in thousands, and much of the time of such
-// a row is that of fetching its code.)
+// group's largest two.  Where all of them come of one logit and one bias, one exponential serves.  (Loops that are not
+// unrolled: this runs for one row in thousands, and much of the time of such a row is that of fetching its code.)
 template <typename T, int VPL>
 __device__ __noinline__ bool choose_groups(const ScoreParams& p, const T* src, uint32_t need) {
   const int lane = threadIdx.x & 31;
   const ScoreMap<T, VPL> map(lane, p.lanes, p.size, p.groups);
-  const double shut = -__longlong_as_double(0x7FF0000000000000ll);
+  auto logit_at = [&](int v) { return logit_value<T>(src[map.expert(v)]); };
+  auto bias_at = [&](int v) { return p.bias != nullptr ? p.bias[map.expert(v)] : 0.0f; };
   double peak = 0.0, sum = 1.0;
   if (!p.sigmoid) softmax_exact<T, VPL>(p, map, src, peak, sum);
-  double a = shut, b = shut;   // the largest two
+  const int one = __ffs(__ballot_sync(kFullMask, need != 0u)) - 1;   // (an expert is open)
+  const float x0 = __shfl_sync(kFullMask, need != 0u ? logit_at(__ffs(need) - 1) : 0.0f, one);
+  const float b0 = __shfl_sync(kFullMask, need != 0u ? bias_at(__ffs(need) - 1) : 0.0f, one);
+  bool same = true;
+#pragma unroll 1
+  for (uint32_t left = need; left != 0u; left &= left - 1u) same = same && logit_at(__ffs(left) - 1) == x0 && bias_at(__ffs(left) - 1) == b0;
+  same = __all_sync(kFullMask, same);
+  auto key = [&](float x, float bias) {
+    const double s = score_exact(p.sigmoid, x, peak, sum);
+    return order64(p.bias != nullptr ? s + static_cast<double>(bias) : s);
+  };
+  const long long all = same ? key(x0, b0) : 0;
+  long long a = kShut64, b = kShut64;   // the largest two
 #pragma unroll 1
   for (; __any_sync(kFullMask, need != 0u); need &= need - 1u) {
-    double c = shut;
-    if (need != 0u) {
-      const int e = map.expert(__ffs(need) - 1);
-      c = score_exact(p.sigmoid, logit_value<T>(src[e]), peak, sum);
-      if (p.bias != nullptr) c += static_cast<double>(p.bias[e]);
-    }
-    b = fmax(b, fmin(a, c));
-    a = fmax(a, c);
+    long long c = kShut64;
+    if (need != 0u) c = same ? all : key(logit_at(__ffs(need) - 1), bias_at(__ffs(need) - 1));
+    b = max(b, min(a, c));
+    a = max(a, c);
   }
 #pragma unroll 1
   for (int d = p.lanes >> 1; d > 0; d >>= 1) {
-    const double oa = __shfl_xor_sync(kFullMask, a, d), ob = __shfl_xor_sync(kFullMask, b, d);
-    b = fmax(fmin(a, oa), fmax(b, ob));
-    a = fmax(a, oa);
+    const long long oa = __shfl_xor_sync(kFullMask, a, d), ob = __shfl_xor_sync(kFullMask, b, d);
+    b = max(min(a, oa), max(b, ob));
+    a = max(a, oa);
   }
-  const double mine = p.best == 2 && b != shut ? a + b : a;
+  const long long mine = p.best == 2 && b != kShut64 ? order64(value64(a) + value64(b)) : a;
   const int g = lane / p.lanes;
   int rank = 0;
 #pragma unroll 1
   for (int i = 0; i < p.groups; ++i) {
-    const double o = __shfl_sync(kFullMask, mine, i * p.lanes);
+    const long long o = __shfl_sync(kFullMask, mine, i * p.lanes);
     rank += o > mine || (o == mine && i < g) ? 1 : 0;
   }
-  return rank < p.top_groups && mine != shut;
+  return rank < p.top_groups && mine != kShut64;
 }
 
 // The order of at most 32 listed experts (lane i holds the i-th) on FP64 values as defined: the lane's place.
@@ -283,12 +301,13 @@ __device__ __noinline__ int choose_listed(const ScoreParams& p, const T* src, in
   const int lane = threadIdx.x & 31;
   double peak = 0.0, sum = 1.0;
   if (!p.sigmoid) softmax_exact<T, VPL>(p, ScoreMap<T, VPL>(lane, p.lanes, p.size, p.groups), src, peak, sum);
-  double c = score_exact(p.sigmoid, mine.logit, peak, sum);
-  if (p.bias != nullptr) c += static_cast<double>(mine.bias);
+  double s = score_exact(p.sigmoid, mine.logit, peak, sum);
+  if (p.bias != nullptr) s += static_cast<double>(mine.bias);
+  const long long c = order64(s);
   int rank = 0;
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    const double o = __shfl_sync(kFullMask, c, i);
+    const long long o = __shfl_sync(kFullMask, c, i);
     const int at = __shfl_sync(kFullMask, mine.expert, i);
     rank += o > c || (o == c && at < mine.expert) ? 1 : 0;
   }
