@@ -98,6 +98,53 @@ def test_route_equals_the_oracle(T, E, k, G, g, best, dtype, score):
         _check(_route(plan, logits, None if bias is None else _dev(bias)), want, l)
 
 
+def _settled(l, bias, G, g):
+    """Rows whose kept groups, by sums of two softmax scores, do not hang on a rounding.  (x + b) + (y + d) and (x + d) + (y + b) are one number
+    and two roundings of it: scores are within 2 u' of the formula's (u' = 2^-53, values up to 2), the sums add
+    2 u' each, so values within 2^-48 = 32 u' of the last one kept have to come of the same logits and biases."""
+    size, out = l.shape[1] // G, np.ones(len(l), dtype=np.uint8)
+    for t in range(len(l)):
+        c = np.where(l[t] > -np.inf, moe.scores(l[t], False) + bias, -np.inf)
+        best = [sorted(range(i * size, (i + 1) * size), key=lambda e: (-c[e], e))[:2] for i in range(G)]
+        groups = sorted(((sum(c[e] for e in b if c[e] > -np.inf), sorted((l[t, e], bias[e]) for e in b if c[e] > -np.inf))
+                         for b in best if c[b[0]] > -np.inf), key=lambda v: -v[0])
+        if len(groups) > g:
+            value, of = groups[g - 1]
+            out[t] = all(o == of for v, o in groups if abs(v - value) < 2.0 ** -48)
+    return out
+
+
+@pytest.mark.parametrize("E,k,G,g,best", [(256, 8, 8, 4, 2), (64, 6, 8, 3, 1), (60, 4, 5, 2, 2), (48, 5, 16, 7, 2), (96, 32, 1, 1, 1), (20, 3, 1, 1, 1)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("kind", ["zeros", "levels", "closed", "saturated"])
+def test_rows_whose_values_tie_or_nearly(E, k, G, g, best, score, kind):
+    """Choices among equal values and among neighbours in FP32: every row is chosen by FP64 values, or by rounds where
+    more than the list holds are in reach.  Two levels a row, so that different sums of two are steps apart."""
+    rng = np.random.default_rng(E + G + len(kind))
+    T = 150
+    l = np.zeros((T, E))
+    if kind in ("levels", "closed"):
+        base = np.float32(rng.normal(size=(T, 1)))
+        l = np.where(rng.random((T, E)) < 0.5, base, np.nextafter(base, np.float32(9))).astype(np.float64)
+    if kind == "closed":   # groups with one open expert, or none
+        l[rng.random((T, E)) < rng.choice([0.5, 0.9, 0.97], (T, 1))] = -np.inf
+    if kind == "saturated":   # 1 / (1 + e^-l) is 1 in FP64 from 37 on
+        l = rng.choice([36.0, 38.0, 50.0], (T, E))
+    biases = [None, np.zeros(E), np.full(E, -0.75), rng.choice([-0.25, 0.0, 0.25], E)]
+    if best == 2 and kind in ("levels", "closed"):   # (x + b) + (y + d) and (x + d) + (y + b) are apart by their roundings alone
+        biases.pop()
+    for bias in biases:
+        bias = None if bias is None else bias.astype(np.float32)
+        logits = _dev(l)
+        plan = tst.moe_plan_create(T, E, k, normalize=False, score=score, groups=G, top_groups=g, group_best=best, balance_coef=0.5)
+        mask = np.ones(T, dtype=np.uint8)
+        if best == 2 and score == "softmax":   # (the sigmoids here have one rounding: 1/2, 1 and 1 - 2^-52, or two levels)
+            mask = _settled(l, np.zeros(E) if bias is None else bias.astype(np.float64), G, g)
+        assert mask.sum() >= T // 2
+        want = moe.route_scored(_host(logits), k, score == "sigmoid", bias, G, g, best, False, 1.0, 0.5, mask=mask)
+        _check(_route(plan, logits, None if bias is None else _dev(bias), mask=torch.from_numpy(mask).cuda()), want, _host(logits))
+
+
 @pytest.mark.parametrize("T", [31, 32, 33, 2000, 4865, 9728, 19457])
 def test_many_chunks(T):
     E, k = 24, 3

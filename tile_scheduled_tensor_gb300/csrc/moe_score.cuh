@@ -239,7 +239,7 @@ struct alignas(16) Ranked {
 };
 
 // FP64 numbers as integers of the same order, and back: comparisons in integers, as one in FP64 takes an SM 16 cycles
-// (131071 x 256 zeros in 4 of 8 groups, each row chosen here: 2.3 ms with those and an exponential per expert, 0.7 so).
+// (131071 x 256 zeros in 4 of 8 groups, each row chosen here: 2.3 ms with those and an exponential per expert, 0.8 so).
 __device__ __forceinline__ long long order64(double x) {
   const long long b = __double_as_longlong(x);
   return b ^ ((b >> 63) & 0x7FFFFFFFFFFFFFFFll);
@@ -420,7 +420,7 @@ __device__ __noinline__ void late_row(const ScoreParams& p, const float* bias, u
   if (!sigmoid) largest = fminf(1.0f, 1.1f * inv);
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
-    c[v] = c[v] * inv + (map.has(v) ? bias[map.expert(v)] : 0.0f);   // -inf stays
+    c[v] = __fadd_rn(__fmul_rn(c[v], inv), map.has(v) ? bias[map.expert(v)] : 0.0f);   // -inf stays
     own = fmaxf(own, c[v]);
   }
   Ranked me = {closed_logit(), closed_logit(), 0.0f, -1};   // lane j: the j-th
@@ -486,7 +486,16 @@ __device__ __noinline__ void late_row(const ScoreParams& p, const float* bias, u
       n = choose_rounds<T, VPL>(map, src, bias, k, c, me);
       const Ranked after = {__shfl_down_sync(kFullMask, me.c, 1), __shfl_down_sync(kFullMask, me.logit, 1),
                             __shfl_down_sync(kFullMask, me.bias, 1), 0};
-      exact = __any_sync(kFullMask, lane < k && lane + 1 < n && (lane == 31 || me.near(after, sigmoid)));   // 32 choices: the 33rd has no lane
+      bool unsure = lane < k && lane + 1 < n && (lane == 31 || me.near(after, sigmoid));   // 32 choices: the 33rd has no lane
+      // what is left within reach of the last choice has to be of its logit and bias
+      const float last = __shfl_sync(kFullMask, me.c, k - 1), last_logit = __shfl_sync(kFullMask, me.logit, k - 1);
+      const float last_bias = __shfl_sync(kFullMask, me.bias, k - 1);
+      const float reach = last - score_gap(sigmoid, largest, last);
+#pragma unroll
+      for (int v = 0; v < VPL; ++v)
+        if (n > k && c[v] >= reach && c[v] != closed_logit())
+          unsure = unsure || logit_value<T>(src[map.expert(v)]) != last_logit || bias[map.expert(v)] != last_bias;
+      exact = __any_sync(kFullMask, unsure);
     }
   }
   if (exact) {
@@ -599,8 +608,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
       const float inv = some ? __fdividef(1.0f, sum) : 0.0f;   // sum <= 1075
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        c[v] *= inv;
-        acc[v] += c[v];
+        c[v] = __fmul_rn(c[v], inv);   // not fused with the bias for some experts and not for others: one logit and bias
+        acc[v] += c[v];                // have one value
       }
       largest = fminf(1.0f, 1.1f * inv);
     }
@@ -618,12 +627,12 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
           if (map.has(q * Map::W)) {
             const Biases b = *reinterpret_cast<const Biases*>(bias + map.expert(q * Map::W));
 #pragma unroll
-            for (int i = 0; i < Map::W; ++i) c[q * Map::W + i] += b.v[i];
+            for (int i = 0; i < Map::W; ++i) c[q * Map::W + i] = __fadd_rn(c[q * Map::W + i], b.v[i]);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < Map::W; ++i)
-            if (map.has(q * Map::W + i)) c[q * Map::W + i] += bias[map.expert(q * Map::W + i)];
+            if (map.has(q * Map::W + i)) c[q * Map::W + i] = __fadd_rn(c[q * Map::W + i], bias[map.expert(q * Map::W + i)]);
         }
       }
     }
@@ -717,7 +726,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
         }
         __syncwarp();
         if (lane < n) me = ranked[warp][lane];
-        near = __any_sync(kFullMask, lane < k && lane + 1 < n && me.near(ranked[warp][lane + 1 < n ? lane + 1 : lane], sigmoid));
+        // neighbours behind the k-th too: one there may belong before several of one logit and bias
+        near = __any_sync(kFullMask, lane + 1 < n && me.near(ranked[warp][lane + 1 < n ? lane + 1 : lane], sigmoid));
       }
       __syncwarp();
     }
