@@ -662,7 +662,11 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
         if (p.best == 2) b = fmaxf(fminf(a, oa), fmaxf(b, __shfl_xor_sync(kFullMask, b, d)));
         a = fmaxf(a, oa);
       }
-      const float mine = p.best == 2 ? select(b != closed_logit(), a + b, a) : a;   // closed for a lane without a group
+      const float second = p.best == 2 ? select(b != closed_logit(), b, 0.0f) : 0.0f;
+      const float mine = a + second;   // closed for a lane without a group
+      // what it may be off by goes with the summands, of which a sum of opposite signs keeps nothing: half of a pair's
+      // distance for each of two scores, u (|a| + |b|) for the biases, and that again for the sum
+      const float off = score_gap(sigmoid, largest, fabsf(a) + fabsf(second));
       // the last value kept, by rounds; equal values are left to choose_groups
       float left = mine, last = warp_max(left);
       for (int j = 1; j < p.top_groups; ++j) {
@@ -672,9 +676,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
         last = m;
       }
       kept = mine >= last && mine != closed_logit();
-      const float first = warp_max(select(kept, closed_logit(), mine)), most = fmaxf(fabsf(last), fabsf(first));
-      groups_near = __popc(__ballot_sync(kFullMask, kept)) > p.top_groups * p.lanes ||
-                    (first != closed_logit() && !(last - first > 2.0f * score_gap(sigmoid, largest, most)));
+      const float least = -warp_max(select(kept, off - mine, closed_logit()));   // of the kept, and the most of the others
+      const float first = warp_max(select(kept || mine == closed_logit(), closed_logit(), mine + off));
+      groups_near = __popc(__ballot_sync(kFullMask, kept)) > p.top_groups * p.lanes || (first != closed_logit() && !(least > first));
       near = near || groups_near;
       own = select(kept, own, closed_logit());
     } else {
