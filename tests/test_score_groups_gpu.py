@@ -53,3 +53,38 @@ def test_a_group_of_opposite_signs_beside_one_without_biases():
     l = np.array([[8e-5, 0.0, 2e-5, 0.0], [2e-5, 0.0, 8e-5, 0.0], [0.0, 8e-5, 0.0, 2e-5]])
     want = _compare(l, np.array([1000.0, -1000.0, 0.0, 0.0], np.float32), "sigmoid", 1, 2, 1, 2)
     assert want["expert"][:, 0].tolist() == [0, 2, 0]
+
+
+def _lowest(E, *off, value=LOWEST):
+    bias = np.zeros(E, np.float32)
+    for part in off:
+        bias[part] = value
+    return bias
+
+
+# the second group held off: its experts come last; two of three groups; all; one expert of each group left; a part of one
+LOW = [(8, 6, 2, 2, _lowest(8, slice(4, 8))), (8, 8, 2, 2, _lowest(8, slice(0, 4))), (12, 5, 3, 2, _lowest(12, slice(0, 8))),
+       (12, 4, 3, 1, _lowest(12, slice(0, 12))), (64, 16, 8, 4, _lowest(64, *[slice(i + 1, i + 8) for i in range(0, 64, 8)])),
+       (256, 20, 8, 4, _lowest(256, slice(0, 160), slice(170, 255))), (256, 8, 8, 4, _lowest(256, slice(0, 3), slice(100, 108)))]
+
+
+@pytest.mark.parametrize("E,k,G,g,bias", LOW, ids=[f"{c[0]}-{i}" for i, c in enumerate(LOW)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("T", [40, 5000])
+def test_biases_of_the_lowest_value(E, k, G, g, bias, score, best, T):
+    # a group's sum of two is beyond FP32, its experts are not closed
+    want = _compare(np.random.default_rng(E + G).normal(size=(T, E)), bias, score, k, G, g, best)
+    assert (want["expert"] >= 0).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_sums_beyond_fp32_keep_their_order(score):
+    # -6e38, -4e38, -6.8e38 and -5e38 for the groups; and the same above zero
+    size = np.repeat(np.array([3e38, 2e38, 3.4e38, 2.5e38]), 4)
+    l = np.random.default_rng(3).normal(size=(50, 16))
+    for bias in ((-size).astype(np.float32), size.astype(np.float32)):
+        for g in (1, 2, 3):
+            want = _compare(l, bias, score, 4, 4, g, 2)
+            first = 4 if bias[0] < 0 else 8
+            assert (want["expert"] // 4 == first // 4).all()

@@ -108,6 +108,7 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
 __device__ __forceinline__ float shifted_sigmoid(float x, float m) {
   return x >= 0.0f ? Sigmoid(x).s : __fdividef(__expf(x - fminf(m, 0.0f)), 1.0f + __expf(x));
 }
+constexpr float kLowest = -3.4028235e38f;
 constexpr float kLeastSum = 8.6736174e-19f;   // 2^-60: sums of sigmoids below this are taken again with a shift
 
 // Sums (not maxima) of a group: at least this far apart, two values computed in FP32 are in the order of
@@ -442,7 +443,7 @@ __device__ __noinline__ void late_row(const ScoreParams& p, const float* bias, u
         a = fmaxf(a, oa);
       }
       const float least = p.best == 2 && b != closed_logit() ? b : a;
-      const float reach = fmaxf(least - 2.0f * score_gap(sigmoid, largest, least), -3.4028235e38f);
+      const float reach = fmaxf(least - 2.0f * score_gap(sigmoid, largest, least), kLowest);
       uint32_t need = 0u;
 #pragma unroll
       for (int v = 0; v < VPL; ++v) need |= (c[v] >= reach ? 1u : 0u) << v;
@@ -459,7 +460,7 @@ __device__ __noinline__ void late_row(const ScoreParams& p, const float* bias, u
       own = own == bound ? closed_logit() : own;
       bound = warp_max(own);
     }
-    bound = fmaxf(bound - 2.0f * score_gap(sigmoid, largest, bound), -3.4028235e38f);
+    bound = fmaxf(bound - 2.0f * score_gap(sigmoid, largest, bound), kLowest);
     const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
@@ -663,10 +664,11 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
         a = fmaxf(a, oa);
       }
       const float second = p.best == 2 ? select(b != closed_logit(), b, 0.0f) : 0.0f;
-      const float mine = a + second;   // closed for a lane without a group
+      // closed for a lane without a group; sums beyond FP32 equal its lowest value, as no open group is closed
+      const float mine = fmaxf(a + second, fminf(a, kLowest));
       // what it may be off by goes with the summands, of which a sum of opposite signs keeps nothing: half of a pair's
       // distance for each of two scores, u (|a| + |b|) for the biases, and that again for the sum
-      const float off = score_gap(sigmoid, largest, fabsf(a) + fabsf(second));
+      const float off = score_gap(sigmoid, largest, a) + score_gap(sigmoid, 0.0f, second);
       // the last value kept, by rounds; equal values are left to choose_groups
       float left = mine, last = warp_max(left);
       for (int j = 1; j < p.top_groups; ++j) {
@@ -694,7 +696,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
         bound = warp_max(own);
       }
       // what is listed: all that may reach the bound; a closed expert reaches none
-      bound = fmaxf(bound - 2.0f * score_gap(sigmoid, largest, bound), -3.4028235e38f);
+      bound = fmaxf(bound - 2.0f * score_gap(sigmoid, largest, bound), kLowest);
       bound = select(kept, bound, __uint_as_float(0x7F800000u));   // (no value is +inf here)
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
