@@ -593,7 +593,8 @@ typedef struct {
     int32_t has_bias;    /* 1: bias is FP32[N], grouped FP32[groups * N] */
     int32_t relu;        /* 1: max(z, 0), a NaN stays */
     int32_t host_only;   /* 1: no GPU (the runs then fail with TST_ERR_NO_DEVICE); num_sms must be set */
-    int32_t num_sms;     /* SMs to use: 0 = all */
+    int32_t num_sms;     /* SMs that compute tiles: 0 = all.  The copy of A that tiles start from, and the form without
+                            tiles, are spread over the GPU */
     int32_t tile_rows;   /* rows of A per tile: 0 = choose, else 16, 32, 64, 128, or 192 (CTA pairs), or 1:
                             no tiles, for few rows (of each group).  No choice changes a bit of D. */
     int64_t timeout_ns;  /* limit of every device-side wait: 0 = 10 s */

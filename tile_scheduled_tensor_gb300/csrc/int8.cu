@@ -70,7 +70,7 @@ int32_t tile_tokens(int64_t M, int64_t N, int64_t K, int64_t groups, int32_t num
     if (few < tiled) return kFewTokens;
   }
   const int64_t wide = ceil_div(M, kInt8WideTokens) * ceil_div(N, 256);
-  if (rows > 96 && 2 * wide >= num_sms) return kInt8WideTokens;
+  if (num_sms > 1 && rows > 96 && 2 * wide >= num_sms) return kInt8WideTokens;
   int32_t t = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   while (t > 16 && parts * ceil_div(rows, t / 2) * ceil_div(N, 128) <= num_sms) t /= 2;
   return t;
