@@ -603,8 +603,8 @@ typedef struct {
 typedef struct {
     int64_t M, N, K;
     int32_t groups;
-    int32_t tile_rows, tile_cols;   /* rows of A (tokens) and columns of D per tile; 1: no tiles */
-    int32_t grid;                   /* CTAs of tiles launched */
+    int32_t tile_rows, tile_cols;   /* rows of A (tokens) and columns of D per tile; 1 and 0: no tiles */
+    int32_t grid;                   /* CTAs of tiles launched; 0: no tiles */
     int32_t smem_bytes;             /* dynamic shared memory per CTA */
     int64_t workspace_bytes;        /* device bytes owned by the plan: A in FP16, 2 M K, but for tile_rows 1 */
 } tst_int8_plan_info;
@@ -613,7 +613,8 @@ typedef struct {
  * other than the two, host_only without num_sms), ALIGNMENT (K not a multiple of 16),
  * UNSUPPORTED (a tile_rows other than those, 192 on one SM, 1 for more than
  * 2^20 - 16 rows, M or groups * N beyond 2^31 - 256, K beyond 131056 (the 32-bit sums), more than
- * 512 groups, or a GPU other than sm_103), OOM, CUDA, NO_DEVICE. */
+ * 512 groups, 2^30 tiles or more (a row of tiles more counted for each group), or a GPU other than
+ * sm_103), OOM, CUDA, NO_DEVICE. */
 tst_status gemm_int8_plan_create(tst_int8_plan **plan, int64_t M, int64_t N, int64_t K, const tst_int8_options *opts);
 tst_status gemm_int8_plan_get_info(const tst_int8_plan *plan, tst_int8_plan_info *info);
 /* NULL is accepted. */

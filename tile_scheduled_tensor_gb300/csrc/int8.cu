@@ -123,12 +123,12 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   p->tokens = tokens;
   p->pairs = tokens == kInt8WideTokens;
   const bool pairs = p->pairs;
-  const int32_t cols = pairs ? 256 : 128;
-  const int64_t mt = ceil_div(M, tokens), nt = ceil_div(N, cols);
-  const int64_t tiles = (mt + groups) * nt;   // grouped: at most, whatever the split
+  const bool few = tokens == kFewTokens;
+  const int32_t cols = few ? 0 : pairs ? 256 : 128;
+  const int64_t mt = few ? 0 : ceil_div(M, tokens), nt = few ? 0 : ceil_div(N, cols);
+  const int64_t tiles = (mt + groups) * nt;   // grouped: at most, whatever the split; none without tiles
   if (tiles >= (int64_t(1) << 30)) { delete p; return TST_ERR_UNSUPPORTED; }
   const int64_t kt = ceil_div(K, 128);
-  const bool few = tokens == kFewTokens;
   if (!few) p->kernel = tst_int8_kernel(tokens, opts->out_dtype == TST_OUT_BF16 ? tst::OUT_BF16 : tst::OUT_F32);
   p->dev_bytes = 256 + (few ? 0 : 2 * static_cast<size_t>(M) * K);
   if (!opts->host_only) {
@@ -157,7 +157,7 @@ tst_status gemm_int8_plan_create(tst_int8_plan** out, int64_t M, int64_t N, int6
   s.group = 8;
   s.dp_tiles = static_cast<int32_t>(mt * nt);
   s.grid = static_cast<int32_t>(std::min<int64_t>(p->num_sms / (pairs ? 2 : 1), tiles));
-  if (s.grid < 1) s.grid = 1;
+  if (!few && s.grid < 1) s.grid = 1;
   s.sk_groups = 1;
   s.rows = static_cast<int32_t>(M);
   s.bm = tokens;
