@@ -115,7 +115,7 @@ __device__ __forceinline__ void place_chunk(const RouteParams& p, const int32_t*
 // After route_scan_kernel.  The last block writes R and the loss too.  (No chunks: counts, totals and
 // loss of no tokens.)
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteParams p) {
-  extern __shared__ uint32_t route_smem[];
+  extern __shared__ __align__(16) uint32_t route_smem[];
   int32_t* first = reinterpret_cast<int32_t*>(route_smem);   // E
   ptx::griddep_wait();
   for (int e = threadIdx.x; e < p.experts; e += kRouteThreads)
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteP
 // launch of its own for the prefix sums.
 constexpr int kFewChunks = 16;
 __global__ void __launch_bounds__(kRouteThreads) route_sum_place_kernel(const RouteParams p) {
-  extern __shared__ uint32_t route_smem[];
+  extern __shared__ __align__(16) uint32_t route_smem[];
   const int E = p.experts;
   int32_t* first = reinterpret_cast<int32_t*>(route_smem);            // E
   int32_t* total = first + E;                                         // E + 1: counts, live rows

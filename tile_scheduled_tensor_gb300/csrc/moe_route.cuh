@@ -348,7 +348,7 @@ struct alignas(8) Candidate {
 template <typename T, int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL == 16 ? 2 : 1) route_rows_kernel(const RouteParams p) {
   using Map = RowMap<T, VPL>;
-  extern __shared__ uint32_t route_smem[];
+  extern __shared__ __align__(16) uint32_t route_smem[];
   __shared__ alignas(16) Candidate list[WARPS][kRouteCandidates + 4];   // and up to 4 that come last
   const int E = p.experts, k = p.top_k, words = p.chunk / 32;
   const RouteShared s(route_smem, E, words, WARPS);
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL
 // 60000 x 32 in 22 us, 131071 x 8 in 14 us, the two launches after it included.
 template <typename T, int EM, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads) route_rows_small_kernel(const RouteParams p) {
-  extern __shared__ uint32_t route_smem[];
+  extern __shared__ __align__(16) uint32_t route_smem[];
   const int E = p.experts, k = p.top_k, words = p.chunk / 32, warps = words;
   const RouteShared s(route_smem, E, words, warps);
   const int pitch = k | 1;   // odd: a warp's threads write distinct banks

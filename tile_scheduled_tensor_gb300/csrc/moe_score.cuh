@@ -518,7 +518,7 @@ template <typename T, int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL == 16 ? 2 : 1)
     score_rows_kernel(const __grid_constant__ ScoreParams p) {
   using Map = ScoreMap<T, VPL>;
-  extern __shared__ uint32_t route_smem[];
+  extern __shared__ __align__(16) uint32_t route_smem[];
   __shared__ Ranked list[WARPS][kRouteCandidates + 1];   // and one place for what is too much
   __shared__ Ranked ranked[WARPS][kRouteCandidates];
   __shared__ alignas(16) float listed[WARPS][kRouteCandidates];
