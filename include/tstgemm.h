@@ -726,8 +726,9 @@ tst_status moe_route(tst_moe_plan *plan, int64_t tokens, const void *logits, int
                      int32_t *totals, float *loss, void *stream);
 
 /* The same by scores, for a plan of moe_plan_create_scored.  With s = 1 / (1 + e^-l), or the softmax of the
- * open logits, and c = s + bias[e] (bias: FP32[experts], NULL: 0), computed as FP64 values, a NaN counting
- * as +inf:
+ * open logits, and c = s + bias[e] (bias: FP32[experts], NULL: none), computed as FP64 values, a NaN counting
+ * as +inf (a softmax without a bias is compared before its division, c = e^(l - the row's largest), so that
+ * scores which differ do not become equal by it):
  *
  *   group value   the sum of the group_best largest c of the group's open experts (of fewer where
  *                 fewer are open); the top_groups groups of the largest values stay (ties: the

@@ -194,6 +194,8 @@ def route_scored(logits, top_k, sigmoid, bias=None, groups=1, top_groups=1, best
         s = scores(l[t], sigmoid)
         with np.errstate(invalid="ignore"):
             c = s + b
+            if bias is None and not sigmoid and not np.isnan(s).any():
+                c = np.exp(l[t] - l[t].max())   # compared before the division
         c = np.where(np.isnan(c), np.inf, c)
         c[~open_] = -np.inf
         prob += np.where(open_, shares(l[t], sigmoid), 0.0)

@@ -2,7 +2,8 @@
 // scaled weights; and the gradient of the logits.
 //
 //   s_te = 1 / (1 + e^-l_te),  or  e^l_te / sum_open e^l      over the open experts (-inf logits are closed)
-//   c_te = s_te + b_e          as an FP64 value; a NaN counts as +inf; c = -inf is never chosen
+//   c_te = s_te + b_e          as an FP64 value; a NaN counts as +inf; c = -inf is never chosen (a softmax without
+//                              a bias: e^(l - max), the sum being the row's)
 //   group g = S adjacent experts, its value the sum of its 1 or 2 largest c; the top_groups groups of
 //   the largest values stay (ties: the lower group)
 //   S_t = the k largest c among them                          (ties: the lower expert)
@@ -149,6 +150,7 @@ __device__ __noinline__ int choose_exact(const ScoreParams& p, const T* src, int
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+    if (p.bias == nullptr && sum == sum) sum = 1.0;   // as softmax_exact
   }
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
@@ -208,7 +210,7 @@ __device__ __forceinline__ double score_exact(bool sigmoid, float x, double peak
   const double e = exp(sigmoid ? -static_cast<double>(x) : static_cast<double>(x) - peak);
   return (sigmoid ? 1.0 : e) / (sigmoid ? 1.0 + e : sum);
 }
-// Softmax's top and sum.  Without a bias the scores are compared before the division, which all share: a sum of 1.
+// Softmax's top and sum.  Without a bias the scores are compared as defined, before the division: a sum of 1.
 template <typename T, int VPL>
 __device__ __forceinline__ void softmax_exact(const ScoreParams& p, const ScoreMap<T, VPL>& map, const T* src, double& peak, double& sum) {
   float x[VPL], top = closed_logit();
