@@ -628,8 +628,8 @@ tst_status gemm_int8_run(tst_int8_plan *plan, const int32_t *group_rows, const i
                          const float *row_scale, const float *col_scale, const float *bias, void *stream);
 
 /* What the runs since the last query recorded on the device: TST_OK, TST_ERR_TIMEOUT (a bounded
- * wait ran out) or TST_ERR_DEVICE_CHECK (the groups' rows add up to more than M: rows past M are
- * not computed).  Synchronises the last run's stream. */
+ * wait ran out: D is not complete) or TST_ERR_DEVICE_CHECK (the groups' rows add up to more than M:
+ * rows past M are not computed).  Synchronises the last run's stream. */
 tst_status gemm_int8_status_query(tst_int8_plan *plan);
 
 /* ---------------------------------------------------------------- mixture of experts

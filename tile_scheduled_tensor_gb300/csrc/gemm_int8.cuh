@@ -141,14 +141,34 @@ struct RingAt {
   }
 };
 
-// bounded wait until the copies of an aborting producer have landed
+// What a CTA has in flight, copies and MMAs, ends before the CTA does, also where a wait of another role ran out: limits of
+// a plan may be shorter than a copy takes, so these waits have at least 100 ms.
+__device__ __forceinline__ uint64_t int8_end_limit(const KernelParams& p) {
+  constexpr uint64_t kLeast = 100ull * 1000 * 1000;
+  return p.timeout_ns > kLeast ? p.timeout_ns : kLeast;
+}
+
+// bounded wait until the copies of a producer have landed: of every one that leaves, as the roles that would wait for them
+// may have given up
 template <int N>
 __device__ __forceinline__ void int8_land(const KernelParams& p, uint32_t full, uint32_t issued, uint32_t parity) {
-  const uint64_t t0 = ptx::globaltimer();
+  const uint64_t t0 = ptx::globaltimer(), limit = int8_end_limit(p);
   for (int s = 0; s < N; ++s) {
     if (!(issued & (1u << s))) continue;
     while (!ptx::mbar_try_wait(full + 8 * s, (parity >> s) & 1u))
-      if (ptx::globaltimer() - t0 > p.timeout_ns) return;
+      if (ptx::globaltimer() - t0 > limit) break;
+  }
+}
+
+// The same for the MMAs, which a commit to `drain` follows.
+template <int CG>
+__device__ __forceinline__ void int8_drain(const KernelParams& p, const Ctx& c, uint32_t drain) {
+  const uint64_t t0 = ptx::globaltimer(), limit = int8_end_limit(p);
+  while (!ptx::mbar_try_wait(drain, 0)) {
+    if (ptx::globaltimer() - t0 > limit) {
+      raise_error<CG>(p, c, ST_TIMEOUT, ROLE_MMA);
+      break;
+    }
   }
 }
 
@@ -171,7 +191,7 @@ __device__ __forceinline__ void int8_producer(const KernelParams& p, const Ctx& 
       r.next();
     }
   }
-  if (!ok) int8_land<Cfg::STAGES>(p, bar.full, issued, issued_parity);
+  int8_land<Cfg::STAGES>(p, bar.full, issued, issued_parity);
 }
 
 // NT rows of two 64-element atoms per k-block.
@@ -194,7 +214,7 @@ __device__ __forceinline__ void int8_token_loads(const KernelParams& p, const Ct
       r.next();
     }
   }
-  if (!ok) int8_land<Cfg::XS>(p, bar.x_full, issued, issued_parity);
+  int8_land<Cfg::XS>(p, bar.x_full, issued, issued_parity);
 }
 
 // issuer: of the two that take the k-blocks in turn, each into its own accumulators
@@ -234,13 +254,7 @@ __device__ __forceinline__ void int8_mma(const KernelParams& p, const Ctx& c, Wa
   }
   // every MMA issued completes before TMEM is released
   ptx::mma_commit(bar.drain);
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try_wait(bar.drain, 0)) {
-    if (ptx::globaltimer() - t0 > p.timeout_ns) {
-      raise_error<1>(p, c, ST_TIMEOUT, ROLE_MMA);
-      break;
-    }
-  }
+  int8_drain<1>(p, c, bar.drain);
 }
 
 // set: of WSETS that take the k-blocks in turn.

@@ -78,15 +78,21 @@ __device__ __forceinline__ void int8_wide_weight_loads(const KernelParams& p, co
       r.next();
     }
   }
-  if (!ok) int8_land<Cfg::WS>(p, bar.w_full, issued, parity);
+  int8_land<Cfg::WS>(p, bar.w_full, issued, parity);
 }
 
-// Both CTAs' tokens arrive on the leader's barrier.
+// Both CTAs' tokens arrive on the leader's barrier.  peer_issued: a word of each CTA, 0 at first.
 template <class Cfg>
-__device__ __forceinline__ void int8_wide_token_loads(const KernelParams& p, const Ctx& c, Walk walk, uint32_t smem, const Int8WideBars<Cfg>& bar) {
+__device__ __forceinline__ void int8_wide_token_loads(const KernelParams& p, const Ctx& c, Walk walk, uint32_t smem, const Int8WideBars<Cfg>& bar,
+                                                      volatile uint32_t* peer_issued) {
   RingAt<Cfg::XS> r;
-  uint32_t issued = 0, parity = 0;
+  uint32_t issued = 0, parity = 0, count = 0;
   bool ok = true;
+  auto mark = [&] {
+    issued |= 1u << r.at;
+    parity = (parity & ~(1u << r.at)) | (r.phase << r.at);
+    r.next();
+  };
   Tile w;
   ptx::griddep_wait();   // the FP16 tokens are the kernel's before
   while (ok && walk.next(w)) {
@@ -98,14 +104,28 @@ __device__ __forceinline__ void int8_wide_token_loads(const KernelParams& p, con
       const uint32_t leader = ptx::mapa(full, 0);
       ptx::tma_load_2d_pair(dst, &p.tmap_a, leader, kb * 128, row0);
       ptx::tma_load_2d_pair(dst + Cfg::X_ATOM, &p.tmap_a, leader, kb * 128 + 64, row0);
-      issued |= 1u << r.at;
-      parity = (parity & ~(1u << r.at)) | (r.phase << r.at);
-      r.next();
+      mark();
+      ++count;
     }
   }
-  // the leader's barrier counts both CTAs' copies; the peer's own land before the cluster's last barrier lets it go,
-  // which the leader reaches only after its wait here
-  if (!ok && c.rank == 0) int8_land<Cfg::XS>(p, bar.x_full, issued, parity);
+  // The leader waits for both CTAs' copies; the peer's own land before the cluster's last barrier lets it go, which the
+  // leader reaches only after its wait here.  Where waits ran out the peer may have issued more (at most its ring), onto
+  // phases that the leader has not opened: the peer tells how many, and the leader opens them for the peer's half.
+  if (c.rank != 0) {
+    ptx::st_cluster_u32(ptx::mapa(ptx::smem_addr(const_cast<uint32_t*>(peer_issued)), 0), 2u * count + 1u);
+    return;
+  }
+  const uint64_t t0 = ptx::globaltimer(), limit = int8_end_limit(p);
+  uint32_t told = 0;
+  while ((told = *peer_issued) == 0u)
+    if (ptx::globaltimer() - t0 > limit) break;
+  // the difference of the counts, each modulo 2^31
+  const int32_t more = told != 0u ? static_cast<int32_t>((told - 1u) - 2u * count) / 2 : 0;
+  for (int32_t i = 0; i < more && i < Cfg::XS; ++i) {
+    ptx::mbar_arrive_expect_tx(bar.x_full + 8 * r.at, Cfg::X_BYTES);
+    mark();
+  }
+  int8_land<Cfg::XS>(p, bar.x_full, issued, parity);
 }
 
 template <class Cfg>
@@ -146,13 +166,7 @@ __device__ __forceinline__ void int8_wide_mma(const KernelParams& p, const Ctx& 
   }
   // every MMA issued completes before TMEM is released
   ptx::mma_commit_pair(bar.drain);
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try_wait(bar.drain, 0)) {
-    if (ptx::globaltimer() - t0 > p.timeout_ns) {
-      raise_error<2>(p, c, ST_TIMEOUT, ROLE_MMA);
-      break;
-    }
-  }
+  int8_drain<2>(p, c, bar.drain);
 }
 
 template <class Cfg>
@@ -271,6 +285,7 @@ __global__ void __launch_bounds__(kInt8WideThreads, 1) gemm_int8_wide_kernel(con
     ptx::mbar_init(bar.drain, 1);
     ctl->abort = 0;
     ctl->ep_ok = 0;
+    ctl->pad = 0;   // the peer's k-blocks of tokens, as int8_wide_token_loads tells them
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&p.tmap_a);
     ptx::prefetch_tmap(&p.tmap_b);
@@ -295,7 +310,7 @@ __global__ void __launch_bounds__(kInt8WideThreads, 1) gemm_int8_wide_kernel(con
     } else if (warp == 1) {
       if (c.rank == 0 && ptx::elect_one()) int8_wide_mma<Cfg>(p, c, walk, tmem_base, base + Cfg::X_OFFSET, bar);
     } else if (warp == 2) {
-      if (ptx::elect_one()) int8_wide_token_loads<Cfg>(p, c, walk, base + Cfg::X_OFFSET, bar);
+      if (ptx::elect_one()) int8_wide_token_loads<Cfg>(p, c, walk, base + Cfg::X_OFFSET, bar, &ctl->pad);
     }
     __syncwarp();
   } else if (warp < 8) {
