@@ -90,7 +90,8 @@ struct ScoreMap {
   }
 };
 
-// 1 / (1 + e^-x) to a few units in the last place, for every x
+// 1 / (1 + e^-x), and 1 less that.  With u = 2^-24 their relative errors are (1.5 |x| + 8) u: the exponent's argument is
+// rounded (1.5 |x| u), and ex2, the sum and the quotient add the rest.
 struct Sigmoid {
   float s, rest;   // and 1 - s
   __device__ __forceinline__ explicit Sigmoid(float x) {
@@ -99,7 +100,7 @@ struct Sigmoid {
     rest = x >= 0.0f ? t * d : d;
   }
 };
-// the same without 1 - s, in four operations: 0 for -inf, a NaN for a NaN
+// the same without 1 - s, in four operations, to the same bound (below 2^-126: 0): 0 for -inf, a NaN for a NaN
 __device__ __forceinline__ float fast_sigmoid(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + RowExp::exp2_approx(-x * kLog2e)));
@@ -112,8 +113,8 @@ __device__ __forceinline__ float shifted_sigmoid(float x, float m) {
 constexpr float kLowest = -3.4028235e38f;
 constexpr float kLeastSum = 8.6736174e-19f;   // 2^-60: sums of sigmoids below this are taken again with a shift
 
-// Sums (not maxima) of a group: at least this far apart, two values computed in FP32 are in the order of
-// their FP64 values.  With u = 2^-24: a score is computed with a relative error below 128 u (sigmoid:
+// At least this far apart, two values c computed in FP32 are in the order of their FP64 values.  (Sums of two: in
+// score_rows_kernel.)  s: the larger score, c: the larger magnitude.  With u = 2^-24: a score is computed with a relative error below 128 u (sigmoid:
 // 1.5 |x| u from the exponent's argument, |x| < 80, and 8 u from ex2, the sum and the quotient; softmax:
 // 2.4 |x - top| u and (12 + log2 E) u, and e^x that small is weighed by x), an absolute one below 8 u for
 // a sigmoid (s (1 - s) |x| < 0.23), and the bias adds u |c|; twice that for a pair, below 2^-120 flushed.
@@ -394,8 +395,12 @@ __device__ __forceinline__ void put_choice(const ScoreParams& p, uint32_t* bitma
 
 // A row that the list left open, whose share of the sums is counted already: by the list again, by rounds where more
 // are in reach than it holds, and by choose_exact where a NaN takes part or rounds do not tell.  Loops are not
-// unrolled: one row in hundreds comes here, and its time is that of fetching the code.  `kept`: the lanes whose groups
-// stay, 0 where that is open.
+// unrolled: of ordinary rows one in hundreds comes here, and its time is that of fetching the code.  All rows come where
+//   - top_k is more than the lanes of the groups kept: the bound of their lanes' largest then bounds nothing (65536 x 512, 2
+//     of 16 groups: k 4 131 us, k 6 532, k 10 648);
+//   - sigmoids lie below 2^-18 without biases that hold them apart: gaps are those of scores up to 1 (131071 x 256, 4
+//     of 8 groups: logits around -10 175 us, -12 342, -16 and less 5.4 ms).
+// `kept`: the lanes whose groups stay, 0 where that is open.
 template <typename T, int VPL>
 __device__ __noinline__ void late_row(const ScoreParams& p, const float* bias, uint32_t* bitmap, int words, int64_t t0, int r, bool odd,
                                       uint32_t kept, Ranked* list) {
@@ -514,8 +519,8 @@ __device__ __noinline__ void late_row(const ScoreParams& p, const float* bias, u
 // close, more than the list holds, a NaN, and every row where a bias is a NaN or +inf) are marked, and chosen by
 // late_row once all others are done: so the rows that come through carry no call (with calls between them, whose
 // registers are then spilled around them, 30 us more of 150).  What bounds it is issue slots, as in route_rows_kernel:
-// 131071 x 256 FP32, 4 of 8 groups, k 8, takes 147 us in a graph with the two launches after it, 138 of them here, in
-// 855 instructions a row at 0.74 of the slots; without groups 115.
+// 131071 x 256 FP32, 4 of 8 groups, k 8, takes 147 us with the two launches after it, 138 of them here, in 861
+// instructions a row at 0.74 of the slots; 220 rows are marked.
 template <typename T, int VPL, bool VEC, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS > 8 ? 1 : VPL <= 8 ? 4 : VPL == 16 ? 2 : 1)
     score_rows_kernel(const __grid_constant__ ScoreParams p) {
